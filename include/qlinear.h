@@ -3,8 +3,10 @@
  *
  *   Y[M,N] = s_a[m] * s_w[n] * (A_q[M,K] . W_q[N,K]^T)      bf16 output
  *
- * plus the dynamic activation quantizer that produces (A_q, s_a) and the
- * offline weight quantizer that produces (W_q, s_w).
+ * plus the dynamic activation quantizer that produces (A_q, s_a), the
+ * offline weight quantizer that produces (W_q, s_w), and the operators that
+ * stand around the linears when a model is served (norm and rotation of the
+ * heads, paged cache, attention, draft verification).
  *
  * Sources.  The operation and its variants are described on five web pages
  * about the article "Building a High-Performance and Portable vLLM Linear
@@ -512,6 +514,170 @@ ql_status qlinear_forward_amax(ql_plan plan, const void* x_bf16, void* x_amax, v
 ql_status qlinear_forward_noalloc(ql_plan plan, const void* x_bf16, void* a_q, void* a_scale,
                                   const void* w_q, const void* w_scale, void* y_bf16,
                                   void* stream);
+
+/*
+ * Serving operators around the linears.  Between the QKV and the O projection
+ * of a layer: norm and rotation of the query and key heads, append to a paged
+ * cache, attention over the cache; after the last layer: verification of
+ * drafted tokens.  They keep this header's rules -- host-checked arguments,
+ * enqueue-only calls that can be captured into a graph, no allocation, and
+ * caller-owned memory.
+ *
+ * ql_rows: bf16 [tokens, heads, head_dim] with head_dim contiguous, e.g. the
+ * query columns of the QKV projection's output.  Strides in elements, each a
+ * multiple of 8; data 16-byte aligned.
+ */
+typedef struct {
+  void* data;
+  int64_t token_stride, head_stride;
+} ql_rows;
+
+typedef enum {
+  QL_KV_BF16 = 0,
+  QL_KV_E4M3 = 1 /* value = code * scale[kv_head] */
+} ql_kv_type;
+
+/*
+ * A paged cache: k and v are [num_pages, page_size, kv_heads, head_dim] with
+ * head_dim contiguous and any order of the other three (strides in elements,
+ * multiples of 16 bytes; 16-byte aligned).  page_size is a multiple of 16 up
+ * to 8192; num_pages * page_size < 2^31; 16 token strides < 2^31 bytes.
+ * E4M3 caches may carry one binary32 scale per KV head (device memory,
+ * [kv_heads]; NULL = 1).
+ */
+typedef struct {
+  void* k;
+  void* v;
+  const float* k_scale;
+  const float* v_scale;
+  int64_t k_page_stride, k_token_stride, k_head_stride;
+  int64_t v_page_stride, v_token_stride, v_head_stride;
+  int64_t num_pages;
+  int32_t type; /* ql_kv_type */
+  int32_t page_size, kv_heads, head_dim;
+} ql_kv_cache;
+
+/*
+ * Norm and rotation of a head x of head_dim values:
+ *   n = x * w / sqrt(mean(x^2) + eps)                (w NULL: n = x)
+ *   y_a = n_a cos_i - n_b sin_i, y_b = n_b cos_i + n_a sin_i
+ * over the pairs (a, b) = (i, rot_dim/2 + i) -- interleaved: (2i, 2i + 1) --
+ * of the first rot_dim values; the rest of n is kept.  cos_sin is binary32
+ * [max_pos, rot_dim], a position's rot_dim/2 cosines followed by its sines.
+ * rot_dim is a multiple of 16 up to head_dim, 0 for no rotation (cos_sin may
+ * then be NULL).  Weights are bf16 [head_dim].  All arithmetic in binary32,
+ * rounded once.
+ */
+typedef struct {
+  const void* q_weight;
+  const void* k_weight;
+  const float* cos_sin;
+  int64_t max_pos;
+  int32_t rot_dim, interleaved;
+  float eps;
+} ql_norm_rope;
+
+/*
+ * q_out = norm and rotation of q's heads, k_out of k's, one launch; an output
+ * may be its input.  positions: int64 [tokens], device memory.  A token whose
+ * position lies outside [0, max_pos) gets NaN rows (rot_dim > 0).  head_dim
+ * 64, 128 or 256.  kv_heads may be 0 (queries alone), q_heads may be 0.
+ */
+ql_status qlinear_qk_norm_rope(const ql_norm_rope* rule, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                               int32_t head_dim, const ql_rows* q, const ql_rows* k, const int64_t* positions,
+                               const ql_rows* q_out, const ql_rows* k_out, void* stream);
+
+/*
+ * The same norm and rotation with k and v going into the cache, one launch:
+ * token t's key and value rows are written at slots[t] = page * page_size +
+ * place (int64, device memory), rounded to the cache's type -- E4M3 as the
+ * library's quantizers round: RNE(clamp(fl(y / scale), -448, 448)).  v is
+ * neither normalised nor rotated.  A slot outside the cache (-1 for padding)
+ * writes nothing; two tokens of one call must not share a slot.  q and q_out
+ * may be NULL with q_heads 0.  head_dim 64, 128 or 256.
+ */
+ql_status qlinear_qkv_append(const ql_norm_rope* rule, int64_t tokens, int32_t q_heads, const ql_rows* q,
+                             const ql_rows* k, const ql_rows* v, const int64_t* positions, const int64_t* slots,
+                             const ql_rows* q_out, const ql_kv_cache* cache, void* stream);
+
+/*
+ * Attention of new tokens over the paged cache.  Sequence b has the new tokens
+ * cu_q[b] .. cu_q[b+1] - 1 of q (int32 [batch + 1], cu_q[0] = 0) and seq_lens[b]
+ * cached tokens, the new ones last and already appended; its pages are
+ * page_table[b * table_stride + i] for i < ceil(seq_lens[b] / page_size).
+ * With n new tokens, token t stands at p = seq_lens[b] - n + t and sees
+ * the cached tokens j <= p (causal) with j > p - window (window > 0, causal
+ * only); not causal: all of them.  Query head h reads KV head h / (q_heads /
+ * kv_heads):
+ *   out[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j
+ * A row that sees nothing is 0 with lse -inf.  lse (binary32 [tokens,
+ * q_heads], natural logarithm of the sum of exponentials) may be NULL.  Rows of
+ * q outside [cu_q[0], cu_q[batch]) are not written.  What the cache holds
+ * beyond a sequence's length may be anything, NaN included; page-table entries
+ * beyond its pages are not read.  Memory safety does not depend on the device
+ * arrays: lengths are clamped to max_kv, pages to the cache, cu_q to
+ * [0, tokens].
+ *
+ * The plan fixes the shape and chooses the kernels and the number of chunks
+ * that long contexts are cut into.  max_q, max_kv: upper bounds of a
+ * sequence's new and cached tokens (the page table holds at least
+ * ceil(max_kv / page_size) columns); rows of a sequence beyond max_q are not
+ * computed.  q_heads a multiple of kv_heads; head_dim 64 or 128; scale 0 =
+ * 1 / sqrt(head_dim).  Chunks are joined by a second launch (no atomics:
+ * results do not depend on timing).  The workspace needs no initialisation;
+ * concurrent calls need distinct ones.
+ */
+typedef struct {
+  int64_t batch, tokens, max_q, max_kv;
+  int32_t q_heads, kv_heads, head_dim, page_size;
+  int32_t kv_type; /* ql_kv_type */
+  int32_t causal, window;
+  float scale;
+} ql_attention_shape;
+
+typedef struct {
+  int32_t rows;       /* (token, query head) rows of a workgroup's unit */
+  int32_t row_blocks; /* units of the longest sequence and one KV head */
+  int32_t splits;     /* most chunks a unit's keys are cut into */
+  int32_t chunk;      /* keys of a chunk */
+  int64_t workspace_bytes;
+} ql_attention_facts;
+
+typedef struct ql_attention_plan_s* ql_attention_plan;
+
+ql_status qlinear_attention_plan(const ql_attention_shape* shape, ql_attention_plan* out_plan);
+ql_status qlinear_attention_plan_info(ql_attention_plan plan, ql_attention_facts* facts);
+int64_t qlinear_attention_workspace_bytes(ql_attention_plan plan);
+void qlinear_attention_plan_destroy(ql_attention_plan plan);
+ql_status qlinear_attention(ql_attention_plan plan, const ql_rows* q, const ql_kv_cache* cache,
+                            const int32_t* page_table, int64_t table_stride, const int32_t* seq_lens,
+                            const int32_t* cu_q, const ql_rows* out, float* lse, void* workspace, void* stream);
+
+/*
+ * Verification of drafted tokens.  Sequence b has the drafts cu_drafts[b] ..
+ * cu_drafts[b+1] - 1 (int32 [batch + 1], cu_drafts[0] = 0; at most max_drafts
+ * of them) of draft_tokens, of the draft's probabilities draft_probs [n_drafts,
+ * vocab] and of the uniforms [0, 1), and one row more of the target's
+ * probabilities target_probs [n_drafts + batch, vocab] (rows cu_drafts[b] + b
+ * onwards): the target's distribution at each draft's place and after the
+ * last.  Drafts are accepted while u_i q_i(x_i) < p_i(x_i); the next token is
+ * argmax_v max(p_v - q_v, 0) / noise[b, v] at the first rejected place (p_v /
+ * noise where that is nowhere positive), argmax_v p_v / noise[b, v] after the
+ * last draft, ties to the lowest index.  With noise drawn from the
+ * exponential distribution the tokens follow the target's distribution.
+ * draft_probs NULL: the drafts were certain (q = 1 at x_i, 0 elsewhere).
+ * Probabilities, uniforms and noise (positive) are binary32; a NaN
+ * probability counts as 0; a drafted token outside the vocabulary is rejected.
+ *   out_tokens int32 [batch, max_drafts + 1]: the accepted drafts, the next
+ *   token, then -1;  accepted int32 [batch]: the number of accepted drafts.
+ * The workspace (qlinear_verify_workspace_bytes, 16-byte aligned) needs no
+ * initialisation.
+ */
+int64_t qlinear_verify_workspace_bytes(int64_t batch, int64_t vocab);
+ql_status qlinear_verify_draft(int64_t batch, int64_t n_drafts, int64_t max_drafts, int64_t vocab,
+                               const float* target_probs, const float* draft_probs, const int32_t* draft_tokens,
+                               const int32_t* cu_drafts, const float* uniforms, const float* noise,
+                               int32_t* out_tokens, int32_t* accepted, void* workspace, void* stream);
 
 /*
  * hipGraph dispatch for the small-M path ([Summary] "Hybrid dispatch

@@ -572,3 +572,10 @@ def load_default_table():
     if os.path.exists(DEFAULT_TABLE):
         return qlinear_table_load(DEFAULT_TABLE)
     return 0
+
+
+# ----------------------------------------------------------------- serving operators around the linears
+
+from .serving import (KV_BF16, KV_E4M3, AttentionPlan, PagedCache, qlinear_attention,  # noqa: E402
+                      qlinear_attention_plan, qlinear_qk_norm_rope, qlinear_qkv_append, qlinear_verify_draft,
+                      qlinear_verify_workspace_bytes, rope_table, verify_workspace)

@@ -19,6 +19,34 @@ class QLPlanFacts(ctypes.Structure):
                 ("threads", c_i32), ("lds_bytes", c_i32), ("workspace_bytes", c_i64), ("epilogue", c_i32)]
 
 
+class QLRows(ctypes.Structure):
+    _fields_ = [("data", c_vp), ("token_stride", c_i64), ("head_stride", c_i64)]
+
+
+class QLKvCache(ctypes.Structure):
+    _fields_ = ([(n, c_vp) for n in ("k", "v", "k_scale", "v_scale")]
+                + [(n, c_i64) for n in ("k_page_stride", "k_token_stride", "k_head_stride", "v_page_stride",
+                                        "v_token_stride", "v_head_stride", "num_pages")]
+                + [(n, c_i32) for n in ("type", "page_size", "kv_heads", "head_dim")])
+
+
+class QLNormRope(ctypes.Structure):
+    _fields_ = [("q_weight", c_vp), ("k_weight", c_vp), ("cos_sin", c_vp), ("max_pos", c_i64), ("rot_dim", c_i32),
+                ("interleaved", c_i32), ("eps", ctypes.c_float)]
+
+
+class QLAttentionShape(ctypes.Structure):
+    _fields_ = ([(n, c_i64) for n in ("batch", "tokens", "max_q", "max_kv")]
+                + [(n, c_i32) for n in ("q_heads", "kv_heads", "head_dim", "page_size", "kv_type", "causal", "window")]
+                + [("scale", ctypes.c_float)])
+
+
+class QLAttentionFacts(ctypes.Structure):
+    _fields_ = [(n, c_i32) for n in ("rows", "row_blocks", "splits", "chunk")] + [("workspace_bytes", c_i64)]
+
+
+c_rows, c_cache = ctypes.POINTER(QLRows), ctypes.POINTER(QLKvCache)
+
 # name -> (restype, argtypes); exactly the functions declared in include/qlinear.h
 SIGNATURES = {
     "qlinear_version": (c_i32, []),
@@ -57,6 +85,17 @@ SIGNATURES = {
     "qlinear_forward_noalloc": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "qlinear_forward_glu_amax": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
     "qlinear_forward_amax": (c_i32, [c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp, c_vp]),
+    "qlinear_qk_norm_rope": (c_i32, [ctypes.POINTER(QLNormRope), c_i64, c_i32, c_i32, c_i32, c_rows, c_rows, c_vp, c_rows,
+                                     c_rows, c_vp]),
+    "qlinear_qkv_append": (c_i32, [ctypes.POINTER(QLNormRope), c_i64, c_i32, c_rows, c_rows, c_rows, c_vp, c_vp, c_rows,
+                                   c_cache, c_vp]),
+    "qlinear_attention_plan": (c_i32, [ctypes.POINTER(QLAttentionShape), ctypes.POINTER(c_vp)]),
+    "qlinear_attention_plan_info": (c_i32, [c_vp, ctypes.POINTER(QLAttentionFacts)]),
+    "qlinear_attention_workspace_bytes": (c_i64, [c_vp]),
+    "qlinear_attention_plan_destroy": (None, [c_vp]),
+    "qlinear_attention": (c_i32, [c_vp, c_rows, c_cache, c_vp, c_i64, c_vp, c_vp, c_rows, c_vp, c_vp, c_vp]),
+    "qlinear_verify_workspace_bytes": (c_i64, [c_i64, c_i64]),
+    "qlinear_verify_draft": (c_i32, [c_i64] * 4 + [c_vp] * 10),
     "qlinear_graph_begin": (c_i32, [c_vp]),
     "qlinear_graph_end": (c_i32, [c_vp, ctypes.POINTER(c_vp)]),
     "qlinear_graph_launch": (c_i32, [c_vp, c_vp]),

@@ -24,11 +24,12 @@
 #include <string>
 #include <vector>
 
+#include "api_common.hpp"
 #include "decode_args.hpp"
 
-namespace {
+namespace qlapi {
 
-thread_local std::string g_err;
+static thread_local std::string g_err;
 
 ql_status fail(ql_status st, const char* fmt, ...) {
   char buf[512];
@@ -44,6 +45,14 @@ ql_status hip_fail(hipError_t e, const char* what) {
   return fail(QL_E_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
+}  // namespace qlapi
+
+namespace {
+
+using qlapi::aligned16;
+using qlapi::fail;
+using qlapi::hip_fail;
+
 // gfx950: LDS per workgroup (above 64 KB with the per-kernel opt-in), less
 // room for the kernels' own static LDS variables
 constexpr int64_t kLdsLimit = 160 * 1024 - 256;
@@ -53,7 +62,6 @@ constexpr int kBuckets[] = {1, 2, 4, 8, 16, 24, 32};
 
 bool valid_fmt(int32_t f) { return f >= QL_FP8_DYNAMIC && f <= QL_MXFP4; }
 bool is_mx(int32_t f) { return f == QL_MXFP8 || f == QL_MXFP4; }
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 bool is_pow2(int64_t v) { return v > 0 && (v & (v - 1)) == 0; }
 int kernel_fmt(int32_t f) {
   return f == QL_W8A8_INT8 ? qlk::FMT_INT8 : f == QL_BLOCK_FP8 ? qlk::FMT_BLOCK : f == QL_MXFP8 ? qlk::FMT_MX
@@ -719,7 +727,7 @@ const char* qlinear_status_string(int32_t s) {
   }
 }
 
-const char* qlinear_last_error(void) { return g_err.c_str(); }
+const char* qlinear_last_error(void) { return qlapi::g_err.c_str(); }
 
 ql_status qlinear_quantize_act(int32_t fmt, const void* x_bf16, int64_t M, int64_t K, void* a_q,
                                void* a_scale, void* stream) {

@@ -1,0 +1,321 @@
+// C ABI of the serving operators around the linears: argument checks, the
+// attention planner, launches.
+#include "../../include/qlinear.h"
+
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <new>
+
+#include "api_common.hpp"
+#include "attention_args.hpp"
+
+using qlapi::aligned;
+using qlapi::aligned16;
+using qlapi::fail;
+using qlapi::hip_fail;
+
+struct ql_attention_plan_s {
+  ql_attention_shape shape;
+  ql_attention_facts facts;
+  int64_t part_ml_at;  // bytes of the partial outputs, before their maxima and sums
+  int units;
+};
+
+namespace {
+
+constexpr int64_t kMaxTokens = int64_t(1) << 24;
+constexpr int64_t kMaxStride = int64_t(1) << 40;  // elements
+
+ql_status check_rows(const ql_rows* r, const char* name, qlk::Rows* out) {
+  if (!r || !r->data) return fail(QL_E_INVALID, "%s is NULL", name);
+  if (!aligned16(r->data)) return fail(QL_E_ALIGN, "%s is not 16-byte aligned", name);
+  if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride > kMaxStride || r->head_stride > kMaxStride)
+    return fail(QL_E_INVALID, "%s strides must be in [0, 2^40]", name);
+  if (r->token_stride % 8 || r->head_stride % 8)
+    return fail(QL_E_ALIGN, "%s strides must be multiples of 8 elements", name);
+  *out = qlk::Rows{static_cast<uint8_t*>(r->data), r->token_stride * 2, r->head_stride * 2};
+  return QL_OK;
+}
+
+ql_status check_pages(void* p, const float* scale, int64_t page, int64_t token, int64_t head, int size,
+                      const char* name, qlk::Pages* out) {
+  if (!p) return fail(QL_E_INVALID, "cache %s is NULL", name);
+  if (!aligned16(p)) return fail(QL_E_ALIGN, "cache %s is not 16-byte aligned", name);
+  if (!aligned(scale, 4)) return fail(QL_E_ALIGN, "cache %s_scale is not 4-byte aligned", name);
+  if (page < 0 || token < 0 || head < 0 || page > kMaxStride || token > kMaxStride || head > kMaxStride)
+    return fail(QL_E_INVALID, "cache %s strides must be in [0, 2^40]", name);
+  if (page * size % 16 || token * size % 16 || head * size % 16)
+    return fail(QL_E_ALIGN, "cache %s strides must be multiples of 16 bytes", name);
+  if (token * size * 16 >= (int64_t(1) << 31))
+    return fail(QL_E_UNSUPPORTED, "cache %s token stride beyond 2^27 bytes", name);
+  *out = qlk::Pages{static_cast<uint8_t*>(p), page * size, token * size, head * size, scale};
+  return QL_OK;
+}
+
+ql_status check_page_size(int32_t page_size) {
+  if (page_size < 16 || page_size % 16 || page_size > 8192)
+    return fail(QL_E_UNSUPPORTED, "page_size %d must be a multiple of 16 in [16, 8192]", page_size);
+  return QL_OK;
+}
+
+uint64_t page_magic(int32_t page_size) {
+  const uint64_t groups = (uint64_t)page_size / 16;
+  return ((uint64_t(1) << qlk::kPageMagicShift) + groups - 1) / groups;
+}
+
+ql_status check_cache(const ql_kv_cache* c, qlk::Pages* k, qlk::Pages* v) {
+  if (!c) return fail(QL_E_INVALID, "cache is NULL");
+  if (c->type != QL_KV_BF16 && c->type != QL_KV_E4M3) return fail(QL_E_INVALID, "unknown cache type %d", c->type);
+  if (c->kv_heads < 1 || c->num_pages < 1)
+    return fail(QL_E_INVALID, "the cache needs at least one page and one head");
+  ql_status st = check_page_size(c->page_size);
+  if (st != QL_OK) return st;
+  if (c->num_pages > (int64_t(1) << 31) / c->page_size || c->num_pages * c->page_size >= (int64_t(1) << 31))
+    return fail(QL_E_UNSUPPORTED, "the cache holds 2^31 tokens or more");
+  const int size = c->type == QL_KV_E4M3 ? 1 : 2;
+  if (c->type == QL_KV_BF16 && (c->k_scale || c->v_scale))
+    return fail(QL_E_INVALID, "a bf16 cache has no scales");
+  st = check_pages(c->k, c->k_scale, c->k_page_stride, c->k_token_stride, c->k_head_stride, size, "k", k);
+  if (st != QL_OK) return st;
+  return check_pages(c->v, c->v_scale, c->v_page_stride, c->v_token_stride, c->v_head_stride, size, "v", v);
+}
+
+bool norm_dim(int32_t d) { return d == 64 || d == 128 || d == 256; }
+
+ql_status check_rule(const ql_norm_rope* r, int64_t tokens, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                     const int64_t* positions, qlk::HeadArgs* a) {
+  if (!r) return fail(QL_E_INVALID, "rule is NULL");
+  if (tokens < 0 || q_heads < 0 || kv_heads < 0) return fail(QL_E_INVALID, "negative size");
+  if (tokens > kMaxTokens || q_heads > 65536 || kv_heads > 65536)
+    return fail(QL_E_UNSUPPORTED, "more than 2^24 tokens or 2^16 heads");
+  if (!norm_dim(head_dim)) return fail(QL_E_UNSUPPORTED, "head_dim %d must be 64, 128 or 256", head_dim);
+  if (r->rot_dim < 0 || r->rot_dim > head_dim || r->rot_dim % 16)
+    return fail(QL_E_INVALID, "rot_dim %d must be a multiple of 16 in [0, head_dim]", r->rot_dim);
+  if (r->interleaved != 0 && r->interleaved != 1) return fail(QL_E_INVALID, "interleaved must be 0 or 1");
+  if (!(r->eps >= 0.0f)) return fail(QL_E_INVALID, "eps must be >= 0");
+  if (r->max_pos < 0 || r->max_pos > (int64_t(1) << 40)) return fail(QL_E_INVALID, "max_pos outside [0, 2^40]");
+  if (!aligned16(r->q_weight) || !aligned16(r->k_weight))
+    return fail(QL_E_ALIGN, "norm weights must be 16-byte aligned");
+  if (tokens > 0 && (q_heads > 0 || kv_heads > 0)) {
+    if (r->rot_dim > 0 && !r->cos_sin) return fail(QL_E_INVALID, "cos_sin is NULL");
+    if (!positions) return fail(QL_E_INVALID, "positions is NULL");
+  }
+  if (!aligned(r->cos_sin, 4) || !aligned(positions, 8)) return fail(QL_E_ALIGN, "cos_sin or positions misaligned");
+  a->q_w = static_cast<const uint16_t*>(r->q_weight);
+  a->k_w = static_cast<const uint16_t*>(r->k_weight);
+  a->table = r->cos_sin;
+  a->pos = positions;
+  a->max_pos = r->max_pos;
+  a->eps = r->eps;
+  a->tokens = (int)tokens;
+  a->q_heads = q_heads;
+  a->kv_heads = kv_heads;
+  a->rot = r->rot_dim;
+  a->interleaved = r->interleaved;
+  return QL_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+ql_status qlinear_qk_norm_rope(const ql_norm_rope* rule, int64_t tokens, int32_t q_heads, int32_t kv_heads,
+                               int32_t head_dim, const ql_rows* q, const ql_rows* k, const int64_t* positions,
+                               const ql_rows* q_out, const ql_rows* k_out, void* stream) {
+  qlk::HeadArgs a{};
+  ql_status st = check_rule(rule, tokens, q_heads, kv_heads, head_dim, positions, &a);
+  if (st != QL_OK) return st;
+  if (tokens == 0 || q_heads + kv_heads == 0) return QL_OK;
+  if (q_heads && ((st = check_rows(q, "q", &a.q)) != QL_OK || (st = check_rows(q_out, "q_out", &a.q_out)) != QL_OK))
+    return st;
+  if (kv_heads && ((st = check_rows(k, "k", &a.k)) != QL_OK || (st = check_rows(k_out, "k_out", &a.k_out)) != QL_OK))
+    return st;
+  hipError_t e = qlk::launch_heads(a, head_dim, false, false, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QL_OK : hip_fail(e, "norm and rotation launch");
+}
+
+ql_status qlinear_qkv_append(const ql_norm_rope* rule, int64_t tokens, int32_t q_heads, const ql_rows* q,
+                             const ql_rows* k, const ql_rows* v, const int64_t* positions, const int64_t* slots,
+                             const ql_rows* q_out, const ql_kv_cache* cache, void* stream) {
+  qlk::HeadArgs a{};
+  ql_status st = check_cache(cache, &a.kc, &a.vc);
+  if (st != QL_OK) return st;
+  st = check_rule(rule, tokens, q_heads, cache->kv_heads, cache->head_dim, positions, &a);
+  if (st != QL_OK) return st;
+  if (tokens == 0) return QL_OK;
+  if (q_heads && ((st = check_rows(q, "q", &a.q)) != QL_OK || (st = check_rows(q_out, "q_out", &a.q_out)) != QL_OK))
+    return st;
+  if ((st = check_rows(k, "k", &a.k)) != QL_OK || (st = check_rows(v, "v", &a.v)) != QL_OK) return st;
+  if (!slots) return fail(QL_E_INVALID, "slots is NULL");
+  if (!aligned(slots, 8)) return fail(QL_E_ALIGN, "slots is not 8-byte aligned");
+  a.slots = slots;
+  a.num_slots = cache->num_pages * cache->page_size;
+  a.page_size = cache->page_size;
+  a.page_magic = page_magic(cache->page_size);
+  hipError_t e = qlk::launch_heads(a, cache->head_dim, true, cache->type == QL_KV_E4M3, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QL_OK : hip_fail(e, "cache append launch");
+}
+
+ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan* out) {
+  if (!out) return fail(QL_E_INVALID, "out_plan is NULL");
+  *out = nullptr;
+  if (!s) return fail(QL_E_INVALID, "shape is NULL");
+  if (s->batch < 0 || s->tokens < 0 || s->max_q < 0 || s->max_kv < 0) return fail(QL_E_INVALID, "negative size");
+  if (s->tokens > kMaxTokens || s->max_q > kMaxTokens || s->batch > 65536 || s->max_kv > (int64_t(1) << 30))
+    return fail(QL_E_UNSUPPORTED, "more than 2^24 new tokens, 2^16 sequences or 2^30 cached tokens");
+  if (s->kv_heads < 1 || s->q_heads < 1 || s->q_heads % s->kv_heads)
+    return fail(QL_E_INVALID, "q_heads %d must be a positive multiple of kv_heads %d", s->q_heads, s->kv_heads);
+  if (s->q_heads > 65536) return fail(QL_E_UNSUPPORTED, "more than 2^16 heads");
+  if (s->head_dim != 64 && s->head_dim != 128) return fail(QL_E_UNSUPPORTED, "head_dim %d must be 64 or 128", s->head_dim);
+  if (s->kv_type != QL_KV_BF16 && s->kv_type != QL_KV_E4M3) return fail(QL_E_INVALID, "unknown cache type %d", s->kv_type);
+  ql_status st = check_page_size(s->page_size);
+  if (st != QL_OK) return st;
+  if (s->causal != 0 && s->causal != 1) return fail(QL_E_INVALID, "causal must be 0 or 1");
+  if (s->window < 0 || (s->window && !s->causal)) return fail(QL_E_INVALID, "a window is >= 0 and causal");
+  if (!std::isfinite(s->scale)) return fail(QL_E_INVALID, "scale must be finite");
+  const int64_t group = s->q_heads / s->kv_heads;
+  const int64_t rows = s->max_q * group;
+  if (rows > (int64_t(1) << 30)) return fail(QL_E_UNSUPPORTED, "max_q * q_heads / kv_heads exceeds 2^30");
+  ql_attention_facts f{};
+  f.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+  const int64_t blocks = (rows + f.rows - 1) / f.rows;
+  const int64_t units = s->batch * blocks * s->kv_heads;
+  // the keys a block of rows can see, from the 64-aligned start of its window
+  const int64_t block_tokens = f.rows / group + 2;
+  const int64_t span = s->window ? std::min<int64_t>(s->max_kv, (int64_t)s->window + block_tokens + 64) : s->max_kv;
+  // chunks: enough workgroups to fill the card a few times over
+  int64_t chunk = 256;
+  while (units * ((span + chunk - 1) / chunk) > 2048 && chunk < span) chunk *= 2;
+  const int64_t splits = std::max<int64_t>(1, (span + chunk - 1) / chunk);
+  if (units * splits * f.rows / 4 >= (int64_t(1) << 31)) return fail(QL_E_UNSUPPORTED, "more than 2^31 workgroups");
+  f.row_blocks = (int32_t)blocks;
+  f.splits = (int32_t)splits;
+  f.chunk = (int32_t)chunk;
+  const int64_t parts = splits > 1 ? units * splits * f.rows : 0;
+  f.workspace_bytes = parts * (s->head_dim + 2) * 4;
+  ql_attention_plan_s* p = new (std::nothrow) ql_attention_plan_s();
+  if (!p) return fail(QL_E_INVALID, "out of host memory");
+  p->shape = *s;
+  p->facts = f;
+  p->part_ml_at = parts * s->head_dim * 4;
+  p->units = (int)units;
+  *out = p;
+  return QL_OK;
+}
+
+ql_status qlinear_attention_plan_info(ql_attention_plan p, ql_attention_facts* facts) {
+  if (!p || !facts) return fail(QL_E_INVALID, "NULL argument");
+  *facts = p->facts;
+  return QL_OK;
+}
+
+int64_t qlinear_attention_workspace_bytes(ql_attention_plan p) { return p ? p->facts.workspace_bytes : 0; }
+
+void qlinear_attention_plan_destroy(ql_attention_plan p) { delete p; }
+
+ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_cache* cache,
+                            const int32_t* page_table, int64_t table_stride, const int32_t* seq_lens,
+                            const int32_t* cu_q, const ql_rows* out, float* lse, void* workspace, void* stream) {
+  if (!p) return fail(QL_E_INVALID, "plan is NULL");
+  const ql_attention_shape& s = p->shape;
+  const ql_attention_facts& f = p->facts;
+  qlk::AttnArgs a{};
+  ql_status st = check_cache(cache, &a.kc, &a.vc);
+  if (st != QL_OK) return st;
+  if (cache->type != s.kv_type || cache->kv_heads != s.kv_heads || cache->head_dim != s.head_dim ||
+      cache->page_size != s.page_size)
+    return fail(QL_E_INVALID, "the cache is not of the plan's type, heads, head_dim and page_size");
+  if (s.batch == 0 || s.tokens == 0 || s.max_q == 0) return QL_OK;
+  if ((st = check_rows(q, "q", &a.q)) != QL_OK || (st = check_rows(out, "out", &a.out)) != QL_OK) return st;
+  if (!page_table || !seq_lens || !cu_q) return fail(QL_E_INVALID, "page_table, seq_lens or cu_q is NULL");
+  if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(lse, 4))
+    return fail(QL_E_ALIGN, "page_table, seq_lens, cu_q and lse must be 4-byte aligned");
+  if (s.batch > 1 && table_stride < (s.max_kv + s.page_size - 1) / s.page_size)
+    return fail(QL_E_INVALID, "page_table rows hold fewer than ceil(max_kv / page_size) entries");
+  if (f.workspace_bytes > 0 && !workspace) return fail(QL_E_INVALID, "this plan needs a workspace");
+  if (!aligned16(workspace)) return fail(QL_E_ALIGN, "workspace is not 16-byte aligned");
+  a.table = page_table;
+  a.table_row = table_stride;
+  a.seq_lens = seq_lens;
+  a.cu_q = cu_q;
+  a.lse = lse;
+  a.part_o = static_cast<float*>(workspace);
+  a.part_ml = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p->part_ml_at) : nullptr;
+  a.page_magic = page_magic(s.page_size);
+  const float scale = s.scale != 0.0f ? s.scale : 1.0f / std::sqrt((float)s.head_dim);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.tokens = (int)s.tokens;
+  a.q_heads = s.q_heads;
+  a.kv_heads = s.kv_heads;
+  a.group = s.q_heads / s.kv_heads;
+  a.page_size = s.page_size;
+  a.num_pages = (int)cache->num_pages;
+  a.max_kv = (int)s.max_kv;
+  a.causal = s.causal;
+  a.window = s.window;
+  a.row_blocks = f.row_blocks;
+  a.splits = f.splits;
+  a.chunk = f.chunk;
+  a.min_rows = 0;
+  a.max_rows = INT32_MAX;
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  hipError_t e = qlk::launch_attn_stream(a, s.head_dim, s.kv_type == QL_KV_E4M3, f.rows, p->units, hs);
+  if (e != hipSuccess) return hip_fail(e, "attention launch");
+  if (f.splits > 1) {
+    e = qlk::launch_attn_join(a, s.head_dim, f.rows, (int)s.batch, hs);
+    if (e != hipSuccess) return hip_fail(e, "attention join launch");
+  }
+  return QL_OK;
+}
+
+// Slices of a vocabulary row: enough workgroups for the card with few
+// sequences, at least 1024 entries (4 a thread) each.
+static int verify_slices(int64_t batch, int64_t vocab) {
+  const int64_t most = std::max<int64_t>(1, vocab / 1024);
+  return (int)std::max<int64_t>(1, std::min<int64_t>(most, 1024 / std::max<int64_t>(1, batch)));
+}
+
+int64_t qlinear_verify_workspace_bytes(int64_t batch, int64_t vocab) {
+  if (batch <= 0 || vocab <= 0) return 0;
+  return batch * verify_slices(batch, vocab) * 16;
+}
+
+ql_status qlinear_verify_draft(int64_t batch, int64_t n_drafts, int64_t max_drafts, int64_t vocab,
+                               const float* target_probs, const float* draft_probs, const int32_t* draft_tokens,
+                               const int32_t* cu_drafts, const float* uniforms, const float* noise,
+                               int32_t* out_tokens, int32_t* accepted, void* workspace, void* stream) {
+  if (batch < 0 || n_drafts < 0 || max_drafts < 0 || vocab < 0) return fail(QL_E_INVALID, "negative size");
+  if (batch > 65535 || n_drafts > kMaxTokens || max_drafts > 65536 || vocab > (int64_t(1) << 30))
+    return fail(QL_E_UNSUPPORTED, "more than 65535 sequences, 2^24 drafts or 2^30 tokens of vocabulary");
+  if (batch == 0) return QL_OK;
+  if (vocab == 0) return fail(QL_E_INVALID, "the vocabulary is empty");
+  if (!target_probs || !cu_drafts || !noise || !out_tokens || !accepted || !workspace)
+    return fail(QL_E_INVALID, "NULL pointer");
+  if (n_drafts > 0 && (!draft_tokens || !uniforms)) return fail(QL_E_INVALID, "draft_tokens or uniforms is NULL");
+  for (const void* p : {(const void*)target_probs, (const void*)draft_probs, (const void*)draft_tokens,
+                        (const void*)cu_drafts, (const void*)uniforms, (const void*)noise, (const void*)out_tokens,
+                        (const void*)accepted})
+    if (!aligned(p, 4)) return fail(QL_E_ALIGN, "pointers must be 4-byte aligned");
+  if (!aligned16(workspace)) return fail(QL_E_ALIGN, "workspace is not 16-byte aligned");
+  qlk::VerifyArgs a{};
+  a.target = target_probs;
+  a.draft = draft_probs;
+  a.tokens = draft_tokens;
+  a.cu = cu_drafts;
+  a.uniforms = uniforms;
+  a.noise = noise;
+  a.out_tokens = out_tokens;
+  a.accepted = accepted;
+  a.part = static_cast<uint64_t*>(workspace);
+  a.n_drafts = n_drafts;
+  a.batch = (int)batch;
+  a.vocab = (int)vocab;
+  a.max_drafts = (int)max_drafts;
+  a.slices = verify_slices(batch, vocab);
+  hipError_t e = qlk::launch_verify(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? QL_OK : hip_fail(e, "draft verification launch");
+}
+
+}  // extern "C"

@@ -1,0 +1,108 @@
+// What the attention kernels share: the rows of a unit, the range of keys
+// they see, page look-up, and the conversion of cache codes to matrix-core
+// operands.
+//
+// One unit is a sequence b, a KV head h and a block of R rows; row r of the
+// sequence's n * group rows is new token r / group, query head h * group + r
+// % group, so the rows of a block share the keys and values they read.  The
+// new token t of n stands at position p = len - n + t and sees the keys
+// j <= p (causal) with j > p - window (window > 0).
+#pragma once
+
+#include "attention_args.hpp"
+#include "device_common.hpp"
+
+namespace qlk {
+
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+
+constexpr float kNegInf = -__builtin_huge_valf();
+
+__device__ __forceinline__ f32x4 mma_bf16(u32x4 a, u32x4 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// Two binary32 values as a pair of bf16, round to nearest even.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  bf16x2 p = {(__bf16)a, (__bf16)b};
+  return __builtin_bit_cast(uint32_t, p);
+}
+
+// Two E4M3 codes (the low or high half of w) as a pair of bf16: exact.
+template <bool HI>
+__device__ __forceinline__ uint32_t e4m3_to_bf16(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+}
+
+// Maximum and sum over lanes l, l^16, l^32, l^48: the four lanes that hold
+// one row's keys.
+__device__ __forceinline__ float row4_max(float v) {
+  v = fmaxf(v, __shfl_xor(v, 16, 64));
+  return fmaxf(v, __shfl_xor(v, 32, 64));
+}
+__device__ __forceinline__ float row4_sum(float v) {
+  v += __shfl_xor(v, 16, 64);
+  return v + __shfl_xor(v, 32, 64);
+}
+
+// A table or length entry at a wave-uniform address.
+__device__ __forceinline__ int uniform_i32(const int32_t* p) { return __builtin_amdgcn_readfirstlane(*p); }
+
+// The rows and keys of one unit; every field is wave-uniform.
+struct Unit {
+  int first;     // the sequence's first token in q
+  int rows;      // rows of this block
+  int row0;      // first row of the block
+  int pos0;      // position of the sequence's first new token
+  int len;       // cached length (keys beyond it are never read)
+  int lo, hi;    // keys any row of the block sees: [lo, hi)
+  int chunks;    // chunks of keys, from lo rounded down to 64
+  int all;       // rows of the sequence
+};
+
+__device__ __forceinline__ Unit unit_of(const AttnArgs& a, int b, int block, int R) {
+  Unit u;
+  int q0 = uniform_i32(a.cu_q + b), q1 = uniform_i32(a.cu_q + b + 1);
+  q0 = min(max(q0, 0), a.tokens);
+  q1 = min(max(q1, q0), a.tokens);
+  u.len = min(max(uniform_i32(a.seq_lens + b), 0), a.max_kv);
+  u.first = q0;
+  u.all = (q1 - q0) * a.group;
+  u.row0 = block * R;
+  u.rows = min(max(u.all - u.row0, 0), R);
+  u.pos0 = u.len - (q1 - q0);
+  u.hi = u.len;
+  u.lo = 0;
+  if (u.rows > 0) {
+    const int t0 = u.row0 / a.group, t1 = (u.row0 + u.rows - 1) / a.group;
+    if (a.causal) u.hi = min(u.len, max(0, u.pos0 + t1 + 1));
+    if (a.window) u.lo = min(u.hi, max(0, u.pos0 + t0 - a.window + 1));
+  } else {
+    u.hi = 0;
+  }
+  const int lo64 = u.lo & ~63;
+  u.chunks = u.hi > u.lo ? (u.hi - lo64 + a.chunk - 1) / a.chunk : 0;
+  return u;
+}
+
+// Keys [lo, hi) that row r of the block sees.
+__device__ __forceinline__ void row_range(const AttnArgs& a, const Unit& u, int r, int* lo, int* hi) {
+  const int p = u.pos0 + (u.row0 + r) / a.group;
+  *hi = a.causal ? min(u.len, max(0, p + 1)) : u.len;
+  *lo = a.window ? max(0, p - a.window + 1) : 0;
+}
+
+// Page of the 16-key group that starts at key `key`, and the key's place in
+// it.  Columns past the sequence's last page are never read, and a page
+// number out of range is taken into range (a wrong answer for a broken
+// table, never a read outside the cache).
+__device__ __forceinline__ int64_t page_at(const AttnArgs& a, const int32_t* row, int key, int last_sub, int* at) {
+  const int sub = min(key >> 4, last_sub);
+  const int col = page_of(sub, a.page_magic);
+  *at = sub * 16 - col * a.page_size;
+  const uint32_t page = (uint32_t)uniform_i32(row + col);
+  return (int64_t)min(page, (uint32_t)(a.num_pages - 1));
+}
+
+}  // namespace qlk
