@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqlinear.so")
 
-SOURCES = ["quant.hip", "heads.hip", "attention_stream.hip", "verify.hip", "attention_api.cpp", "decode_fp8.hip", "decode_int8.hip", "decode_block.hip", "decode_mx.hip", "decode_mx4.hip", "tiled_fp8.hip",
+SOURCES = ["quant.hip", "heads.hip", "attention_stream.hip", "attention_tile.hip", "verify.hip", "attention_api.cpp", "decode_fp8.hip", "decode_int8.hip", "decode_block.hip", "decode_mx.hip", "decode_mx4.hip", "tiled_fp8.hip",
            "tiled_int8.hip", "tiled_block.hip", "tiled_mx.hip", "tiled_mx4.hip", "stream_read.hip", "api.cpp"]
 
 HIPCC_FLAGS = [

@@ -16,11 +16,21 @@ using qlapi::aligned16;
 using qlapi::fail;
 using qlapi::hip_fail;
 
+namespace {
+
+// One kernel's share of a plan.
+struct Part {
+  bool used;
+  int rows, row_blocks, splits, chunk, units;
+  int64_t o_at, ml_at, end;  // partial outputs, their maxima and sums, in the workspace (bytes)
+};
+
+}  // namespace
+
 struct ql_attention_plan_s {
   ql_attention_shape shape;
-  ql_attention_facts facts;
-  int64_t part_ml_at;  // bytes of the partial outputs, before their maxima and sums
-  int units;
+  Part stream, tile;
+  int tile_from;  // rows of a sequence from which it goes to the tile kernel
 };
 
 namespace {
@@ -117,6 +127,62 @@ ql_status check_rule(const ql_norm_rope* r, int64_t tokens, int32_t q_heads, int
   return QL_OK;
 }
 
+// Rows (new tokens x query heads of a KV head) of a sequence up to which the
+// stream kernel serves it; in a batch that has longer ones too, up to which
+// sequences get a stream launch of their own.
+constexpr int64_t kStreamRows = 64;
+constexpr int64_t kMixedRows = 16;
+
+constexpr int kTileRows = 128;
+
+// Chunk of the stream kernel: it is bound by memory, so any cut costs the same
+// as long as the card is full and the partial results stay small beside the
+// keys: the shortest power of two from 256 keys with at most 2048 workgroups.
+int64_t stream_chunk(int64_t units, int64_t span) {
+  int64_t chunk = 256;
+  while (units * ((span + chunk - 1) / chunk) > 2048 && chunk < span) chunk *= 2;
+  return chunk;
+}
+
+// Chunk of the tile kernel, bound by arithmetic: a workgroup runs at its own
+// pace, 512 of them at a time (two a compute unit).  Measured for head_dim 128:
+// 23 ns a key while every workgroup has a compute unit to itself, 37 ns when two
+// share one, 4 us around that, and for a cut the join's launch (6 us) and
+// its traffic (0.06 us a workgroup's partial result).  Takes the number of
+// chunks that this makes cheapest.
+int64_t tile_chunk(int64_t units, int64_t span) {
+  int64_t best = span;
+  double least = 0;
+  for (int64_t s = 1; s == 1 || (s <= 64 && span / s >= 256); ++s) {
+    const int64_t chunk = ((span + s - 1) / s + 63) / 64 * 64, groups = units * s;
+    const double rounds = groups <= 512 ? 1.0 : groups <= 4096 ? (double)((groups + 511) / 512) : groups / 512.0;
+    const double us = rounds * (4.0 + chunk * (groups <= 256 ? 0.023 : 0.037)) + (s > 1 ? 6.0 + groups * 0.03 : 0.0);
+    if (s == 1 || us < least) {
+      least = us;
+      best = chunk;
+    }
+  }
+  return std::max<int64_t>(best, 64);
+}
+
+// Cuts a batch into units of `R` rows and their keys into chunks.  `at`: free
+// workspace.
+ql_status plan_part(const ql_attention_shape& s, bool tile, int R, int64_t rows, int64_t at, Part* p) {
+  const int64_t group = s.q_heads / s.kv_heads;
+  const int64_t blocks = (rows + R - 1) / R;
+  const int64_t units = s.batch * blocks * s.kv_heads;
+  // the keys a block of rows can see, from the 64-aligned start of its window
+  const int64_t span = s.window ? std::min<int64_t>(s.max_kv, (int64_t)s.window + R / group + 2 + 64) : s.max_kv;
+  const int64_t chunk = tile ? tile_chunk(units, span) : stream_chunk(units, span);
+  const int64_t splits = std::max<int64_t>(1, (span + chunk - 1) / chunk);
+  if (units * splits >= (int64_t(1) << 31) || units * R / 4 >= (int64_t(1) << 31))
+    return fail(QL_E_UNSUPPORTED, "more than 2^31 workgroups");
+  const int64_t parts = splits > 1 ? units * splits * R : 0;
+  *p = Part{true, R, (int)blocks, (int)splits, (int)chunk, (int)units, at, at + parts * s.head_dim * 4,
+            at + parts * (s.head_dim + 2) * 4};
+  return QL_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -178,40 +244,35 @@ ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan*
   const int64_t group = s->q_heads / s->kv_heads;
   const int64_t rows = s->max_q * group;
   if (rows > (int64_t(1) << 30)) return fail(QL_E_UNSUPPORTED, "max_q * q_heads / kv_heads exceeds 2^30");
-  ql_attention_facts f{};
-  f.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
-  const int64_t blocks = (rows + f.rows - 1) / f.rows;
-  const int64_t units = s->batch * blocks * s->kv_heads;
-  // the keys a block of rows can see, from the 64-aligned start of its window
-  const int64_t block_tokens = f.rows / group + 2;
-  const int64_t span = s->window ? std::min<int64_t>(s->max_kv, (int64_t)s->window + block_tokens + 64) : s->max_kv;
-  // chunks: enough workgroups to fill the card a few times over
-  int64_t chunk = 256;
-  while (units * ((span + chunk - 1) / chunk) > 2048 && chunk < span) chunk *= 2;
-  const int64_t splits = std::max<int64_t>(1, (span + chunk - 1) / chunk);
-  if (units * splits * f.rows / 4 >= (int64_t(1) << 31)) return fail(QL_E_UNSUPPORTED, "more than 2^31 workgroups");
-  f.row_blocks = (int32_t)blocks;
-  f.splits = (int32_t)splits;
-  f.chunk = (int32_t)chunk;
-  const int64_t parts = splits > 1 ? units * splits * f.rows : 0;
-  f.workspace_bytes = parts * (s->head_dim + 2) * 4;
   ql_attention_plan_s* p = new (std::nothrow) ql_attention_plan_s();
   if (!p) return fail(QL_E_INVALID, "out of host memory");
   p->shape = *s;
-  p->facts = f;
-  p->part_ml_at = parts * s->head_dim * 4;
-  p->units = (int)units;
+  const bool chunks = rows > kStreamRows;
+  // sequences of few rows among longer ones: a launch of their own, unless
+  // every sequence has max_q new tokens
+  const bool mixed = chunks && s->tokens < s->batch * s->max_q;
+  p->tile_from = mixed ? kMixedRows + 1 : 0;
+  if (!chunks || mixed) {
+    const int64_t most = mixed ? kMixedRows : rows;
+    st = plan_part(*s, false, most <= 16 ? 16 : most <= 32 ? 32 : 64, most, 0, &p->stream);
+  }
+  if (st == QL_OK && chunks) st = plan_part(*s, true, kTileRows, rows, p->stream.end, &p->tile);
+  if (st != QL_OK) {
+    delete p;
+    return st;
+  }
   *out = p;
   return QL_OK;
 }
 
 ql_status qlinear_attention_plan_info(ql_attention_plan p, ql_attention_facts* facts) {
   if (!p || !facts) return fail(QL_E_INVALID, "NULL argument");
-  *facts = p->facts;
+  const Part& x = p->tile.used ? p->tile : p->stream;
+  *facts = ql_attention_facts{x.rows, x.row_blocks, x.splits, x.chunk, std::max(p->stream.end, p->tile.end)};
   return QL_OK;
 }
 
-int64_t qlinear_attention_workspace_bytes(ql_attention_plan p) { return p ? p->facts.workspace_bytes : 0; }
+int64_t qlinear_attention_workspace_bytes(ql_attention_plan p) { return p ? std::max(p->stream.end, p->tile.end) : 0; }
 
 void qlinear_attention_plan_destroy(ql_attention_plan p) { delete p; }
 
@@ -220,7 +281,6 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
                             const int32_t* cu_q, const ql_rows* out, float* lse, void* workspace, void* stream) {
   if (!p) return fail(QL_E_INVALID, "plan is NULL");
   const ql_attention_shape& s = p->shape;
-  const ql_attention_facts& f = p->facts;
   qlk::AttnArgs a{};
   ql_status st = check_cache(cache, &a.kc, &a.vc);
   if (st != QL_OK) return st;
@@ -234,15 +294,13 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
     return fail(QL_E_ALIGN, "page_table, seq_lens, cu_q and lse must be 4-byte aligned");
   if (s.batch > 1 && table_stride < (s.max_kv + s.page_size - 1) / s.page_size)
     return fail(QL_E_INVALID, "page_table rows hold fewer than ceil(max_kv / page_size) entries");
-  if (f.workspace_bytes > 0 && !workspace) return fail(QL_E_INVALID, "this plan needs a workspace");
+  if (qlinear_attention_workspace_bytes(p) > 0 && !workspace) return fail(QL_E_INVALID, "this plan needs a workspace");
   if (!aligned16(workspace)) return fail(QL_E_ALIGN, "workspace is not 16-byte aligned");
   a.table = page_table;
   a.table_row = table_stride;
   a.seq_lens = seq_lens;
   a.cu_q = cu_q;
   a.lse = lse;
-  a.part_o = static_cast<float*>(workspace);
-  a.part_ml = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p->part_ml_at) : nullptr;
   a.page_magic = page_magic(s.page_size);
   const float scale = s.scale != 0.0f ? s.scale : 1.0f / std::sqrt((float)s.head_dim);
   a.scale_log2 = scale * 1.4426950408889634f;
@@ -255,17 +313,24 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
   a.max_kv = (int)s.max_kv;
   a.causal = s.causal;
   a.window = s.window;
-  a.row_blocks = f.row_blocks;
-  a.splits = f.splits;
-  a.chunk = f.chunk;
-  a.min_rows = 0;
-  a.max_rows = INT32_MAX;
   hipStream_t hs = static_cast<hipStream_t>(stream);
-  hipError_t e = qlk::launch_attn_stream(a, s.head_dim, s.kv_type == QL_KV_E4M3, f.rows, p->units, hs);
-  if (e != hipSuccess) return hip_fail(e, "attention launch");
-  if (f.splits > 1) {
-    e = qlk::launch_attn_join(a, s.head_dim, f.rows, (int)s.batch, hs);
-    if (e != hipSuccess) return hip_fail(e, "attention join launch");
+  const bool e4m3 = s.kv_type == QL_KV_E4M3;
+  for (int pass = 0; pass < 2; ++pass) {  // both kernels, then the joins: the kernels may overlap
+    for (const Part* x : {&p->stream, &p->tile}) {
+      if (!x->used || (pass && x->splits <= 1)) continue;
+      const bool tile = x == &p->tile;
+      a.row_blocks = x->row_blocks;
+      a.splits = x->splits;
+      a.chunk = x->chunk;
+      a.min_rows = tile ? p->tile_from : 0;
+      a.max_rows = !tile && p->tile.used ? p->tile_from - 1 : INT32_MAX;
+      a.part_o = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x->o_at) : nullptr;
+      a.part_ml = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x->ml_at) : nullptr;
+      hipError_t e = pass ? qlk::launch_attn_join(a, s.head_dim, x->rows, (int)s.batch, hs)
+                    : tile ? qlk::launch_attn_tile(a, s.head_dim, e4m3, x->units, hs)
+                           : qlk::launch_attn_stream(a, s.head_dim, e4m3, x->rows, x->units, hs);
+      if (e != hipSuccess) return hip_fail(e, pass ? "attention join launch" : "attention launch");
+    }
   }
   return QL_OK;
 }

@@ -70,8 +70,6 @@ struct VerifyArgs {
   int batch, vocab, max_drafts, slices;
 };
 
-// Rows of a unit each attention kernel handles in one workgroup.
-constexpr int kStreamRowsMax = 64;  // the stream kernel: 16, 32 or 64
 constexpr int kPageMagicShift = 36;
 
 // The page column of the 16-key group `sub` (page_size / 16 groups a page):
@@ -83,6 +81,7 @@ __host__ __device__ __forceinline__ int page_of(int sub, uint64_t magic) {
 
 hipError_t launch_heads(const HeadArgs& a, int head_dim, bool append, bool e4m3, hipStream_t s);
 hipError_t launch_attn_stream(const AttnArgs& a, int head_dim, bool e4m3, int rows, int units, hipStream_t s);
+hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, bool e4m3, int units, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, int batch, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
 

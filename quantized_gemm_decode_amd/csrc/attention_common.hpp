@@ -35,6 +35,20 @@ __device__ __forceinline__ uint32_t e4m3_to_bf16(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
 }
 
+// Pins a value's computation to this place: without it the compiler turns a
+// rarely taken branch into arithmetic that is always done, or sinks work out
+// of the block whose products are to cover it.
+template <class T>
+__device__ __forceinline__ void pin(T& x) {
+  asm volatile("" : "+v"(x));
+}
+
+// Maximum over a lane and the lane 32 away.
+__device__ __forceinline__ float half_max(float v) {
+  const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+}
+
 // Maximum and sum over lanes l, l^16, l^32, l^48: the four lanes that hold
 // one row's keys.
 __device__ __forceinline__ float row4_max(float v) {
@@ -93,16 +107,30 @@ __device__ __forceinline__ void row_range(const AttnArgs& a, const Unit& u, int 
   *lo = a.window ? max(0, p - a.window + 1) : 0;
 }
 
-// Page of the 16-key group that starts at key `key`, and the key's place in
-// it.  Columns past the sequence's last page are never read, and a page
-// number out of range is taken into range (a wrong answer for a broken
-// table, never a read outside the cache).
-__device__ __forceinline__ int64_t page_at(const AttnArgs& a, const int32_t* row, int key, int last_sub, int* at) {
-  const int sub = min(key >> 4, last_sub);
+// Where 64 16-key groups of a sequence lie: lane i holds the byte offsets of
+// group `group` of its own in K and V.  One gather of page numbers and one
+// round of address arithmetic serve 64 groups; a wave then picks a group by
+// its lane number, without a dependent scalar load per tile.  Columns past
+// the sequence's last page are never read, and a page number out of range is
+// taken into range (a wrong answer for a broken table, never a read outside
+// the cache).
+struct Groups {
+  uint32_t k_lo, k_hi, v_lo, v_hi;
+};
+
+__device__ __forceinline__ Groups groups_at(const AttnArgs& a, const int32_t* row, int h, int group, int last) {
+  const int sub = min(group, last);
   const int col = page_of(sub, a.page_magic);
-  *at = sub * 16 - col * a.page_size;
-  const uint32_t page = (uint32_t)uniform_i32(row + col);
-  return (int64_t)min(page, (uint32_t)(a.num_pages - 1));
+  const int64_t at = sub * 16 - col * a.page_size;
+  const int64_t page = min((uint32_t)row[col], (uint32_t)(a.num_pages - 1));
+  const uint64_t k = (uint64_t)(page * a.kc.page + at * a.kc.token + h * a.kc.head);
+  const uint64_t v = (uint64_t)(page * a.vc.page + at * a.vc.token + h * a.vc.head);
+  return Groups{(uint32_t)k, (uint32_t)(k >> 32), (uint32_t)v, (uint32_t)(v >> 32)};
+}
+
+__device__ __forceinline__ uint64_t pick(uint32_t lo, uint32_t hi, int i) {
+  return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)lo, i) |
+         (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, i) << 32;
 }
 
 }  // namespace qlk

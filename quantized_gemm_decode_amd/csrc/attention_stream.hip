@@ -56,22 +56,26 @@ __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* o) {
   }
 }
 
-// Loads the tile that starts at key `key` (a multiple of 32).
+// Loads a tile: its two 16-key groups are entries i and i + 1 of `at`.
 template <int D, bool E4M3>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, const int32_t* table, int h, int key, int last_sub,
-                                          uint32_t k_lane, uint32_t v_lane, KvTile<D, E4M3>* t) {
+__device__ __forceinline__ void load_tile(const AttnArgs& a, const Groups& at, int i, uint32_t k_lane, uint32_t v_lane,
+                                          KvTile<D, E4M3>* t) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    int at;
-    const int64_t page = page_at(a, table, key + 16 * u, last_sub, &at);
-    const uint8_t* k = a.kc.p + page * a.kc.page + at * a.kc.token + h * a.kc.head;
-    const uint8_t* v = a.vc.p + page * a.vc.page + at * a.vc.token + h * a.vc.head;
+    const uint8_t* k = a.kc.p + pick(at.k_lo, at.k_hi, i + u);
+    const uint8_t* v = a.vc.p + pick(at.v_lo, at.v_hi, i + u);
 #pragma unroll
     for (int s = 0; s < KvTile<D, E4M3>::KP; ++s) t->k[u][s] = *reinterpret_cast<const u32x4*>(k + k_lane + 64 * s);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      load_words<KvTile<D, E4M3>::VW>(v + v_lane + (uint32_t)(j * (int)a.vc.token), t->v[4 * u + j]);
+      load_words<KvTile<D, E4M3>::VW>(v + j * (int)a.vc.token + v_lane, t->v[4 * u + j]);
   }
+}
+
+// The groups of a wave's next 32 tiles, the first at key `key`.
+__device__ __forceinline__ Groups tile_groups(const AttnArgs& a, const int32_t* table, int h, int key, int last) {
+  const int lane = threadIdx.x & 63;
+  return groups_at(a, table, h, (key >> 4) + 2 * kStreamWaves * (lane >> 1) + (lane & 1), last);
 }
 
 // V^T operand of product dt from a tile's value rows: 8 keys of one value.
@@ -149,14 +153,22 @@ __global__ void __launch_bounds__(kStreamWaves * 64, NR == 4 ? 1 : 2) attn_strea
   const uint32_t k_lane = (uint32_t)(r * (int)a.kc.token + g * 16);
   const uint32_t v_lane = (uint32_t)(4 * g * (int)a.vc.token + r * Tile::VW * 4);
 
-  int key = begin + 32 * wave;
+  // this wave's tiles are every fourth: lane i holds group i % 2 of its tile
+  // i / 2, 32 tiles at a time
+  int key = begin + 32 * wave, tile = 0;
+  Groups at;
   Tile cur;
-  if (AHEAD && key < end) load_tile<D, E4M3>(a, table, h, key, last_sub, k_lane, v_lane, &cur);
+  if (key < end) {
+    at = tile_groups(a, table, h, key, last_sub);
+    if (AHEAD) load_tile<D, E4M3>(a, at, 0, k_lane, v_lane, &cur);
+  }
   for (; key < end; key += 32 * kStreamWaves) {
     Tile next;
-    if (!AHEAD) load_tile<D, E4M3>(a, table, h, key, last_sub, k_lane, v_lane, &cur);
-    if (AHEAD && key + 32 * kStreamWaves < end)
-      load_tile<D, E4M3>(a, table, h, key + 32 * kStreamWaves, last_sub, k_lane, v_lane, &next);
+    if (!AHEAD) load_tile<D, E4M3>(a, at, 2 * (tile & 31), k_lane, v_lane, &cur);
+    if (key + 32 * kStreamWaves < end) {
+      if ((++tile & 31) == 0) at = tile_groups(a, table, h, key + 32 * kStreamWaves, last_sub);
+      if (AHEAD) load_tile<D, E4M3>(a, at, 2 * (tile & 31), k_lane, v_lane, &next);
+    }
     if (key + 32 > u.len) {  // the cache beyond the sequence may hold anything: 0 * NaN would reach every row
 #pragma unroll
       for (int j = 0; j < 8; ++j)

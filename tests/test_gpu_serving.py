@@ -270,6 +270,8 @@ ATTEND_CASES = [  # new, kv, hq, hk, D, page, e4m3, order, causal, window
     ([260], [777], 6, 2, 64, 32, True, "token", True, 200),
     ([131], [400], 5, 1, 64, 16, False, "token", False, 0),
     ([300], [2000], 4, 1, 128, 48, False, "token", True, 333),
+    ([40, 1], [9000, 8500], 4, 1, 128, 16, False, "token", True, 0),          # many pages a wave
+    ([33], [4500], 4, 1, 64, 32, True, "head", True, 4200),
 ]
 
 
