@@ -618,12 +618,14 @@ ql_status qlinear_qkv_append(const ql_norm_rope* rule, int64_t tokens, int32_t q
  * arrays: lengths are clamped to max_kv, pages to the cache, cu_q to
  * [0, tokens].
  *
- * The plan fixes the shape and chooses the kernels and the number of chunks
- * that long contexts are cut into.  max_q, max_kv: upper bounds of a
+ * The plan fixes the shape and chooses the kernels: up to 32 rows (new tokens
+ * times query heads of a KV head) of a sequence, one that streams the keys; above,
+ * one that shares tiles of them between many rows; both for batches that mix
+ * such sequences with ones of up to 16 rows.  max_q, max_kv: upper bounds of a
  * sequence's new and cached tokens (the page table holds at least
  * ceil(max_kv / page_size) columns); rows of a sequence beyond max_q are not
  * computed.  q_heads a multiple of kv_heads; head_dim 64 or 128; scale 0 =
- * 1 / sqrt(head_dim).  Chunks are joined by a second launch (no atomics:
+ * 1 / sqrt(head_dim).  Partial results are joined by a second launch (no atomics:
  * results do not depend on timing).  The workspace needs no initialisation;
  * concurrent calls need distinct ones.
  */
@@ -636,10 +638,12 @@ typedef struct {
 } ql_attention_shape;
 
 typedef struct {
-  int32_t rows;       /* (token, query head) rows of a workgroup's unit */
-  int32_t row_blocks; /* units of the longest sequence and one KV head */
-  int32_t splits;     /* most chunks a unit's keys are cut into */
-  int32_t chunk;      /* keys of a chunk */
+  int32_t stream_rows;  /* stream kernel: (token, query head) rows of a sequence and KV head it is built for, 0 = not used */
+  int32_t slots;        /* shares that it cuts all sequences' keys into, for each KV head */
+  int32_t tile_rows;    /* tile kernel: rows of a unit, 0 = not used */
+  int32_t row_blocks;   /* units of the longest sequence and one KV head */
+  int32_t splits;       /* most chunks a unit's keys are cut into */
+  int32_t chunk;        /* keys of a chunk */
   int64_t workspace_bytes;
 } ql_attention_facts;
 

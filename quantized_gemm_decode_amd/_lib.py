@@ -42,7 +42,7 @@ class QLAttentionShape(ctypes.Structure):
 
 
 class QLAttentionFacts(ctypes.Structure):
-    _fields_ = [(n, c_i32) for n in ("rows", "row_blocks", "splits", "chunk")] + [("workspace_bytes", c_i64)]
+    _fields_ = [(n, c_i32) for n in ("stream_rows", "slots", "tile_rows", "row_blocks", "splits", "chunk")] + [("workspace_bytes", c_i64)]
 
 
 c_rows, c_cache = ctypes.POINTER(QLRows), ctypes.POINTER(QLKvCache)

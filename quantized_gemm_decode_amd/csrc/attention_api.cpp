@@ -21,8 +21,10 @@ namespace {
 // One kernel's share of a plan.
 struct Part {
   bool used;
-  int rows, row_blocks, splits, chunk, units;
-  int64_t o_at, ml_at, end;  // partial outputs, their maxima and sums, in the workspace (bytes)
+  int rows;                              // rows of a unit
+  int row_blocks, splits, chunk, units;  // tile kernel
+  int slots, heads_wg, most;             // stream kernel; most rows of its sequences
+  int64_t o_at, ml_at, end;              // partial outputs, their maxima and sums, in the workspace (bytes)
 };
 
 }  // namespace
@@ -129,20 +131,19 @@ ql_status check_rule(const ql_norm_rope* r, int64_t tokens, int32_t q_heads, int
 
 // Rows (new tokens x query heads of a KV head) of a sequence up to which the
 // stream kernel serves it; in a batch that has longer ones too, up to which
-// sequences get a stream launch of their own.
-constexpr int64_t kStreamRows = 64;
+// sequences get a stream launch of their own.  16 sequences of 4,000 keys: 61 us
+// with 32 rows each here; with 64 rows the tile kernel takes 66 us and the
+// stream kernel would not hold their sums in registers.
+constexpr int64_t kStreamRows = 32;
 constexpr int64_t kMixedRows = 16;
 
-constexpr int kTileRows = 128;
+// Tiles of 32 keys that a slot of the stream kernel holds at least.  One
+// sequence of 1,000 keys: 10.6, 11.3, 12.4 us with 1, 2, 3; of 2,000: 13.5,
+// 12.7, 13.7; two of 6,000 (E4M3): 17.9, 16.6, 15.7 -- shorter slots, more
+// partial results.
+constexpr int kLeastTiles = 2;
 
-// Chunk of the stream kernel: it is bound by memory, so any cut costs the same
-// as long as the card is full and the partial results stay small beside the
-// keys: the shortest power of two from 256 keys with at most 2048 workgroups.
-int64_t stream_chunk(int64_t units, int64_t span) {
-  int64_t chunk = 256;
-  while (units * ((span + chunk - 1) / chunk) > 2048 && chunk < span) chunk *= 2;
-  return chunk;
-}
+constexpr int kTileRows = 128;
 
 // Chunk of the tile kernel, bound by arithmetic: a workgroup runs at its own
 // pace, 512 of them at a time (two a compute unit).  Measured for head_dim 128:
@@ -165,21 +166,48 @@ int64_t tile_chunk(int64_t units, int64_t span) {
   return std::max<int64_t>(best, 64);
 }
 
-// Cuts a batch into units of `R` rows and their keys into chunks.  `at`: free
-// workspace.
-ql_status plan_part(const ql_attention_shape& s, bool tile, int R, int64_t rows, int64_t at, Part* p) {
-  const int64_t group = s.q_heads / s.kv_heads;
+// Cuts a batch into units of kTileRows rows and their keys into chunks.
+// `at`: free workspace.
+ql_status plan_tile(const ql_attention_shape& s, int64_t rows, int64_t at, Part* p) {
+  const int64_t group = s.q_heads / s.kv_heads, R = kTileRows;
   const int64_t blocks = (rows + R - 1) / R;
   const int64_t units = s.batch * blocks * s.kv_heads;
   // the keys a block of rows can see, from the 64-aligned start of its window
   const int64_t span = s.window ? std::min<int64_t>(s.max_kv, (int64_t)s.window + R / group + 2 + 64) : s.max_kv;
-  const int64_t chunk = tile ? tile_chunk(units, span) : stream_chunk(units, span);
+  const int64_t chunk = tile_chunk(units, span);
   const int64_t splits = std::max<int64_t>(1, (span + chunk - 1) / chunk);
   if (units * splits >= (int64_t(1) << 31) || units * R / 4 >= (int64_t(1) << 31))
     return fail(QL_E_UNSUPPORTED, "more than 2^31 workgroups");
   const int64_t parts = splits > 1 ? units * splits * R : 0;
-  *p = Part{true, R, (int)blocks, (int)splits, (int)chunk, (int)units, at, at + parts * s.head_dim * 4,
-            at + parts * (s.head_dim + 2) * 4};
+  p->used = true;
+  p->rows = (int)R;
+  p->row_blocks = (int)blocks;
+  p->splits = (int)splits;
+  p->chunk = (int)chunk;
+  p->units = (int)units;
+  p->o_at = at;
+  p->ml_at = at + parts * s.head_dim * 4;
+  p->end = p->ml_at + parts * 2 * 4;
+  return QL_OK;
+}
+
+// The stream kernel for sequences of at most `rows` rows: the shares of the
+// keys are cut on the device, the plan fixes how many there can be.
+ql_status plan_stream(const ql_attention_shape& s, int64_t rows, Part* p) {
+  const int64_t tiles = s.batch * (s.max_kv / 32 + 1);
+  if (tiles >= (int64_t(1) << 31)) return fail(QL_E_UNSUPPORTED, "batch * max_kv / 32 exceeds 2^31");
+  p->used = true;
+  p->rows = rows <= 16 ? 16 : 32;
+  p->most = (int)rows;
+  p->heads_wg = s.kv_heads % 4 == 0 ? 4 : s.kv_heads % 2 == 0 ? 2 : 1;
+  p->slots = qlk::attn_stream_slots(s.head_dim, s.kv_type == QL_KV_E4M3, p->rows, s.kv_heads, p->heads_wg);
+  if ((int64_t)p->slots * s.kv_heads >= (int64_t(1) << 31) || rows * s.kv_heads >= (int64_t(1) << 31))
+    return fail(QL_E_UNSUPPORTED, "more than 2^31 workgroups");
+  // a batch that fits one tile a sequence is never cut
+  const int64_t parts = s.max_kv > 32 ? (int64_t)p->slots * 2 * s.kv_heads * p->rows : 0;
+  p->splits = parts ? 2 : 1;
+  p->ml_at = parts * s.head_dim * 4;
+  p->end = p->ml_at + parts * 2 * 4;
   return QL_OK;
 }
 
@@ -252,11 +280,8 @@ ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan*
   // every sequence has max_q new tokens
   const bool mixed = chunks && s->tokens < s->batch * s->max_q;
   p->tile_from = mixed ? kMixedRows + 1 : 0;
-  if (!chunks || mixed) {
-    const int64_t most = mixed ? kMixedRows : rows;
-    st = plan_part(*s, false, most <= 16 ? 16 : most <= 32 ? 32 : 64, most, 0, &p->stream);
-  }
-  if (st == QL_OK && chunks) st = plan_part(*s, true, kTileRows, rows, p->stream.end, &p->tile);
+  if (!chunks || mixed) st = plan_stream(*s, mixed ? kMixedRows : rows, &p->stream);
+  if (st == QL_OK && chunks) st = plan_tile(*s, rows, p->stream.end, &p->tile);
   if (st != QL_OK) {
     delete p;
     return st;
@@ -267,8 +292,9 @@ ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan*
 
 ql_status qlinear_attention_plan_info(ql_attention_plan p, ql_attention_facts* facts) {
   if (!p || !facts) return fail(QL_E_INVALID, "NULL argument");
-  const Part& x = p->tile.used ? p->tile : p->stream;
-  *facts = ql_attention_facts{x.rows, x.row_blocks, x.splits, x.chunk, std::max(p->stream.end, p->tile.end)};
+  *facts = ql_attention_facts{p->stream.used ? p->stream.rows : 0, p->stream.slots, p->tile.used ? p->tile.rows : 0,
+                              p->tile.row_blocks, p->tile.splits, p->tile.chunk,
+                              qlinear_attention_workspace_bytes(p)};
   return QL_OK;
 }
 
@@ -304,6 +330,7 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
   a.page_magic = page_magic(s.page_size);
   const float scale = s.scale != 0.0f ? s.scale : 1.0f / std::sqrt((float)s.head_dim);
   a.scale_log2 = scale * 1.4426950408889634f;
+  a.batch = (int)s.batch;
   a.tokens = (int)s.tokens;
   a.q_heads = s.q_heads;
   a.kv_heads = s.kv_heads;
@@ -315,24 +342,32 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
   a.window = s.window;
   hipStream_t hs = static_cast<hipStream_t>(stream);
   const bool e4m3 = s.kv_type == QL_KV_E4M3;
-  for (int pass = 0; pass < 2; ++pass) {  // both kernels, then the joins: the kernels may overlap
-    for (const Part* x : {&p->stream, &p->tile}) {
-      if (!x->used || (pass && x->splits <= 1)) continue;
-      const bool tile = x == &p->tile;
-      a.row_blocks = x->row_blocks;
-      a.splits = x->splits;
-      a.chunk = x->chunk;
-      a.min_rows = tile ? p->tile_from : 0;
-      a.max_rows = !tile && p->tile.used ? p->tile_from - 1 : INT32_MAX;
-      a.part_o = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x->o_at) : nullptr;
-      a.part_ml = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x->ml_at) : nullptr;
-      hipError_t e = pass ? qlk::launch_attn_join(a, s.head_dim, x->rows, (int)s.batch, hs)
-                    : tile ? qlk::launch_attn_tile(a, s.head_dim, e4m3, x->units, hs)
-                           : qlk::launch_attn_stream(a, s.head_dim, e4m3, x->rows, x->units, hs);
-      if (e != hipSuccess) return hip_fail(e, pass ? "attention join launch" : "attention launch");
-    }
+  auto partials = [&](const Part& x) {
+    a.part_o = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x.o_at) : nullptr;
+    a.part_ml = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x.ml_at) : nullptr;
+  };
+  hipError_t e = hipSuccess;
+  if (p->stream.used) {
+    const Part& x = p->stream;
+    partials(x);
+    a.slots = x.slots;
+    a.least_tiles = kLeastTiles;
+    a.heads_wg = x.heads_wg;
+    a.max_rows = x.most;
+    e = qlk::launch_attn_stream(a, s.head_dim, e4m3, x.rows, hs);
+    if (e == hipSuccess && x.splits > 1) e = qlk::launch_attn_stream_join(a, s.head_dim, x.rows, x.most, hs);
   }
-  return QL_OK;
+  if (e == hipSuccess && p->tile.used) {
+    const Part& x = p->tile;
+    partials(x);
+    a.row_blocks = x.row_blocks;
+    a.splits = x.splits;
+    a.chunk = x.chunk;
+    a.min_rows = p->tile_from;
+    e = qlk::launch_attn_tile(a, s.head_dim, e4m3, x.units, hs);
+    if (e == hipSuccess && x.splits > 1) e = qlk::launch_attn_join(a, s.head_dim, x.rows, (int)s.batch, hs);
+  }
+  return e == hipSuccess ? QL_OK : hip_fail(e, "attention launch");
 }
 
 // Slices of a vocabulary row: enough workgroups for the card with few

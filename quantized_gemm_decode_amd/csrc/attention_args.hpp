@@ -45,15 +45,21 @@ struct AttnArgs {
   const int32_t* seq_lens;
   const int32_t* cu_q;
   float* lse;            // [tokens, q_heads] or null
-  float* part_o;         // [units, splits, R, head_dim] partial outputs
-  float* part_ml;        // [units, splits, R, 2] their row maxima (base 2) and sums
+  float* part_o;         // partial outputs of head_dim values a row: [units, splits, R] rows of the tile
+                         // kernel, [slots, 2, kv_heads, R] rows of the stream kernel
+  float* part_ml;        // their rows' maxima (base 2) and sums
   uint64_t page_magic;
   float scale_log2;      // softmax scale * log2(e)
-  int tokens, q_heads, kv_heads, group, page_size, num_pages, max_kv, causal, window;
+  int batch, tokens, q_heads, kv_heads, group, page_size, num_pages, max_kv, causal, window;
+  // tile kernel
   int row_blocks;        // blocks of R (token, head of the group) rows of a sequence and KV head
   int splits, chunk;     // most chunks of keys of a unit, and their length
-  int min_rows;          // sequences with fewer rows are left to the other kernel (tile kernel)
-  int max_rows;          // sequences with more rows are left to the other kernel (stream kernel)
+  int min_rows;          // sequences with fewer rows are left to the stream kernel
+  // stream kernel
+  int slots;             // shares that all sequences' keys are cut into, for each KV head
+  int least_tiles;       // tiles of a slot at least (fewer slots otherwise)
+  int heads_wg;          // KV heads of a workgroup (1, 2 or 4); its other waves take other slots
+  int max_rows;          // sequences with more rows are left to the tile kernel
 };
 
 struct VerifyArgs {
@@ -80,7 +86,10 @@ __host__ __device__ __forceinline__ int page_of(int sub, uint64_t magic) {
 }
 
 hipError_t launch_heads(const HeadArgs& a, int head_dim, bool append, bool e4m3, hipStream_t s);
-hipError_t launch_attn_stream(const AttnArgs& a, int head_dim, bool e4m3, int rows, int units, hipStream_t s);
+// Slots of the stream kernel: as many as the card holds waves for each KV head.
+int attn_stream_slots(int head_dim, bool e4m3, int rows, int kv_heads, int heads_wg);
+hipError_t launch_attn_stream(const AttnArgs& a, int head_dim, bool e4m3, int rows, hipStream_t s);
+hipError_t launch_attn_stream_join(const AttnArgs& a, int head_dim, int rows, int most_rows, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, bool e4m3, int units, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, int batch, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);

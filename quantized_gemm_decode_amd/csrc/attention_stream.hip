@@ -5,12 +5,19 @@
 //
 // Few rows (new tokens x query heads of a KV head) read long K and V, 2
 // bytes (E4M3: 1) for 2 flops a row and value: bound by memory up to about
-// 150 rows.  So the kernel is built as a stream.  Every wave takes tiles of
-// 32 keys of its own and loads them straight into matrix-core operands, the
-// next tile's loads in flight while it works on one; there is no barrier and
-// no LDS until the workgroup's four waves join at the end.  Long contexts are
-// cut into chunks over many workgroups; attention_join adds their partial
-// results.
+// 150 rows.  So the kernel is built as a stream.
+//
+// All sequences' keys, in tiles of 32, are laid end to end and cut into equal
+// slots, one a wave and KV head, as many as the card holds at once: every wave
+// starts at once, reads the same amount and ends at the same time, whatever
+// the lengths.  (Chunks of one length in a grid of all sequences' longest left
+// the compute units idle for 40 % of the time: sequences end at different
+// chunks.)  A wave that passes from one sequence to the next writes the first
+// one's result and starts over; where a sequence lies in several slots their
+// results are partial and the join kernel adds them.  There are no barriers
+// and no LDS; waves of a workgroup take the heads of the same keys, which lie
+// next to each other in memory, and workgroups of the same slot follow each
+// other on one XCD.
 //
 // Operands (16x16x32 bf16; lane l = 16 g + r):
 //   S^T = K Q^T: the first operand is 16 keys (key r of the group in lane r)
@@ -23,7 +30,7 @@
 //     (whole rows of V per 16 lanes), and the 8 x D/16 transposition into
 //     operands stays inside the lane (one byte permutation per two values).
 //     So output value d sits in operand row d / (D/16) of product d % (D/16).
-// P is rounded to bf16 for the product (its error, 2^-9 of a term at most,
+// P is rounded to bf16 for the product (its error, 2^-8 of a term at most,
 // averages out below the output's own rounding); the row sums take P in
 // binary32 before that, and all sums and maxima are binary32.
 #include "attention_common.hpp"
@@ -44,38 +51,104 @@ struct KvTile {
 template <int N>
 __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t* o) {
   if constexpr (N == 4) {
-    const u32x4 t = *reinterpret_cast<const u32x4*>(p);
+    const u32x4 t = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(p));
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[i] = t[i];
   } else if constexpr (N == 2) {
-    const u32x2 t = *reinterpret_cast<const u32x2*>(p);
+    const u32x2 t = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p));
     o[0] = t.x;
     o[1] = t.y;
   } else {
-    o[0] = *reinterpret_cast<const uint32_t*>(p);
+    o[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(p));
   }
 }
 
-// Loads a tile: its two 16-key groups are entries i and i + 1 of `at`.
+// Loads a tile's K or V: its two 16-key groups are entries i and i + 1 of `at`.
 template <int D, bool E4M3>
-__device__ __forceinline__ void load_tile(const AttnArgs& a, const Groups& at, int i, uint32_t k_lane, uint32_t v_lane,
-                                          KvTile<D, E4M3>* t) {
+__device__ __forceinline__ void load_k(const AttnArgs& a, const Groups& at, int i, uint32_t lane, KvTile<D, E4M3>* t) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const uint8_t* k = a.kc.p + pick(at.k_lo, at.k_hi, i + u);
-    const uint8_t* v = a.vc.p + pick(at.v_lo, at.v_hi, i + u);
 #pragma unroll
-    for (int s = 0; s < KvTile<D, E4M3>::KP; ++s) t->k[u][s] = *reinterpret_cast<const u32x4*>(k + k_lane + 64 * s);
-#pragma unroll
-    for (int j = 0; j < 4; ++j)
-      load_words<KvTile<D, E4M3>::VW>(v + j * (int)a.vc.token + v_lane, t->v[4 * u + j]);
+    for (int s = 0; s < KvTile<D, E4M3>::KP; ++s) t->k[u][s] = *reinterpret_cast<const u32x4*>(k + lane + 64 * s);
   }
 }
 
-// The groups of a wave's next 32 tiles, the first at key `key`.
-__device__ __forceinline__ Groups tile_groups(const AttnArgs& a, const int32_t* table, int h, int key, int last) {
+template <int D, bool E4M3>
+__device__ __forceinline__ void load_v(const AttnArgs& a, const Groups& at, int i, uint32_t lane, KvTile<D, E4M3>* t) {
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const uint8_t* v = a.vc.p + pick(at.v_lo, at.v_hi, i + u);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) load_words<KvTile<D, E4M3>::VW>(v + j * (int)a.vc.token + lane, t->v[4 * u + j]);
+  }
+}
+
+// One sequence of the stream: its new tokens, cached length and tiles.  lo is
+// the first key that any of its rows sees.
+struct Seq {
+  int first, n, len, lo, tiles;
+};
+
+// Sequence b as this lane's own (b < batch; no tiles if it has no rows here).
+__device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
+  Seq s = {0, 0, 0, 0, 0};
+  if (b < a.batch) {
+    const int q0 = min(max(a.cu_q[b], 0), a.tokens);
+    const int q1 = min(max(a.cu_q[b + 1], q0), a.tokens);
+    s.first = q0;
+    s.n = q1 - q0;
+    s.len = min(max(a.seq_lens[b], 0), a.max_kv);
+    s.lo = a.window ? min(s.len, max(0, s.len - s.n - a.window + 1)) : 0;
+    // rows without any key still need one tile to be written
+    if (s.n > 0 && s.n * a.group <= a.max_rows) s.tiles = max(1, (s.len - (s.lo & ~31) + 31) >> 5);
+  }
+  return s;
+}
+
+__device__ __forceinline__ int inclusive_sum(int v) {
   const int lane = threadIdx.x & 63;
-  return groups_at(a, table, h, (key >> 4) + 2 * kStreamWaves * (lane >> 1) + (lane & 1), last);
+#pragma unroll
+  for (int o = 1; o < 64; o *= 2) {
+    const int x = __shfl_up(v, o, 64);
+    if (lane >= o) v += x;
+  }
+  return v;
+}
+
+__device__ __forceinline__ int lane_i32(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
+
+// All sequences' tiles, and how they are cut: `slots` slots of `each` tiles,
+// the first `more` of them one longer.
+struct Cut {
+  int slots, each, more;
+  __device__ __forceinline__ int start(int j) const { return j * each + min(j, more); }
+  __device__ __forceinline__ int slot_of(int t) const {
+    const int longer = more * (each + 1);
+    return t < longer ? t / (each + 1) : more + (t - longer) / each;
+  }
+};
+
+__device__ __forceinline__ Cut cut_of(const AttnArgs& a, int tiles) {
+  Cut c;
+  c.slots = max(1, min(a.slots, (tiles + a.least_tiles - 1) / a.least_tiles));
+  c.each = tiles / c.slots;
+  c.more = tiles - c.each * c.slots;
+  return c;
+}
+
+// The 16-key groups of the 32 tiles of a sequence from key `key` on: lane i
+// holds group i % 2 of tile i / 2.
+__device__ __forceinline__ Groups tile_groups(const AttnArgs& a, const int32_t* table, int h, int key, int last) {
+  return groups_at(a, table, h, (key >> 4) + (threadIdx.x & 63), last);
+}
+
+// Operand k of the products over D for the 16 keys v: 8 values of one key.
+template <int D, bool E4M3>
+__device__ __forceinline__ u32x4 k_operand(const KvTile<D, E4M3>& t, int v, int k) {
+  if constexpr (!E4M3) return t.k[v][k];
+  const uint32_t c0 = t.k[v][k / 2][k % 2 * 2], c1 = t.k[v][k / 2][k % 2 * 2 + 1];
+  return u32x4{e4m3_to_bf16<false>(c0), e4m3_to_bf16<true>(c0), e4m3_to_bf16<false>(c1), e4m3_to_bf16<true>(c1)};
 }
 
 // V^T operand of product dt from a tile's value rows: 8 keys of one value.
@@ -95,237 +168,306 @@ __device__ __forceinline__ u32x4 v_operand(const KvTile<D, E4M3>& t, int dt) {
   return o;
 }
 
+// Workgroups a compute unit gets.  Measured over 32 sequences of 1,021 ..
+// 8,190 keys, bf16: 94.8 us with one, 100.3 us with two (16 sequences of 64-wide
+// heads: 30.1 and 31.3 us); 64 sequences of 4,003 .. 16,001, E4M3: 232.9 and
+// 210.9 us (64-wide: 27.9 and 22.3 us).  More requests on their way than that
+// only queue; E4M3's are half as large.  With 32 rows the sums of 128-wide heads
+// leave one workgroup its registers (E4M3: 51.5 us, 60.3 us squeezed into two;
+// 64-wide: 35.6 and 31.2 us).
+constexpr int stream_workgroups(int D, bool e4m3, int row_tiles) { return e4m3 && (row_tiles == 1 || D == 64) ? 2 : 1; }
+
 template <int D, bool E4M3, int NR>
-__global__ void __launch_bounds__(kStreamWaves * 64, NR == 4 ? 1 : 2) attn_stream_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, NR)) attn_stream_kernel(AttnArgs a) {
   constexpr int R = 16 * NR, DT = D / 16;
   constexpr int KS = D / 32;  // products over D of one 16-key group
   using Tile = KvTile<D, E4M3>;
-  // the next tile's registers fit beside the sums of few rows only
-  constexpr bool AHEAD = NR == 1 || E4M3;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  int id = blockIdx.x;
-  const int h = id % a.kv_heads;
-  id /= a.kv_heads;
-  const int split = id % a.splits;
-  id /= a.splits;
-  const int block = id % a.row_blocks, b = id / a.row_blocks;
-  const Unit u = unit_of(a, b, block, R);
-  if (u.rows == 0 || u.all > a.max_rows) return;
-  if (u.chunks == 0 ? split != 0 : split >= u.chunks) return;
-  const int begin = (u.lo & ~63) + split * a.chunk;
-  const int end = min(u.hi, begin + a.chunk);
+  const int head_groups = a.kv_heads / a.heads_wg;
+  const int h = (int)(blockIdx.x / 8) % head_groups * a.heads_wg + wave % a.heads_wg;
+  const int slot = ((int)(blockIdx.x / 8) / head_groups * 8 + (int)blockIdx.x % 8) * (kStreamWaves / a.heads_wg) +
+                   wave / a.heads_wg;
 
-  // Q operands, and the keys each of this lane's rows sees
-  u32x4 q[NR][KS];
-  int lo[NR], hi[NR];
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    const int row = 16 * n + r;
-    row_range(a, u, row, &lo[n], &hi[n]);
-    if (row >= u.rows) lo[n] = hi[n] = 0;
-    const int at = u.row0 + row, tok = at / a.group, head = h * a.group + at % a.group;
-    const uint8_t* p = a.q.p + (int64_t)(u.first + tok) * a.q.token + (int64_t)head * a.q.head;
-#pragma unroll
-    for (int s = 0; s < KS; ++s) {
-      const int d0 = E4M3 ? ((s / 2) * 4 + g) * 16 + (s % 2) * 8 : (s * 4 + g) * 8;
-      q[n][s] = row < u.rows ? *reinterpret_cast<const u32x4*>(p + d0 * 2) : u32x4{0u, 0u, 0u, 0u};
-    }
-  }
+  // the tiles of all sequences, 64 sequences at a time; `before`: of those
+  // before the ones the lanes hold
+  Seq mine = seq_of(a, lane);
+  int upto = inclusive_sum(mine.tiles), before = 0, base = 0;
+  int total = lane_i32(upto, 63);
+  for (int b0 = 64; b0 < a.batch; b0 += 64) total += lane_i32(inclusive_sum(seq_of(a, b0 + lane).tiles), 63);
+  const Cut cut = cut_of(a, total);
+  if (total == 0 || slot >= cut.slots) return;
+  int t = cut.start(slot);
+  const int t_begin = t, t_end = cut.start(slot + 1);
+
   const float scale = a.scale_log2 * (E4M3 && a.kc.scale ? a.kc.scale[h] : 1.0f);
-
-  f32x4 o[NR][DT];
-  float m[NR], l[NR];
-#pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    m[n] = kNegInf;
-    l[n] = 0.0f;
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) o[n][dt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-
-  // tiles every row of the block sees whole need no mask
-  int full_lo, full_hi, x;
-  row_range(a, u, u.rows - 1, &full_lo, &x);
-  row_range(a, u, 0, &x, &full_hi);
-  const int32_t* table = a.table + b * a.table_row;
-  const int last_sub = (u.len - 1) >> 4;
+  const float v_scale = E4M3 && a.vc.scale ? a.vc.scale[h] : 1.0f;
   const uint32_t k_lane = (uint32_t)(r * (int)a.kc.token + g * 16);
   const uint32_t v_lane = (uint32_t)(4 * g * (int)a.vc.token + r * Tile::VW * 4);
 
-  // this wave's tiles are every fourth: lane i holds group i % 2 of its tile
-  // i / 2, 32 tiles at a time
-  int key = begin + 32 * wave, tile = 0;
-  Groups at;
-  Tile cur;
-  if (key < end) {
-    at = tile_groups(a, table, h, key, last_sub);
-    if (AHEAD) load_tile<D, E4M3>(a, at, 0, k_lane, v_lane, &cur);
-  }
-  for (; key < end; key += 32 * kStreamWaves) {
-    Tile next;
-    if (!AHEAD) load_tile<D, E4M3>(a, at, 2 * (tile & 31), k_lane, v_lane, &cur);
-    if (key + 32 * kStreamWaves < end) {
-      if ((++tile & 31) == 0) at = tile_groups(a, table, h, key + 32 * kStreamWaves, last_sub);
-      if (AHEAD) load_tile<D, E4M3>(a, at, 2 * (tile & 31), k_lane, v_lane, &next);
+  while (t < t_end) {
+    // the sequence that tile t belongs to
+    while (before + lane_i32(upto, 63) <= t) {
+      before += lane_i32(upto, 63);
+      base += 64;
+      mine = seq_of(a, base + lane);
+      upto = inclusive_sum(mine.tiles);
     }
-    if (key + 32 > u.len) {  // the cache beyond the sequence may hold anything: 0 * NaN would reach every row
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (key + 16 * (j / 4) + 4 * g + j % 4 >= u.len)
-#pragma unroll
-          for (int w = 0; w < Tile::VW; ++w) cur.v[j][w] = 0u;
-    }
-    const bool whole = key >= full_lo && key + 32 <= full_hi;
-    u32x4 p[NR];
+    const int i = __ffsll((unsigned long long)__ballot(before + upto > t)) - 1;
+    const int b = base + i;
+    const Seq s = {lane_i32(mine.first, i), lane_i32(mine.n, i), lane_i32(mine.len, i), lane_i32(mine.lo, i),
+                   lane_i32(mine.tiles, i)};
+    const int seq_begin = before + lane_i32(upto, i) - s.tiles;
+    const int t_stop = min(t_end, seq_begin + s.tiles);
+    const int rows = min(s.n * a.group, R), pos0 = s.len - s.n;
+    int key = (s.lo & ~31) + (t - seq_begin) * 32;
+    const int end = (s.lo & ~31) + (t_stop - seq_begin) * 32;
+
+    const int32_t* table = a.table + (int64_t)b * a.table_row;
+    const int last_sub = max(s.len - 1, 0) >> 4;
+    Groups at = tile_groups(a, table, h, key, last_sub);
+
+    // Q operands, and the keys each of this lane's rows sees
+    u32x4 q[NR][KS];
+    int lo[NR], hi[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
-      float s[8];
+      const int row = 16 * n + r, tok = row / a.group, head = h * a.group + row % a.group;
+      hi[n] = row < rows ? a.causal ? min(s.len, max(0, pos0 + tok + 1)) : s.len : 0;
+      lo[n] = a.window ? max(0, pos0 + tok - a.window + 1) : 0;
+      const uint8_t* p = a.q.p + (int64_t)(s.first + tok) * a.q.token + (int64_t)head * a.q.head;
 #pragma unroll
-      for (int v = 0; v < 2; ++v) {
-        f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int i = 0; i < KS; ++i) {
-          u32x4 k;
-          if constexpr (E4M3) {
-#pragma unroll
-            for (int w = 0; w < 2; ++w) {
-              const uint32_t codes = cur.k[v][i / 2][(i % 2) * 2 + w];
-              k[2 * w] = e4m3_to_bf16<false>(codes);
-              k[2 * w + 1] = e4m3_to_bf16<true>(codes);
-            }
-          } else {
-            k = cur.k[v][i];
-          }
-          c = mma_bf16(k, q[n][i], c);
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[4 * v + i] = c[i];
+      for (int k = 0; k < KS; ++k) {
+        const int d0 = E4M3 ? ((k / 2) * 4 + g) * 16 + (k % 2) * 8 : (k * 4 + g) * 8;
+        q[n][k] = row < rows ? *reinterpret_cast<const u32x4*>(p + d0 * 2) : u32x4{0u, 0u, 0u, 0u};
       }
-      if (whole) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) s[i] *= scale;
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const int at = key + 16 * (i / 4) + 4 * g + i % 4;
-          s[i] = at >= lo[n] && at < hi[n] ? s[i] * scale : kNegInf;
-        }
-      }
-      float top = s[0];
-#pragma unroll
-      for (int i = 1; i < 8; ++i) top = fmaxf(top, s[i]);
-      top = fmaxf(m[n], row4_max(top));
-      const float base = top == kNegInf ? 0.0f : top;  // a row that has seen no key yet
-      const float keep = __builtin_amdgcn_exp2f(m[n] - base);
-      m[n] = top;
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        s[i] = __builtin_amdgcn_exp2f(s[i] - base);
-        sum += s[i];
-      }
-      l[n] = l[n] * keep + sum;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) p[n][i] = bf16_pair(s[2 * i], s[2 * i + 1]);
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) o[n][dt] *= keep;
     }
-#pragma unroll
-    for (int dt = 0; dt < DT; ++dt) {
-      const u32x4 v = v_operand<D, E4M3>(cur, dt);
-#pragma unroll
-      for (int n = 0; n < NR; ++n) o[n][dt] = mma_bf16(v, p[n], o[n][dt]);
-    }
-    if (AHEAD) cur = next;
-  }
+    // keys that every row sees
+    const int full_lo = a.window ? max(0, pos0 + (rows - 1) / a.group - a.window + 1) : 0;
+    const int full_hi = a.causal ? min(s.len, max(0, pos0 + 1)) : s.len;
 
-  // join the four waves: each scales its sums to the common maximum, then a
-  // thread adds 8 values of a row over the waves
-  constexpr int LD = D + 4;  // floats between rows
-  extern __shared__ float lds[];
-  float* const ml = lds + kStreamWaves * 16 * LD;  // [wave][NR][16][2]
+    f32x4 o[NR][DT];
+    float m[NR], l[NR];
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    l[n] = row4_sum(l[n]);
-    if (g == 0) {
-      ml[((wave * NR + n) * 16 + r) * 2] = m[n];
-      ml[((wave * NR + n) * 16 + r) * 2 + 1] = l[n];
+    for (int n = 0; n < NR; ++n) {
+      m[n] = kNegInf;
+      l[n] = 0.0f;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) o[n][dt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
-  }
-  __syncthreads();
-  const float v_scale = E4M3 && a.vc.scale ? a.vc.scale[h] : 1.0f;
-  const bool alone = u.chunks <= 1;
-  const int64_t unit = ((int64_t)b * a.row_blocks + block) * a.kv_heads + h;
+
+    // K of the next tile is on its way while the weights and sums of this one
+    // are made, V while the next one's scores are: one set of registers each
+    int tile = 0;
+    Tile cur;
+    load_k<D, E4M3>(a, at, 0, k_lane, &cur);
+    load_v<D, E4M3>(a, at, 0, v_lane, &cur);
+    for (; key < end; key += 32) {
+      float x[NR][8];
 #pragma unroll
-  for (int n = 0; n < NR; ++n) {
-    float top = kNegInf, sum = 0.0f;
+      for (int v = 0; v < 2; ++v)
 #pragma unroll
-    for (int w = 0; w < kStreamWaves; ++w) top = fmaxf(top, ml[((w * NR + n) * 16 + r) * 2]);
-    const float base = top == kNegInf ? 0.0f : top;
-    const float keep = __builtin_amdgcn_exp2f(m[n] - base);
-    if (n) __syncthreads();
+        for (int n = 0; n < NR; ++n) {
+          f32x4 c = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
+          for (int k = 0; k < KS; ++k) c = mma_bf16(k_operand<D, E4M3>(cur, v, k), q[n][k], c);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) lds[(wave * 16 + r) * LD + (4 * g + i) * DT + dt] = o[n][dt][i] * keep;
-    __syncthreads();
-    // 16 threads a row, D/16 values each
-    const int row = threadIdx.x / 16, d0 = (threadIdx.x % 16) * DT;
-    const int mine = 16 * n + row;
-    if (mine < u.rows) {
-      float acc[DT];
-#pragma unroll
-      for (int i = 0; i < DT; ++i) acc[i] = 0.0f;
-      float rt = kNegInf;
-#pragma unroll
-      for (int w = 0; w < kStreamWaves; ++w) rt = fmaxf(rt, ml[((w * NR + n) * 16 + row) * 2]);
-      const float rb = rt == kNegInf ? 0.0f : rt;
-#pragma unroll
-      for (int w = 0; w < kStreamWaves; ++w) {
-        sum += ml[((w * NR + n) * 16 + row) * 2 + 1] * __builtin_amdgcn_exp2f(ml[((w * NR + n) * 16 + row) * 2] - rb);
-#pragma unroll
-        for (int i = 0; i < DT; ++i) acc[i] += lds[(w * 16 + row) * LD + d0 + i];
+          for (int j = 0; j < 4; ++j) x[n][4 * v + j] = c[j] * scale;
+        }
+      const bool more = key + 32 < end;
+      if (more) {
+        if ((++tile & 31) == 0) at = tile_groups(a, table, h, key + 32, last_sub);
+        load_k<D, E4M3>(a, at, 2 * (tile & 31), k_lane, &cur);
       }
-      const int at = u.row0 + mine, tok = u.first + at / a.group, head = h * a.group + at % a.group;
-      if (alone) {
-        // a row that saw no key is zero
-        const float inv = sum > 0.0f || sum != sum ? v_scale / sum : 0.0f;
-        uint32_t w[DT / 2];
+      if (key + 32 > s.len) {  // the cache beyond the sequence may hold anything: 0 * NaN would reach every row
 #pragma unroll
-        for (int i = 0; i < DT / 2; ++i) w[i] = bf16_pair(acc[2 * i] * inv, acc[2 * i + 1] * inv);
-        uint8_t* out = a.out.p + (int64_t)tok * a.out.token + (int64_t)head * a.out.head + d0 * 2;
-        if constexpr (DT == 8)
-          *reinterpret_cast<u32x4*>(out) = u32x4{w[0], w[1], w[2], w[3]};
-        else
-          *reinterpret_cast<u32x2*>(out) = u32x2{w[0], w[1]};
-        if (a.lse && d0 == 0)
-          a.lse[(int64_t)tok * a.q_heads + head] = rt == kNegInf ? kNegInf : (rt + log2f(sum)) * 0.6931471805599453f;
-      } else {
-        const int64_t part = (unit * a.splits + split) * R + mine;
+        for (int j = 0; j < 8; ++j)
+          if (key + 16 * (j / 4) + 4 * g + j % 4 >= s.len)
 #pragma unroll
-        for (int i = 0; i < DT; ++i) acc[i] *= v_scale;
+            for (int w = 0; w < Tile::VW; ++w) cur.v[j][w] = 0u;
+      }
+      const bool whole = key >= full_lo && key + 32 <= full_hi;
+      u32x4 p[NR];
 #pragma unroll
-        for (int i = 0; i < DT; i += 4)
-          *reinterpret_cast<f32x4*>(a.part_o + part * D + d0 + i) = f32x4{acc[i], acc[i + 1], acc[i + 2], acc[i + 3]};
-        if (d0 == 0) {
-          a.part_ml[part * 2] = rt;
-          a.part_ml[part * 2 + 1] = sum;
+      for (int n = 0; n < NR; ++n) {
+        if (!whole) {
+          int first = key + 4 * g;
+          pin(first);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const int k = first + 16 * (j / 4) + j % 4;
+            x[n][j] = k >= lo[n] && k < hi[n] ? x[n][j] : kNegInf;
+          }
+        }
+        float top = x[n][0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) top = fmaxf(top, x[n][j]);
+        top = fmaxf(m[n], row4_max(top));
+        const float ref = top == kNegInf ? 0.0f : top;  // a row that has seen no key yet
+        const float keep = __builtin_amdgcn_exp2f(m[n] - ref);
+        m[n] = top;
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[n][j] = __builtin_amdgcn_exp2f(x[n][j] - ref);
+          sum += x[n][j];
+        }
+        l[n] = l[n] * keep + sum;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) p[n][j] = bf16_pair(x[n][2 * j], x[n][2 * j + 1]);
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) o[n][dt] *= keep;
+      }
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        const u32x4 v = v_operand<D, E4M3>(cur, dt);
+#pragma unroll
+        for (int n = 0; n < NR; ++n) o[n][dt] = mma_bf16(v, p[n], o[n][dt]);
+      }
+      if (more) load_v<D, E4M3>(a, at, 2 * (tile & 31), v_lane, &cur);
+    }
+
+    // the sequence's output if all of it lies in this slot, else this slot's
+    // share: number 0 if it is the slot's first sequence, else 1
+    const bool alone = t_stop - t == s.tiles;
+    const int64_t part = (((int64_t)slot * 2 + (t == t_begin ? 0 : 1)) * a.kv_heads + h) * R;
+#pragma unroll
+    for (int n = 0; n < NR; ++n) {
+      const int row = 16 * n + r;
+      const float sum = row4_sum(l[n]);
+      if (row < rows) {
+        const int tok = s.first + row / a.group, head = h * a.group + row % a.group;
+        const float f = alone ? (sum > 0.0f || sum != sum ? v_scale / sum : 0.0f) : v_scale;  // no key seen: zero
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int d0 = (4 * g + j) * DT;
+          float x[DT];
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) x[dt] = o[n][dt][j] * f;
+          if (alone) {
+            uint8_t* out = a.out.p + (int64_t)tok * a.out.token + (int64_t)head * a.out.head + d0 * 2;
+            if constexpr (DT == 8)
+              *reinterpret_cast<u32x4*>(out) = u32x4{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3]), bf16_pair(x[4], x[5]),
+                                                     bf16_pair(x[6], x[7])};
+            else
+              *reinterpret_cast<u32x2*>(out) = u32x2{bf16_pair(x[0], x[1]), bf16_pair(x[2], x[3])};
+          } else {
+#pragma unroll
+            for (int w = 0; w < DT; w += 4)
+              *reinterpret_cast<f32x4*>(a.part_o + (part + row) * D + d0 + w) = f32x4{x[w], x[w + 1], x[w + 2], x[w + 3]};
+          }
+        }
+        if (g == 0) {
+          if (!alone) {
+            a.part_ml[(part + row) * 2] = m[n];
+            a.part_ml[(part + row) * 2 + 1] = sum;
+          } else if (a.lse) {
+            a.lse[(int64_t)tok * a.q_heads + head] = m[n] == kNegInf ? kNegInf : (m[n] + log2f(sum)) * 0.6931471805599453f;
+          }
         }
       }
     }
+    t = t_stop;
   }
 }
 
-// Adds the chunks of a unit: one wave a row.  o = sum_c e_c o_c / sum_c e_c
-// l_c with e_c = exp(m_c - max m).  Rows whose unit had one chunk were
-// written by the attention kernel.
+// A running softmax sum: maximum (base 2), sum and 4 values of the output.
+struct Partial {
+  float m, l;
+  f32x4 x;
+  __device__ __forceinline__ void add(float m2, float l2, const f32x4& x2) {
+    const float top = fmaxf(m, m2), base = top == kNegInf ? 0.0f : top;
+    const float e = __builtin_amdgcn_exp2f(m - base), e2 = __builtin_amdgcn_exp2f(m2 - base);
+    m = top;
+    l = l * e + l2 * e2;
+    x = x * e + x2 * e2;
+  }
+};
+
+// Adds `n` partial results of one row, by WAVES waves.  Entry 0 lies at row
+// `first` of the partial results, entry c at second + (c - 1) step.  D/4 lanes
+// take an entry, 16 bytes each, four entries on their way at once: what this
+// costs is latency.
+template <int D, int WAVES>
+__device__ __forceinline__ void join_row(const AttnArgs& a, int64_t first, int64_t second, int64_t step, int n, int tok,
+                                         int head) {
+  constexpr int L = D / 4, P = 64 * WAVES / L;
+  const int id = WAVES == 1 ? threadIdx.x & 63 : threadIdx.x, d0 = id % L * 4;
+  Partial p = {kNegInf, 0.0f, {0.0f, 0.0f, 0.0f, 0.0f}};
+  for (int c = id / L; c < n; c += 4 * P) {
+    float m[4], l[4];
+    f32x4 x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int i = min(c + k * P, n - 1);
+      const int64_t at = i == 0 ? first : second + (int64_t)(i - 1) * step;
+      m[k] = a.part_ml[at * 2];
+      l[k] = a.part_ml[at * 2 + 1];
+      x[k] = *reinterpret_cast<const f32x4*>(a.part_o + at * D + d0);
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (c + k * P < n) p.add(m[k], l[k], x[k]);
+  }
+#pragma unroll
+  for (int s = L; s < 64; s *= 2) {
+    const float m = __shfl_xor(p.m, s, 64), l = __shfl_xor(p.l, s, 64);
+    f32x4 x;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = __shfl_xor(p.x[i], s, 64);
+    p.add(m, l, x);
+  }
+  if constexpr (WAVES > 1) {
+    __shared__ Partial shared[WAVES][L];
+    if ((id & 63) < L) shared[id >> 6][id & 63] = p;
+    __syncthreads();
+    if (id >= L) return;
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) p.add(shared[w][id].m, shared[w][id].l, shared[w][id].x);
+  }
+  const float inv = p.l > 0.0f || p.l != p.l ? 1.0f / p.l : 0.0f;
+  if (id < L)
+    *reinterpret_cast<u32x2*>(a.out.p + (int64_t)tok * a.out.token + (int64_t)head * a.out.head + d0 * 2) =
+        u32x2{bf16_pair(p.x[0] * inv, p.x[1] * inv), bf16_pair(p.x[2] * inv, p.x[3] * inv)};
+  if (a.lse && id == 0)
+    a.lse[(int64_t)tok * a.q_heads + head] = p.m == kNegInf ? kNegInf : (p.m + log2f(p.l)) * 0.6931471805599453f;
+}
+
 constexpr int kJoinWaves = 4;
 
+// The stream kernel's sequences that lie in several slots: WAVES waves a row.
+// grid.y: sequences; grid.x: rows of all KV heads.
+template <int D, int WAVES>
+__global__ void __launch_bounds__(kJoinWaves * 64) attn_stream_join_kernel(AttnArgs a, int R) {
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int id = WAVES == 1 ? (int)blockIdx.x * kJoinWaves + wave : blockIdx.x;
+  const int h = id % a.kv_heads, row = id / a.kv_heads, b = blockIdx.y;
+  Seq mine = {0, 0, 0, 0, 0};
+  int total = 0, seq_begin = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    const Seq s = seq_of(a, b0 + lane);
+    const int upto = inclusive_sum(s.tiles);
+    if (b >= b0 && b < b0 + 64) {
+      const int i = b - b0;
+      mine = Seq{lane_i32(s.first, i), lane_i32(s.n, i), 0, 0, lane_i32(s.tiles, i)};
+      seq_begin = total + lane_i32(upto, i) - mine.tiles;
+    }
+    total += lane_i32(upto, 63);
+  }
+  if (mine.tiles == 0 || row >= mine.n * a.group) return;
+  const Cut cut = cut_of(a, total);
+  const int s0 = cut.slot_of(seq_begin), s1 = cut.slot_of(seq_begin + mine.tiles - 1);
+  if (s0 == s1) return;  // written by the stream kernel
+  const int64_t step = (int64_t)a.kv_heads * R;
+  const int64_t first = ((int64_t)s0 * 2 + (seq_begin == cut.start(s0) ? 0 : 1)) * step + (int64_t)h * R + row;
+  join_row<D, WAVES>(a, first, (int64_t)(s0 + 1) * 2 * step + (int64_t)h * R + row, 2 * step, s1 - s0 + 1,
+                     mine.first + row / a.group, h * a.group + row % a.group);
+}
+
+// The tile kernel's units that were cut into chunks: one wave a row.
 template <int D>
 __global__ void __launch_bounds__(kJoinWaves * 64) attn_join_kernel(AttnArgs a, int R) {
-  constexpr int W = D / 64;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   int id = blockIdx.x;
   const int h = id % a.kv_heads;
   id /= a.kv_heads;
@@ -334,54 +476,55 @@ __global__ void __launch_bounds__(kJoinWaves * 64) attn_join_kernel(AttnArgs a, 
   id /= per;
   const int block = id % a.row_blocks, b = id / a.row_blocks;
   const Unit u = unit_of(a, b, block, R);
-  if (row >= u.rows || u.chunks <= 1 || u.all > a.max_rows || u.all < a.min_rows) return;
+  if (row >= u.rows || u.chunks <= 1 || u.all < a.min_rows) return;
   const int64_t unit = ((int64_t)b * a.row_blocks + block) * a.kv_heads + h;
-  const float* ml = a.part_ml + (unit * a.splits * R + row) * 2;
-  const int n = min(u.chunks, a.splits);
-  float top = kNegInf;
-  for (int c = lane; c < n; c += 64) top = fmaxf(top, ml[(int64_t)c * R * 2]);
-  for (int s = 32; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor(top, s, 64));
-  const float base = top == kNegInf ? 0.0f : top;
-  float sum = 0.0f, acc[W];
-#pragma unroll
-  for (int i = 0; i < W; ++i) acc[i] = 0.0f;
-  const float* po = a.part_o + (unit * a.splits * R + row) * D + lane * W;
-  for (int c = 0; c < n; ++c) {
-    const float e = __builtin_amdgcn_exp2f(ml[(int64_t)c * R * 2] - base);
-    sum = __fmaf_rn(e, ml[(int64_t)c * R * 2 + 1], sum);
-#pragma unroll
-    for (int i = 0; i < W; ++i) acc[i] = __fmaf_rn(e, po[(int64_t)c * R * D + i], acc[i]);
-  }
-  const int at = u.row0 + row, tok = u.first + at / a.group, head = h * a.group + at % a.group;
-  const float inv = sum > 0.0f || sum != sum ? 1.0f / sum : 0.0f;
-  uint8_t* out = a.out.p + (int64_t)tok * a.out.token + (int64_t)head * a.out.head + lane * W * 2;
-  if constexpr (W == 2)
-    *reinterpret_cast<uint32_t*>(out) = bf16_pair(acc[0] * inv, acc[1] * inv);
-  else
-    *reinterpret_cast<uint16_t*>(out) = (uint16_t)bf16_rne(acc[0] * inv);
-  if (a.lse && lane == 0)
-    a.lse[(int64_t)tok * a.q_heads + head] = top == kNegInf ? kNegInf : (top + log2f(sum)) * 0.6931471805599453f;
+  const int64_t first = unit * a.splits * R + row;
+  const int place = u.row0 + row;
+  join_row<D, 1>(a, first, first + R, R, min(u.chunks, a.splits), u.first + place / a.group,
+                 h * a.group + place % a.group);
 }
 
 template <int D, bool E4M3, int NR>
-static hipError_t launch_stream(const AttnArgs& a, int units, hipStream_t s) {
-  const unsigned grid = (unsigned)units * (unsigned)a.splits;
-  const size_t lds = (kStreamWaves * 16 * (D + 4) + kStreamWaves * NR * 16 * 2) * sizeof(float);
-  hipLaunchKernelGGL((attn_stream_kernel<D, E4M3, NR>), dim3(grid), dim3(kStreamWaves * 64), lds, s, a);
+static hipError_t launch_stream(const AttnArgs& a, hipStream_t s) {
+  const unsigned grid = (unsigned)(a.slots / (kStreamWaves / a.heads_wg)) * (unsigned)(a.kv_heads / a.heads_wg);
+  hipLaunchKernelGGL((attn_stream_kernel<D, E4M3, NR>), dim3(grid), dim3(kStreamWaves * 64), 0, s, a);
   return hipGetLastError();
 }
 
 template <int D, bool E4M3>
-static hipError_t launch_stream_d(const AttnArgs& a, int rows, int units, hipStream_t s) {
-  if (rows == 16) return launch_stream<D, E4M3, 1>(a, units, s);
-  if (rows == 32) return launch_stream<D, E4M3, 2>(a, units, s);
-  return launch_stream<D, E4M3, 4>(a, units, s);
+static hipError_t launch_stream_d(const AttnArgs& a, int rows, hipStream_t s) {
+  return rows == 16 ? launch_stream<D, E4M3, 1>(a, s) : launch_stream<D, E4M3, 2>(a, s);
 }
 
-hipError_t launch_attn_stream(const AttnArgs& a, int head_dim, bool e4m3, int rows, int units, hipStream_t s) {
+hipError_t launch_attn_stream(const AttnArgs& a, int head_dim, bool e4m3, int rows, hipStream_t s) {
+  if (head_dim == 64) return e4m3 ? launch_stream_d<64, true>(a, rows, s) : launch_stream_d<64, false>(a, rows, s);
+  return e4m3 ? launch_stream_d<128, true>(a, rows, s) : launch_stream_d<128, false>(a, rows, s);
+}
+
+int attn_stream_slots(int head_dim, bool e4m3, int rows, int kv_heads, int heads_wg) {
+  const int per_cu = stream_workgroups(head_dim, e4m3, rows / 16), head_groups = kv_heads / heads_wg;
+  const int workgroups = 256 * per_cu / head_groups / 8 * 8;  // of one group of heads; a multiple of the XCDs
+  return (workgroups < 8 ? 8 : workgroups) * (kStreamWaves / heads_wg);
+}
+
+template <int D>
+static void launch_stream_join(const AttnArgs& a, int rows, int most_rows, hipStream_t s) {
+  const unsigned all = (unsigned)(most_rows * a.kv_heads);
+  // sequences in more than 16 slots on average: a workgroup a row, else a wave
+  if (a.slots > 16 * a.batch)
+    hipLaunchKernelGGL((attn_stream_join_kernel<D, kJoinWaves>), dim3(all, (unsigned)a.batch), dim3(kJoinWaves * 64), 0, s,
+                       a, rows);
+  else
+    hipLaunchKernelGGL((attn_stream_join_kernel<D, 1>), dim3((all + kJoinWaves - 1) / kJoinWaves, (unsigned)a.batch),
+                       dim3(kJoinWaves * 64), 0, s, a, rows);
+}
+
+hipError_t launch_attn_stream_join(const AttnArgs& a, int head_dim, int rows, int most_rows, hipStream_t s) {
   if (head_dim == 64)
-    return e4m3 ? launch_stream_d<64, true>(a, rows, units, s) : launch_stream_d<64, false>(a, rows, units, s);
-  return e4m3 ? launch_stream_d<128, true>(a, rows, units, s) : launch_stream_d<128, false>(a, rows, units, s);
+    launch_stream_join<64>(a, rows, most_rows, s);
+  else
+    launch_stream_join<128>(a, rows, most_rows, s);
+  return hipGetLastError();
 }
 
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, int batch, hipStream_t s) {

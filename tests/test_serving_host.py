@@ -106,16 +106,22 @@ def test_attention_plan_facts():
         f = p.facts
         assert f["workspace_bytes"] == p.workspace_bytes
         return f
-    one = facts(batch=1, tokens=1, max_kv=100)
-    assert one["splits"] == 1 and one["workspace_bytes"] == 0
+    one = facts(batch=1, tokens=1, max_kv=32)
+    assert one["stream_rows"] == 16 and one["tile_rows"] == 0 and one["workspace_bytes"] == 0
     long = facts(batch=1, tokens=1, max_kv=100000)
-    assert long["splits"] * long["chunk"] >= 100000 and long["splits"] > 16
-    # partial outputs, maxima and sums of every chunk of every unit
-    assert long["workspace_bytes"] == 8 * long["splits"] * long["rows"] * (128 + 2) * 4
-    # a window bounds the keys of a unit, whatever the context
-    near = facts(batch=1, tokens=1, max_kv=100000, window=500)
-    assert near["splits"] * near["chunk"] < 2000
-    assert facts(batch=0)["workspace_bytes"] == 0
+    # two partial results a slot: outputs, maxima and sums of every row of every KV head
+    assert long["workspace_bytes"] == 2 * 8 * long["slots"] * 16 * (128 + 2) * 4
+    assert long == facts(batch=300, tokens=300, max_kv=5000)      # neither lengths nor batch enter
+    assert facts(batch=2, tokens=10, max_q=5)["stream_rows"] == 32 and facts(batch=1, tokens=8, max_q=8)["stream_rows"] == 32
+    chunk = facts(batch=1, tokens=9, max_q=9)
+    assert chunk["stream_rows"] == 0 and chunk["tile_rows"] == 128 and chunk["row_blocks"] == 1
+    both = facts(batch=3, tokens=200, max_q=190)                   # single tokens beside a chunk
+    assert both["stream_rows"] == 16 and both["tile_rows"] == 128 and both["row_blocks"] == 6
+    cut = facts(batch=1, tokens=64, max_q=64, max_kv=100000)
+    assert cut["splits"] * cut["chunk"] >= 100000 and cut["splits"] > 4
+    near = facts(batch=1, tokens=64, max_q=64, max_kv=100000, window=500)      # a window bounds a unit's keys
+    assert near["splits"] * near["chunk"] < 1000
+    assert facts(batch=0)["row_blocks"] == 0
 
 
 def run(plan, c=None, q=None, table=A, stride=1000, lens=A, cu=A, out=None, lse=None, ws=A):
