@@ -40,13 +40,15 @@ namespace {
 constexpr int64_t kMaxTokens = int64_t(1) << 24;
 constexpr int64_t kMaxStride = int64_t(1) << 40;  // elements
 
-ql_status check_rows(const ql_rows* r, const char* name, qlk::Rows* out) {
+ql_status check_rows(const ql_rows* r, const char* name, int64_t heads, qlk::Rows* out) {
   if (!r || !r->data) return fail(QL_E_INVALID, "%s is NULL", name);
   if (!aligned16(r->data)) return fail(QL_E_ALIGN, "%s is not 16-byte aligned", name);
   if (r->token_stride < 0 || r->head_stride < 0 || r->token_stride > kMaxStride || r->head_stride > kMaxStride)
     return fail(QL_E_INVALID, "%s strides must be in [0, 2^40]", name);
   if (r->token_stride % 8 || r->head_stride % 8)
     return fail(QL_E_ALIGN, "%s strides must be multiples of 8 elements", name);
+  if (r->head_stride * 2 * heads >= (int64_t(1) << 31))
+    return fail(QL_E_UNSUPPORTED, "%s heads span 2^31 bytes or more", name);
   *out = qlk::Rows{static_cast<uint8_t*>(r->data), r->token_stride * 2, r->head_stride * 2};
   return QL_OK;
 }
@@ -222,9 +224,9 @@ ql_status qlinear_qk_norm_rope(const ql_norm_rope* rule, int64_t tokens, int32_t
   ql_status st = check_rule(rule, tokens, q_heads, kv_heads, head_dim, positions, &a);
   if (st != QL_OK) return st;
   if (tokens == 0 || q_heads + kv_heads == 0) return QL_OK;
-  if (q_heads && ((st = check_rows(q, "q", &a.q)) != QL_OK || (st = check_rows(q_out, "q_out", &a.q_out)) != QL_OK))
+  if (q_heads && ((st = check_rows(q, "q", q_heads, &a.q)) != QL_OK || (st = check_rows(q_out, "q_out", q_heads, &a.q_out)) != QL_OK))
     return st;
-  if (kv_heads && ((st = check_rows(k, "k", &a.k)) != QL_OK || (st = check_rows(k_out, "k_out", &a.k_out)) != QL_OK))
+  if (kv_heads && ((st = check_rows(k, "k", a.kv_heads, &a.k)) != QL_OK || (st = check_rows(k_out, "k_out", a.kv_heads, &a.k_out)) != QL_OK))
     return st;
   hipError_t e = qlk::launch_heads(a, head_dim, false, false, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? QL_OK : hip_fail(e, "norm and rotation launch");
@@ -239,9 +241,9 @@ ql_status qlinear_qkv_append(const ql_norm_rope* rule, int64_t tokens, int32_t q
   st = check_rule(rule, tokens, q_heads, cache->kv_heads, cache->head_dim, positions, &a);
   if (st != QL_OK) return st;
   if (tokens == 0) return QL_OK;
-  if (q_heads && ((st = check_rows(q, "q", &a.q)) != QL_OK || (st = check_rows(q_out, "q_out", &a.q_out)) != QL_OK))
+  if (q_heads && ((st = check_rows(q, "q", q_heads, &a.q)) != QL_OK || (st = check_rows(q_out, "q_out", q_heads, &a.q_out)) != QL_OK))
     return st;
-  if ((st = check_rows(k, "k", &a.k)) != QL_OK || (st = check_rows(v, "v", &a.v)) != QL_OK) return st;
+  if ((st = check_rows(k, "k", a.kv_heads, &a.k)) != QL_OK || (st = check_rows(v, "v", a.kv_heads, &a.v)) != QL_OK) return st;
   if (!slots) return fail(QL_E_INVALID, "slots is NULL");
   if (!aligned(slots, 8)) return fail(QL_E_ALIGN, "slots is not 8-byte aligned");
   a.slots = slots;
@@ -314,7 +316,7 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
       cache->page_size != s.page_size)
     return fail(QL_E_INVALID, "the cache is not of the plan's type, heads, head_dim and page_size");
   if (s.batch == 0 || s.tokens == 0 || s.max_q == 0) return QL_OK;
-  if ((st = check_rows(q, "q", &a.q)) != QL_OK || (st = check_rows(out, "out", &a.out)) != QL_OK) return st;
+  if ((st = check_rows(q, "q", s.q_heads, &a.q)) != QL_OK || (st = check_rows(out, "out", s.q_heads, &a.out)) != QL_OK) return st;
   if (!page_table || !seq_lens || !cu_q) return fail(QL_E_INVALID, "page_table, seq_lens or cu_q is NULL");
   if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(lse, 4))
     return fail(QL_E_ALIGN, "page_table, seq_lens, cu_q and lse must be 4-byte aligned");
@@ -379,7 +381,7 @@ static int verify_slices(int64_t batch, int64_t vocab) {
 
 int64_t qlinear_verify_workspace_bytes(int64_t batch, int64_t vocab) {
   if (batch <= 0 || vocab <= 0) return 0;
-  return batch * verify_slices(batch, vocab) * 16;
+  return (batch * verify_slices(batch, vocab) * 8 + 15) / 16 * 16;
 }
 
 ql_status qlinear_verify_draft(int64_t batch, int64_t n_drafts, int64_t max_drafts, int64_t vocab,

@@ -71,7 +71,7 @@ struct VerifyArgs {
   const float* noise;     // [batch, vocab]
   int32_t* out_tokens;    // [batch, max_drafts + 1]
   int32_t* accepted;      // [batch]
-  uint64_t* part;         // [batch, slices, 2]
+  uint64_t* part;         // [batch, slices]
   int64_t n_drafts;       // rows of draft / tokens / uniforms
   int batch, vocab, max_drafts, slices;
 };

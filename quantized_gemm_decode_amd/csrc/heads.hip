@@ -15,16 +15,26 @@
 // of squares stays inside a 16-lane row of the wave, and a pair's other half
 // is one exchange away.  A lane keeps its 8 cosines and sines for every head
 // of its token: read per head they would be four times a row's own bytes.
-#include "attention_args.hpp"
+#include <algorithm>
+#include <type_traits>
+
+#include "attention_common.hpp"
 #include "quant_common.hpp"
 
 namespace qlk {
 
-// Sum over the L lanes that hold one row (L = 8, 16 or 32, aligned).
+// Sum over the L lanes that hold one row (L = 8, 16 or 32, aligned): lane
+// swaps inside 16 lanes (xor 1, xor 2, half-row mirror, row mirror).
 template <int L>
 __device__ __forceinline__ float row_sum(float v) {
-#pragma unroll
-  for (int o = 1; o < L; o *= 2) v += __shfl_xor(v, o, 64);
+  auto swap = [](float x, auto ctrl) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, false));
+  };
+  v += swap(v, std::integral_constant<int, 0xB1>());
+  v += swap(v, std::integral_constant<int, 0x4E>());
+  v += swap(v, std::integral_constant<int, 0x141>());
+  if (L >= 16) v += swap(v, std::integral_constant<int, 0x140>());
+  if (L >= 32) v += __shfl_xor(v, 16, 64);
   return v;
 }
 
@@ -37,34 +47,44 @@ __device__ __forceinline__ void unpack8(const u32x4& v, float* f) {
 }
 
 __device__ __forceinline__ u32x4 pack8(const float* f) {
-  u32x4 o;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) o[i] = bf16_rne(f[2 * i]) | (bf16_rne(f[2 * i + 1]) << 16);
-  return o;
+  return u32x4{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]), bf16_pair(f[6], f[7])};
 }
 
-// y / scale as E4M3, the quantizers' rule: the quotient clamped to +-448 and
-// rounded to nearest even; a NaN stays one.
-__device__ __forceinline__ uint32_t e4m3_pair(float a, float b, float s) {
-  const float qa = __fdiv_rn(a, s), qb = __fdiv_rn(b, s);
+// y / s as E4M3, the quantizers' rule: the quotient clamped to +-448 and
+// rounded to nearest even; a NaN stays one.  The quotient comes from the
+// rounded reciprocal with the exact remainder put right (div_fast), which
+// needs y within reach of the clamp and s a normal number with a normal
+// reciprocal; any other scale takes the division.
+__device__ __forceinline__ uint32_t e4m3_pair(float a, float b, float s, float r) {
+  const float reach = 512.0f * s;
+  const float qa = r != 0.0f ? div_fast(__builtin_amdgcn_fmed3f(a, -reach, reach), s, r) : __fdiv_rn(a, s);
+  const float qb = r != 0.0f ? div_fast(__builtin_amdgcn_fmed3f(b, -reach, reach), s, r) : __fdiv_rn(b, s);
   const uint32_t c = e4m3_pk2<false>(clamp448(qa), clamp448(qb), 0u) & 0xffffu;
-  return (qa != qa ? (c & 0xff00u) | 0x7fu : c) | (qb != qb ? 0x7f00u : 0u);
+  return (a != a ? (c & 0xff00u) | 0x7fu : c) | (b != b ? 0x7f00u : 0u);
 }
 
 __device__ __forceinline__ u32x2 e4m3_row8(const float* y, float s) {
-  u32x2 o = {e4m3_pair(y[0], y[1], s) | (e4m3_pair(y[2], y[3], s) << 16),
-             e4m3_pair(y[4], y[5], s) | (e4m3_pair(y[6], y[7], s) << 16)};
+  const float r = s >= FAST_DIV_MIN_SCALE && s <= 1.0f / FAST_DIV_MIN_SCALE ? __fdiv_rn(1.0f, s) : 0.0f;
+  u32x2 o = {e4m3_pair(y[0], y[1], s, r) | (e4m3_pair(y[2], y[3], s, r) << 16),
+             e4m3_pair(y[4], y[5], s, r) | (e4m3_pair(y[6], y[7], s, r) << 16)};
   return o;
 }
 
 constexpr int kHeadThreads = 256;
+constexpr int kHeadWaves = 4096;
+constexpr int kHeadRows = 4;  // rows a lane has on their way at once
 
-// Workgroup (t, part): token t, rows part*G + g, + G*gridDim.y ... of its
-// heads, G = 256 / L rows at a time.  Head order: queries, keys, values.
+// Wave (t, part) of tokens x parts: token t, rows part*G + g, + G*parts, ... of
+// its heads, G = 64 / L rows at a time.  Head order: queries, keys, values.
+// Many tokens: a wave has a whole token, so that its cosines, sines and
+// weights serve all heads; few: a token's rows over several waves.
 template <int D, bool APPEND, bool E4M3>
-__global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a) {
-  constexpr int L = D / 8, G = kHeadThreads / L;
-  const int t = blockIdx.x, lane = threadIdx.x % L;
+__global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a, int parts) {
+  constexpr int L = D / 8, G = 64 / L;
+  const int w = __builtin_amdgcn_readfirstlane((int)(blockIdx.x * (kHeadThreads / 64) + threadIdx.x / 64));
+  const int t = w / parts, part = w - t * parts;
+  if (t >= a.tokens) return;
+  const int lane = threadIdx.x % L;
   const int d0 = lane * 8;
   const int64_t pos = a.pos[t];
   const bool known = pos >= 0 && pos < a.max_pos;
@@ -78,8 +98,8 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a) {
     k_at = page * a.kc.page + at * a.kc.token;
     v_at = page * a.vc.page + at * a.vc.token;
   }
-  // this lane's cosines and sines; for the half-split pairs with the sign of
-  // its own side, so that y = n * cos + other * sin on either side
+  // y = inv (x A + x' B) with x' the pair's other half: A = w cos, B = w' sin
+  // with the sign of this lane's side, once a token for its queries and keys
   const int half = a.rot / 2;
   const bool turned = d0 < a.rot;
   float c[8], s[8];
@@ -111,66 +131,88 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a) {
       s[i] = 0.0f;
     }
   }
-  // a position outside the table has no rotation: its rows become NaN
-  // instead of a read out of the table's range
-  const float nan = __uint_as_float(0x7fc00000u);
+  if (!known && a.rot) {
+    // a position outside the table has no rotation: its rows become NaN
+    // instead of a read out of the table's range
+#pragma unroll
+    for (int i = 0; i < 8; ++i) c[i] = __uint_as_float(0x7fc00000u);
+  }
+  float A[2][8], B[2][8];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint16_t* weight = k ? a.k_w : a.q_w;
+    float mine[8], far[8];
+    if (weight) {
+      unpack8(*reinterpret_cast<const u32x4*>(weight + d0), mine);
+      unpack8(*reinterpret_cast<const u32x4*>(weight + other * 8), far);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      A[k][i] = weight ? mine[i] * c[i] : c[i];
+      B[k][i] = weight ? far[a.interleaved ? i ^ 1 : i] * s[i] : s[i];
+    }
+  }
+  const bool some = a.rot < D && !turned;  // values beyond the rotation: not even 0 times the partner
   const int rows = a.q_heads + (APPEND ? 2 : 1) * a.kv_heads;
-  for (int r = (int)blockIdx.y * G + (int)threadIdx.x / L; r < rows; r += G * (int)gridDim.y) {
-    const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + a.kv_heads;
-    const int h = is_q ? r : is_v ? r - a.q_heads - a.kv_heads : r - a.q_heads;
-    if (APPEND && !is_q && slot < 0) continue;  // whole rows: a row's lanes leave together
-    const Rows& in = is_q ? a.q : is_v ? a.v : a.k;
-    const u32x4 raw = *reinterpret_cast<const u32x4*>(in.p + t * in.token + h * in.head + d0 * 2);
-    float y[8];
-    unpack8(raw, y);
-    if (!is_v) {
-      const uint16_t* w = is_q ? a.q_w : a.k_w;
-      u32x4 far;
+  const int step = G * parts;
+  const uint8_t* in_q = a.q.p + t * a.q.token;
+  const uint8_t* in_k = a.k.p + t * a.k.token;
+  const uint8_t* in_v = a.v.p + t * a.v.token;
+  for (int r0 = part * G + (int)(threadIdx.x & 63) / L; r0 < rows; r0 += step * kHeadRows) {
+    u32x4 raw[kHeadRows];  // all rows of a round are on their way before the first is worked on
 #pragma unroll
-      for (int i = 0; i < 4; ++i) far[i] = (uint32_t)__shfl((int)raw[i], other, L);
-      float o[8];
-      unpack8(far, o);
-      if (w) {
-        float ss = 0.0f;
+    for (int i = 0; i < kHeadRows; ++i) {
+      const int r = r0 + i * step;
+      if (r >= rows) continue;
+      const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + a.kv_heads;
+      const int h = is_q ? r : is_v ? r - a.q_heads - a.kv_heads : r - a.q_heads;
+      const uint32_t at = (uint32_t)h * (uint32_t)(is_q ? a.q.head : is_v ? a.v.head : a.k.head) + d0 * 2;
+      raw[i] = *reinterpret_cast<const u32x4*>((is_q ? in_q : is_v ? in_v : in_k) + at);
+    }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __fmaf_rn(y[i], y[i], ss);
-        const float inv = rsqrtf(__fmaf_rn(row_sum<L>(ss), 1.0f / D, a.eps));
-        float wy[8], wo[8];
-        unpack8(*reinterpret_cast<const u32x4*>(w + d0), wy);
-        unpack8(*reinterpret_cast<const u32x4*>(w + other * 8), wo);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          y[i] = y[i] * inv * wy[i];
-          o[i] = o[i] * inv * wo[i];
-        }
-      }
-      if (turned) {
-        float z[8];
+    for (int i = 0; i < kHeadRows; ++i) {
+      const int r = r0 + i * step;
+      if (r >= rows) continue;  // a row's lanes leave together
+      const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + a.kv_heads;
+      const int h = is_q ? r : is_v ? r - a.q_heads - a.kv_heads : r - a.q_heads;
+      if (APPEND && !is_q && slot < 0) continue;
+      float y[8];
+      unpack8(raw[i], y);
+      if (!is_v) {
+        float o[8];
         if (a.interleaved) {
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = y[i] * c[i] + y[i ^ 1] * s[i];
+          for (int j = 0; j < 8; ++j) o[j] = y[j ^ 1];
         } else {
+          u32x4 far;
 #pragma unroll
-          for (int i = 0; i < 8; ++i) z[i] = y[i] * c[i] + o[i] * s[i];
+          for (int j = 0; j < 4; ++j) far[j] = (uint32_t)__shfl((int)raw[i][j], other, L);
+          unpack8(far, o);
+        }
+        float inv = 1.0f;
+        if (is_q ? a.q_w != nullptr : a.k_w != nullptr) {
+          float ss = 0.0f;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) ss = __fmaf_rn(y[j], y[j], ss);
+          inv = rsqrtf(__fmaf_rn(row_sum<L>(ss), 1.0f / D, a.eps));
         }
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = z[i];
+        for (int j = 0; j < 8; ++j) {
+          const float b = is_q ? B[0][j] : B[1][j], z = y[j] * (is_q ? A[0][j] : A[1][j]);
+          y[j] = inv * (some ? z : __fmaf_rn(o[j], b, z));
+        }
       }
-      if (!known && a.rot) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = nan;
+      if (is_q || !APPEND) {
+        const Rows& out = is_q ? a.q_out : a.k_out;
+        *reinterpret_cast<u32x4*>(out.p + t * out.token + (uint32_t)h * (uint32_t)out.head + d0 * 2) = pack8(y);
+      } else {
+        const Pages& to = is_v ? a.vc : a.kc;
+        uint8_t* at = to.p + (is_v ? v_at : k_at) + h * to.head;
+        if constexpr (E4M3)
+          *reinterpret_cast<u32x2*>(at + d0) = e4m3_row8(y, to.scale ? to.scale[h] : 1.0f);
+        else
+          *reinterpret_cast<u32x4*>(at + d0 * 2) = pack8(y);
       }
-    }
-    if (is_q || !APPEND) {
-      const Rows& out = is_q ? a.q_out : a.k_out;
-      *reinterpret_cast<u32x4*>(out.p + t * out.token + h * out.head + d0 * 2) = pack8(y);
-    } else {
-      const Pages& to = is_v ? a.vc : a.kc;
-      uint8_t* at = to.p + (is_v ? v_at : k_at) + h * to.head;
-      if constexpr (E4M3)
-        *reinterpret_cast<u32x2*>(at + d0) = e4m3_row8(y, to.scale ? to.scale[h] : 1.0f);
-      else
-        *reinterpret_cast<u32x4*>(at + d0 * 2) = pack8(y);
     }
   }
 }
@@ -178,16 +220,17 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a) {
 template <int D>
 static hipError_t launch_heads_d(const HeadArgs& a, bool append, bool e4m3, hipStream_t s) {
   const int rows = a.q_heads + (append ? 2 : 1) * a.kv_heads;
-  const int passes = (rows + kHeadThreads / (D / 8) - 1) / (kHeadThreads / (D / 8));
-  // few tokens: a token's rows over as many workgroups as it takes
-  const int parts = (int64_t)a.tokens * passes <= 1024 ? passes : 1;
-  const dim3 grid((unsigned)a.tokens, (unsigned)parts), block(kHeadThreads);
+  const int passes = (rows + 64 / (D / 8) - 1) / (64 / (D / 8));
+  // a few waves for each SIMD before a wave gets more than one pass
+  const int parts = std::max(1, std::min(passes, kHeadWaves / a.tokens));
+  const int waves = kHeadThreads / 64;
+  const dim3 grid((unsigned)(((int64_t)a.tokens * parts + waves - 1) / waves)), block(kHeadThreads);
   if (!append)
-    hipLaunchKernelGGL((heads_kernel<D, false, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((heads_kernel<D, false, false>), grid, block, 0, s, a, parts);
   else if (e4m3)
-    hipLaunchKernelGGL((heads_kernel<D, true, true>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((heads_kernel<D, true, true>), grid, block, 0, s, a, parts);
   else
-    hipLaunchKernelGGL((heads_kernel<D, true, false>), grid, block, 0, s, a);
+    hipLaunchKernelGGL((heads_kernel<D, true, false>), grid, block, 0, s, a, parts);
   return hipGetLastError();
 }
 

@@ -67,10 +67,55 @@ __device__ __forceinline__ uint64_t wave_max_u64(uint64_t v) {
   return v;
 }
 
-// Entry v of one slice: the best of the difference's and of p's own scores.
-__device__ __forceinline__ void take(float p, float q, float e, uint32_t v, bool diff, uint64_t* best, uint64_t* own) {
-  *own = max_u64(*own, score_key(p, e, v));
-  if (diff) *best = max_u64(*best, score_key(fmaxf(p - q, 0.0f), e, v));
+// Four binary32 values at a 4-byte aligned address: rows of an odd vocabulary
+// start anywhere.
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
+// The weights of one place: p, or what is left of it above q.
+struct Weights {
+  const float* p;
+  const float* q;  // null: nothing is subtracted but `certain`
+  int certain;     // a certain draft (q = 1), else -1
+  __device__ __forceinline__ float at(float p, float q, int v) const { return fmaxf(p - (v == certain ? 1.0f : q), 0.0f); }
+};
+
+// Best score of entries [v0, v1) of a row, over one workgroup's (or wave's)
+// `threads` threads.
+__device__ __forceinline__ uint64_t scan(const Weights& w, const float* e, int v0, int v1, int thread, int threads) {
+  constexpr int U = 2;
+  uint64_t best = 0;
+  int v = v0 + thread * 4;
+  for (; v + 4 * threads * (U - 1) + 4 <= v1; v += 4 * threads * U) {
+    f32x4u p[U], q[U], n[U];
+#pragma unroll
+    for (int i = 0; i < U; ++i) {
+      p[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4u*>(w.p + v + 4 * threads * i));
+      n[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4u*>(e + v + 4 * threads * i));
+      if (w.q) q[i] = __builtin_nontemporal_load(reinterpret_cast<const f32x4u*>(w.q + v + 4 * threads * i));
+    }
+#pragma unroll
+    for (int i = 0; i < U; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int at = v + 4 * threads * i + j;
+        best = max_u64(best, score_key(w.at(p[i][j], w.q ? q[i][j] : 0.0f, at), n[i][j], (uint32_t)at));
+      }
+  }
+  for (; v < v1; v += 4 * threads)
+    for (int at = v; at < v + 4 && at < v1; ++at)
+      best = max_u64(best, score_key(w.at(w.p[at], w.q ? w.q[at] : 0.0f, at), e[at], (uint32_t)at));
+  return best;
+}
+
+__device__ __forceinline__ Weights weights_of(const VerifyArgs& a, int64_t first, int n, int k, int b, bool diff) {
+  Weights w = {a.target + (first + k + b) * a.vocab, nullptr, -1};
+  if (diff && k < n) {  // rejected: the draft's row is subtracted
+    if (a.draft)
+      w.q = a.draft + (first + k) * a.vocab;
+    else
+      w.certain = a.tokens[first + k];
+  }
+  return w;
 }
 
 __global__ void __launch_bounds__(kVerifyThreads) verify_scan_kernel(VerifyArgs a) {
@@ -78,46 +123,32 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_scan_kernel(VerifyArgs 
   int64_t first;
   const int n = draft_range(a, b, &first);
   const int k = accepted_drafts(a, first, n, b);
-  const bool diff = k < n;  // rejected: the draft's row is subtracted
-  const float* p = a.target + (first + k + b) * a.vocab;
-  const float* q = diff && a.draft ? a.draft + (first + k) * a.vocab : nullptr;
-  const int certain = diff && !a.draft ? a.tokens[first + k] : -1;
-  const float* e = a.noise + (int64_t)b * a.vocab;
-  const int per = (a.vocab + a.slices - 1) / a.slices;
-  const int v0 = (int)blockIdx.x * per, v1 = v0 + per < a.vocab ? v0 + per : a.vocab;
-  uint64_t best = 0, own = 0;
-  for (int v = v0 + (int)threadIdx.x; v < v1; v += kVerifyThreads)
-    take(p[v], q ? q[v] : (v == certain ? 1.0f : 0.0f), e[v], (uint32_t)v, diff, &best, &own);
-  best = wave_max_u64(best);
-  own = wave_max_u64(own);
-  __shared__ uint64_t part[2][kVerifyThreads / 64];
-  if ((threadIdx.x & 63) == 0) {
-    part[0][threadIdx.x >> 6] = best;
-    part[1][threadIdx.x >> 6] = own;
-  }
+  const int per = ((a.vocab + a.slices - 1) / a.slices + 3) / 4 * 4;
+  const int v0 = min((int)blockIdx.x * per, a.vocab), v1 = min(v0 + per, a.vocab);
+  uint64_t best = wave_max_u64(scan(weights_of(a, first, n, k, b, true), a.noise + (int64_t)b * a.vocab, v0, v1,
+                                    threadIdx.x, kVerifyThreads));
+  __shared__ uint64_t part[kVerifyThreads / 64];
+  if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = best;
   __syncthreads();
-  if (threadIdx.x < 2) {
-    uint64_t m = 0;
-    for (int w = 0; w < kVerifyThreads / 64; ++w) m = max_u64(m, part[threadIdx.x][w]);
-    a.part[((int64_t)b * a.slices + blockIdx.x) * 2 + threadIdx.x] = m;
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kVerifyThreads / 64; ++w) best = max_u64(best, part[w]);
+    a.part[(int64_t)b * a.slices + blockIdx.x] = best;
   }
 }
 
 // One wave a sequence: the maximum over the slices, then the row of tokens.
 __global__ void __launch_bounds__(64) verify_pick_kernel(VerifyArgs a) {
   const int b = blockIdx.x, lane = threadIdx.x;
+  uint64_t best = 0;
+  for (int i = lane; i < a.slices; i += 64) best = max_u64(best, a.part[(int64_t)b * a.slices + i]);
   int64_t first;
   const int n = draft_range(a, b, &first);
   const int k = accepted_drafts(a, first, n, b);
-  uint64_t best = 0, own = 0;
-  for (int i = lane; i < a.slices; i += 64) {
-    best = max_u64(best, a.part[((int64_t)b * a.slices + i) * 2]);
-    own = max_u64(own, a.part[((int64_t)b * a.slices + i) * 2 + 1]);
-  }
   best = wave_max_u64(best);
-  own = wave_max_u64(own);
-  const uint64_t w = best ? best : own;
-  const int next = w ? (int)(0xffffffffu - (uint32_t)w) : 0;
+  // p - q nowhere positive (rounding alone): p itself, by this wave
+  if (best == 0 && k < n)
+    best = wave_max_u64(scan(weights_of(a, first, n, k, b, false), a.noise + (int64_t)b * a.vocab, 0, a.vocab, lane, 64));
+  const int next = best ? (int)(0xffffffffu - (uint32_t)best) : 0;
   for (int i = lane; i <= a.max_drafts; i += 64)
     a.out_tokens[(int64_t)b * (a.max_drafts + 1) + i] = i < k ? a.tokens[first + i] : i == k ? next : -1;
   if (lane == 0) a.accepted[b] = k;
