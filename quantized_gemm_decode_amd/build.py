@@ -1,7 +1,8 @@
 """Build libqlinear.so (the HIP kernels + C ABI) in-tree for gfx950.
 
 Every translation unit is compiled with hipcc in parallel, then linked into
-``quantized_gemm_decode_amd/libqlinear.so``.  Run ``python -m
+``quantized_gemm_decode_amd/libqlinear.so``; the serving operators' binding to torch
+tensors goes into ``_binding.so`` beside it.  Run ``python -m
 quantized_gemm_decode_amd.build`` (or ``__graft_entry__.build()``).
 """
 
@@ -16,6 +17,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libqlinear.so")
+BINDING = os.path.join(PKG, "_binding.so")
 
 SOURCES = ["quant.hip", "heads.hip", "attention_stream.hip", "attention_tile.hip", "verify.hip", "attention_api.cpp", "decode_fp8.hip", "decode_int8.hip", "decode_block.hip", "decode_mx.hip", "decode_mx4.hip", "tiled_fp8.hip",
            "tiled_int8.hip", "tiled_block.hip", "tiled_mx.hip", "tiled_mx4.hip", "stream_read.hip", "api.cpp"]
@@ -71,20 +73,54 @@ def _compile(src):
     return out
 
 
+def _compile_binding():
+    """The serving operators' binding: host code on torch's headers, its own object."""
+    from torch.utils import cpp_extension
+    import sysconfig
+    import torch
+    out = os.path.join(OBJ, "binding.o")
+    cmd = [hipcc(), "-x", "c++", "-D__HIP_PLATFORM_AMD__", "-DUSE_ROCM", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % torch._C._GLIBCXX_USE_CXX11_ABI, "-I" + os.path.join(ROOT, "include"),
+           "-I" + sysconfig.get_paths()["include"], "-Wno-unused-command-line-argument"]
+    rocm = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(hipcc()))), "include")
+    cmd += ["-isystem" + p for p in cpp_extension.include_paths() + [rocm]]
+    r = subprocess.run(cmd + ["-c", os.path.join(CSRC, "binding.cpp"), "-o", out], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("compile failed: binding.cpp\n%s\n%s" % (r.stdout, r.stderr))
+    return out
+
+
+def _link_binding(obj):
+    # torch's libraries are those the process has loaded (torch is imported first); ours lies beside the module
+    import torch
+    torch_lib = os.path.join(os.path.dirname(os.path.abspath(torch.__file__)), "lib")
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or hipcc(), "-shared", "-fPIC", "-o", BINDING + ".tmp", obj,
+           "-L" + PKG, "-lqlinear", "-L" + torch_lib, "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_hip",
+           "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("link failed: _binding.so\n%s\n%s" % (r.stdout, r.stderr))
+    os.replace(BINDING + ".tmp", BINDING)
+
+
 def build(verbose=False, jobs=None):
-    """Compile all sources and link the shared library; returns its path."""
+    """Compile all sources and link the shared library and the binding; returns the library's path."""
     os.makedirs(OBJ, exist_ok=True)
     jobs = jobs or min(len(SOURCES), max(1, min(16, os.cpu_count() or 1)))
     with cf.ThreadPoolExecutor(jobs) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, SOURCES))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     cmd = [hipcc(), "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp] + objs
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError("link failed: %s\n%s" % (r.stdout, r.stderr))
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     if verbose:
         print("built", LIB)
+        print("built", BINDING)
     return LIB
 
 

@@ -378,6 +378,47 @@ def test_attention_over_an_appended_cache():
     assert (np.abs(f64(out) - r["out"]) <= tol).all()
 
 
+def test_binding_refusals():
+    """Tensors that do not fit are refused by name before anything is launched;
+    the library's own refusals come as QLinearError."""
+    q, k, v, qw, kw = head_inputs(1, 4, 4, 2, 64, True)
+    pos, table = torch.zeros(4, dtype=torch.int64).cuda(), ql.rope_table(8, 64)
+    qo, ko = torch.zeros_like(q).contiguous(), torch.zeros_like(k).contiguous()
+
+    def norm(**kw_):
+        d = dict(q=q, k=k, positions=pos, cos_sin=table, q_out=qo, k_out=ko, q_weight=qw, k_weight=kw)
+        d.update(kw_)
+        return ql.qlinear_qk_norm_rope(*d.values())
+    for name, bad in (("q", q.float()), ("q", q.cpu()), ("k", k[:3]), ("q_out", qo[:, :3]), ("k_out", ko.transpose(0, 2)),
+                      ("positions", pos.int()), ("positions", pos[:3]), ("q_weight", qw[:60]), ("k_weight", kw.float()),
+                      ("cos_sin", table.double()), ("cos_sin", ql.rope_table(8, 128)), ("q", 3), ("q", q[0])):
+        with pytest.raises(ValueError, match=name):
+            norm(**{name: bad})
+    with pytest.raises(ql.QLinearError) as e:
+        norm(q=torch.zeros(4, 4, 72, dtype=BF16, device="cuda")[:, :, 4:68])    # 8 bytes off
+    assert e.value.status == 5
+    p = Problem(1, [1, 1], [900, 40], 4, 2, 64, 16, False)
+    plan = p.plan()
+    args = dict(plan=plan, q=p.q, cache=p.cache, page_table=p.table.cuda(), seq_lens=p.lens.cuda(), cu_q=p.cu.cuda(),
+                out=torch.zeros(2, 4, 64, dtype=BF16, device="cuda"), lse=None, workspace=plan.new_workspace())
+    for name, bad in (("q", p.q[:1]), ("page_table", p.table.cuda()[:, :50]), ("page_table", p.table.cuda().long()),
+                      ("seq_lens", p.lens.cuda()[:1]), ("cu_q", p.cu.cuda()[:2]), ("workspace", None),
+                      ("workspace", plan.new_workspace()[:-1]), ("out", args["out"].float()),
+                      ("lse", torch.zeros(7, device="cuda"))):
+        with pytest.raises(ValueError, match=name):
+            ql.qlinear_attention(*dict(args, **{name: bad}).values())
+    x = verify_inputs(1, [2, 1], 50)
+    dev = [None if t is None else (torch.from_numpy(t) if isinstance(t, np.ndarray) else t).cuda() for t in x]
+    out, acc = torch.zeros(2, 3, dtype=torch.int32).cuda(), torch.zeros(2, dtype=torch.int32).cuda()
+    ws = ql.verify_workspace(2, 50)
+    for i, name, bad in ((0, "target_probs", dev[0][:-1]), (1, "draft_probs", dev[1].half()), (3, "cu_drafts", dev[3][:2]),
+                         (4, "uniforms", dev[4][:2]), (5, "noise", dev[5][0])):
+        with pytest.raises(ValueError, match=name):
+            ql.qlinear_verify_draft(*dev[:i], bad, *dev[i + 1:], out, acc, ws)
+    with pytest.raises(ValueError, match="out_tokens"):
+        ql.qlinear_verify_draft(*dev, out[:1], acc, ws)
+
+
 # ------------------------------------------------------------------ draft verification
 
 def verify_inputs(seed, counts, vocab, spread=0.6, certain=False):
