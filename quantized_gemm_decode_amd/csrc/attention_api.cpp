@@ -168,14 +168,20 @@ int64_t tile_chunk(int64_t units, int64_t span) {
   return std::max<int64_t>(best, 64);
 }
 
+// The most keys that a unit's rows can see, from the 64-aligned start of
+// their window.
+int64_t tile_span(const ql_attention_shape& s) {
+  if (!s.window) return s.max_kv;
+  return std::min<int64_t>(s.max_kv, (int64_t)s.window + kTileRows / (s.q_heads / s.kv_heads) + 2 + 64);
+}
+
 // Cuts a batch into units of kTileRows rows and their keys into chunks.
 // `at`: free workspace.
 ql_status plan_tile(const ql_attention_shape& s, int64_t rows, int64_t at, Part* p) {
   const int64_t group = s.q_heads / s.kv_heads, R = kTileRows;
   const int64_t blocks = (rows + R - 1) / R;
   const int64_t units = s.batch * blocks * s.kv_heads;
-  // the keys a block of rows can see, from the 64-aligned start of its window
-  const int64_t span = s.window ? std::min<int64_t>(s.max_kv, (int64_t)s.window + R / group + 2 + 64) : s.max_kv;
+  const int64_t span = tile_span(s);
   const int64_t chunk = tile_chunk(units, span);
   const int64_t splits = std::max<int64_t>(1, (span + chunk - 1) / chunk);
   if (units * splits >= (int64_t(1) << 31) || units * R / 4 >= (int64_t(1) << 31))
@@ -278,9 +284,15 @@ ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan*
   if (!p) return fail(QL_E_INVALID, "out of host memory");
   p->shape = *s;
   const bool chunks = rows > kStreamRows;
-  // sequences of few rows among longer ones: a launch of their own, unless
-  // every sequence has max_q new tokens
-  const bool mixed = chunks && s->tokens < s->batch * s->max_q;
+  // Sequences of few rows among longer ones get a launch of their own where
+  // there can be many of them with long contexts: to the tile kernel each is a
+  // workgroup of mostly idle rows for each KV head.  By the (sequence, KV head,
+  // key) triples that this would take: 48 k (one chunk of 64 and 7 x 1,000) 39.9 us
+  // apart, 26.3 us together; 84 k (attend_mixed of perf/operators.py) 110.7 and
+  // 99.3; 240 k (4 x 128 and 60 x 500) 35.3 and 51.0; 448 k (256 and 15 x 4,000) 133
+  // and 188; 4 M (512 and 63 x 8,000) 497 and 1031.
+  const int64_t few = s->max_q > 0 ? s->batch - (s->tokens + s->max_q - 1) / s->max_q : 0;
+  const bool mixed = chunks && few * s->kv_heads * tile_span(*s) > 160000;
   p->tile_from = mixed ? kMixedRows + 1 : 0;
   if (!chunks || mixed) st = plan_stream(*s, mixed ? kMixedRows : rows, &p->stream);
   if (st == QL_OK && chunks) st = plan_tile(*s, rows, p->stream.end, &p->tile);
@@ -373,10 +385,10 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
 }
 
 // Slices of a vocabulary row: enough workgroups for the card with few
-// sequences, at least 1024 entries (4 a thread) each.
+// sequences, at least 1024 entries (4 a thread) each, at most kVerifySlice.
 static int verify_slices(int64_t batch, int64_t vocab) {
-  const int64_t most = std::max<int64_t>(1, vocab / 1024);
-  return (int)std::max<int64_t>(1, std::min<int64_t>(most, 1024 / std::max<int64_t>(1, batch)));
+  const int64_t most = std::max<int64_t>(1, vocab / 1024), least = (vocab + qlk::kVerifySlice - 8) / (qlk::kVerifySlice - 4);
+  return (int)std::max(least, std::min<int64_t>(most, 1024 / std::max<int64_t>(1, batch)));
 }
 
 int64_t qlinear_verify_workspace_bytes(int64_t batch, int64_t vocab) {

@@ -85,6 +85,9 @@ __host__ __device__ __forceinline__ int page_of(int sub, uint64_t magic) {
   return (int)(((uint64_t)(uint32_t)sub * magic) >> kPageMagicShift);
 }
 
+// Most entries of a vocabulary row that one workgroup of the verification takes.
+constexpr int kVerifySlice = 4096;
+
 hipError_t launch_heads(const HeadArgs& a, int head_dim, bool append, bool e4m3, hipStream_t s);
 // Slots of the stream kernel: as many as the card holds waves for each KV head.
 int attn_stream_slots(int head_dim, bool e4m3, int rows, int kv_heads, int heads_wg);

@@ -17,6 +17,10 @@ namespace qlk {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 
+// Four binary32 values at a 4-byte aligned address: rows of an odd vocabulary,
+// or a caller's table, start anywhere.
+typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
+
 constexpr float kNegInf = -__builtin_huge_valf();
 
 __device__ __forceinline__ f32x4 mma_bf16(u32x4 a, u32x4 b, f32x4 c) {

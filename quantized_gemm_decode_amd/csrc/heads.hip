@@ -13,8 +13,15 @@
 // for few tokens.  A row is held by head_dim/8 lanes, 8 values (16 bytes)
 // each, so a wave reads and writes whole rows in contiguous pieces, the sum
 // of squares stays inside a 16-lane row of the wave, and a pair's other half
-// is one exchange away.  A lane keeps its 8 cosines and sines for every head
-// of its token: read per head they would be four times a row's own bytes.
+// is one exchange away.  Norm weight and rotation are folded into two factors
+// a value, kept for all heads of a token by the wave that has the token: made
+// anew for every head they are most of the arithmetic, which then bounds it.
+// Two rows a lane are on their way while the two before are worked on.
+// Measured: 8,191 tokens of 40 + 8 heads of 128 (206 MB) 42.1 us, 4.9 TB/s, what a
+// large copy reaches here; 43.1 and 43.6 us with three and four rows ahead.
+// Append of 4,096 tokens of 32 + 2 x 8 heads as E4M3 (94 MB) 24.6 us, 3.8 TB/s:
+// with one token a wave 4,096 waves do not fill the card, and with half a token
+// each (27.1 us) the factors are made twice.
 #include <algorithm>
 #include <type_traits>
 
@@ -71,8 +78,25 @@ __device__ __forceinline__ u32x2 e4m3_row8(const float* y, float s) {
 }
 
 constexpr int kHeadThreads = 256;
-constexpr int kHeadWaves = 4096;
-constexpr int kHeadRows = 4;  // rows a lane has on their way at once
+constexpr int kHeadWaves = 4096;  // waves up to which a token's rows go to several
+constexpr int kHeadRows = 2;      // rows a lane has on their way at once
+
+// Requests a round of rows: kHeadRows of them, `step` apart.
+__device__ __forceinline__ void load_rows(u32x4 (&raw)[kHeadRows], int r0, int step, int rows, int first_k, int first_v,
+                                          const uint8_t* in_q, const uint8_t* in_k, const uint8_t* in_v, uint32_t head_q,
+                                          uint32_t head_k, uint32_t head_v, int d) {
+#pragma unroll
+  for (int i = 0; i < kHeadRows; ++i) {
+    const int r = r0 + i * step;
+    if (r >= rows) continue;
+    const bool is_q = r < first_k, is_v = r >= first_v;
+    const uint8_t* in = is_v ? in_v : in_k;
+    in = is_q ? in_q : in;
+    const uint32_t head = is_q ? head_q : is_v ? head_v : head_k;
+    const uint32_t h = (uint32_t)(r - (is_q ? 0 : is_v ? first_v : first_k));
+    raw[i] = *reinterpret_cast<const u32x4*>(in + h * head + d);
+  }
+}
 
 // Wave (t, part) of tokens x parts: token t, rows part*G + g, + G*parts, ... of
 // its heads, G = 64 / L rows at a time.  Head order: queries, keys, values.
@@ -86,7 +110,32 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a, int par
   if (t >= a.tokens) return;
   const int lane = threadIdx.x % L;
   const int d0 = lane * 8;
+  // a round of rows is on its way before the tables' values that it waits for
+  // (which hang on the position), later rounds while the one before is worked on
+  const int rows = a.q_heads + (APPEND ? 2 : 1) * a.kv_heads;
+  const int step = G * parts;
+  const uint8_t* in_q = a.q.p + t * a.q.token;
+  const uint8_t* in_k = a.k.p + t * a.k.token;
+  const uint8_t* in_v = a.v.p + t * a.v.token;
+  const uint32_t head_q = (uint32_t)a.q.head, head_k = (uint32_t)a.k.head, head_v = (uint32_t)a.v.head;
+  const int first_k = a.q_heads, first_v = a.q_heads + a.kv_heads;
+  u32x4 raw[kHeadRows];
+  int r0 = part * G + (int)(threadIdx.x & 63) / L;
+  const int half = a.rot / 2;
+  const bool turned = d0 < a.rot, low = d0 < half;
+  // the lane of a pair's other halves
+  const int other = !turned || a.interleaved ? lane : low ? lane + half / 8 : lane - half / 8;
   const int64_t pos = a.pos[t];
+  load_rows(raw, r0, step, rows, first_k, first_v, in_q, in_k, in_v, head_q, head_k, head_v, d0 * 2);
+  u32x4 weight[2][2] = {};
+  if (a.q_w) {
+    weight[0][0] = *reinterpret_cast<const u32x4*>(a.q_w + d0);
+    weight[0][1] = *reinterpret_cast<const u32x4*>(a.q_w + other * 8);
+  }
+  if (a.k_w) {
+    weight[1][0] = *reinterpret_cast<const u32x4*>(a.k_w + d0);
+    weight[1][1] = *reinterpret_cast<const u32x4*>(a.k_w + other * 8);
+  }
   const bool known = pos >= 0 && pos < a.max_pos;
   int64_t slot = -1;
   int64_t k_at = 0, v_at = 0;
@@ -100,28 +149,27 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a, int par
   }
   // y = inv (x A + x' B) with x' the pair's other half: A = w cos, B = w' sin
   // with the sign of this lane's side, once a token for its queries and keys
-  const int half = a.rot / 2;
-  const bool turned = d0 < a.rot;
   float c[8], s[8];
-  int other = lane;
   if (turned) {
     const float* row = a.table + (known ? pos : 0) * a.rot;
     if (a.interleaved) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        c[2 * i] = c[2 * i + 1] = row[d0 / 2 + i];
-        s[2 * i + 1] = row[half + d0 / 2 + i];
+        c[2 * i] = c[2 * i + 1] = (*reinterpret_cast<const f32x4u*>(row + d0 / 2))[i];
+        s[2 * i + 1] = (*reinterpret_cast<const f32x4u*>(row + half + d0 / 2))[i];
         s[2 * i] = -s[2 * i + 1];
       }
     } else {
-      const bool low = d0 < half;
       const int at = low ? d0 : d0 - half;
-      other = low ? lane + half / 8 : lane - half / 8;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        c[i] = row[at + i];
-        const float v = row[half + at + i];
-        s[i] = low ? -v : v;
+      for (int i = 0; i < 8; i += 4) {
+        const f32x4u x = *reinterpret_cast<const f32x4u*>(row + at + i);
+        const f32x4u z = *reinterpret_cast<const f32x4u*>(row + half + at + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          c[i + j] = x[j];
+          s[i + j] = low ? -z[j] : z[j];
+        }
       }
     }
   } else {
@@ -140,35 +188,30 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a, int par
   float A[2][8], B[2][8];
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
-    const uint16_t* weight = k ? a.k_w : a.q_w;
+    const bool given = (k ? a.k_w : a.q_w) != nullptr;
     float mine[8], far[8];
-    if (weight) {
-      unpack8(*reinterpret_cast<const u32x4*>(weight + d0), mine);
-      unpack8(*reinterpret_cast<const u32x4*>(weight + other * 8), far);
-    }
+    unpack8(weight[k][0], mine);
+    unpack8(weight[k][1], far);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      A[k][i] = weight ? mine[i] * c[i] : c[i];
-      B[k][i] = weight ? far[a.interleaved ? i ^ 1 : i] * s[i] : s[i];
+      A[k][i] = given ? mine[i] * c[i] : c[i];
+      B[k][i] = given ? far[a.interleaved ? i ^ 1 : i] * s[i] : s[i];
     }
   }
+  uint8_t* const out_q = a.q_out.p + t * a.q_out.token;
+  uint8_t* const out_k = a.k_out.p + t * a.k_out.token;
+  const uint32_t out_head_q = (uint32_t)a.q_out.head, out_head_k = (uint32_t)a.k_out.head;
+  uint8_t* const cache_k = a.kc.p + k_at;
+  uint8_t* const cache_v = a.vc.p + v_at;
+  const int64_t cache_head_k = a.kc.head, cache_head_v = a.vc.head;
+  const float *const scale_k = a.kc.scale, *const scale_v = a.vc.scale;
   const bool some = a.rot < D && !turned;  // values beyond the rotation: not even 0 times the partner
-  const int rows = a.q_heads + (APPEND ? 2 : 1) * a.kv_heads;
-  const int step = G * parts;
-  const uint8_t* in_q = a.q.p + t * a.q.token;
-  const uint8_t* in_k = a.k.p + t * a.k.token;
-  const uint8_t* in_v = a.v.p + t * a.v.token;
-  for (int r0 = part * G + (int)(threadIdx.x & 63) / L; r0 < rows; r0 += step * kHeadRows) {
-    u32x4 raw[kHeadRows];  // all rows of a round are on their way before the first is worked on
+  for (; r0 < rows; r0 += step * kHeadRows) {
+    u32x4 now[kHeadRows];
 #pragma unroll
-    for (int i = 0; i < kHeadRows; ++i) {
-      const int r = r0 + i * step;
-      if (r >= rows) continue;
-      const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + a.kv_heads;
-      const int h = is_q ? r : is_v ? r - a.q_heads - a.kv_heads : r - a.q_heads;
-      const uint32_t at = (uint32_t)h * (uint32_t)(is_q ? a.q.head : is_v ? a.v.head : a.k.head) + d0 * 2;
-      raw[i] = *reinterpret_cast<const u32x4*>((is_q ? in_q : is_v ? in_v : in_k) + at);
-    }
+    for (int i = 0; i < kHeadRows; ++i) now[i] = raw[i];
+    if (r0 + step * kHeadRows < rows)
+      load_rows(raw, r0 + step * kHeadRows, step, rows, first_k, first_v, in_q, in_k, in_v, head_q, head_k, head_v, d0 * 2);
 #pragma unroll
     for (int i = 0; i < kHeadRows; ++i) {
       const int r = r0 + i * step;
@@ -177,7 +220,7 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a, int par
       const int h = is_q ? r : is_v ? r - a.q_heads - a.kv_heads : r - a.q_heads;
       if (APPEND && !is_q && slot < 0) continue;
       float y[8];
-      unpack8(raw[i], y);
+      unpack8(now[i], y);
       if (!is_v) {
         float o[8];
         if (a.interleaved) {
@@ -186,7 +229,7 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a, int par
         } else {
           u32x4 far;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) far[j] = (uint32_t)__shfl((int)raw[i][j], other, L);
+          for (int j = 0; j < 4; ++j) far[j] = (uint32_t)__shfl((int)now[i][j], other, L);
           unpack8(far, o);
         }
         float inv = 1.0f;
@@ -203,13 +246,13 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a, int par
         }
       }
       if (is_q || !APPEND) {
-        const Rows& out = is_q ? a.q_out : a.k_out;
-        *reinterpret_cast<u32x4*>(out.p + t * out.token + (uint32_t)h * (uint32_t)out.head + d0 * 2) = pack8(y);
+        uint8_t* at = (is_q ? out_q : out_k) + (uint32_t)h * (is_q ? out_head_q : out_head_k) + d0 * 2;
+        *reinterpret_cast<u32x4*>(at) = pack8(y);
       } else {
-        const Pages& to = is_v ? a.vc : a.kc;
-        uint8_t* at = to.p + (is_v ? v_at : k_at) + h * to.head;
+        uint8_t* at = (is_v ? cache_v : cache_k) + (int64_t)h * (is_v ? cache_head_v : cache_head_k);
+        const float* scale = is_v ? scale_v : scale_k;
         if constexpr (E4M3)
-          *reinterpret_cast<u32x2*>(at + d0) = e4m3_row8(y, to.scale ? to.scale[h] : 1.0f);
+          *reinterpret_cast<u32x2*>(at + d0) = e4m3_row8(y, scale ? scale[h] : 1.0f);
         else
           *reinterpret_cast<u32x4*>(at + d0 * 2) = pack8(y);
       }
