@@ -543,7 +543,7 @@ typedef enum {
  * multiples of 16 bytes; 16-byte aligned).  page_size is a multiple of 16 up
  * to 8192; num_pages * page_size < 2^31; 16 token strides < 2^31 bytes.
  * E4M3 caches may carry one binary32 scale per KV head (device memory,
- * [kv_heads]; NULL = 1).
+ * [kv_heads], positive; NULL = 1).
  */
 typedef struct {
   void* k;
@@ -613,8 +613,10 @@ ql_status qlinear_qkv_append(const ql_norm_rope* rule, int64_t tokens, int32_t q
  * A row that sees nothing is 0 with lse -inf.  lse (binary32 [tokens,
  * q_heads], natural logarithm of the sum of exponentials) may be NULL.  Rows of
  * q outside [cu_q[0], cu_q[batch]) are not written.  What the cache holds
- * beyond a sequence's length may be anything, NaN included; page-table entries
- * beyond its pages are not read.  Memory safety does not depend on the device
+ * beyond a sequence's length may be anything, NaN included, and an infinity or
+ * NaN in a key or value never reaches a row that does not see it (a row that
+ * sees one gets non-finite outputs); page-table entries beyond a sequence's
+ * pages are not read.  Memory safety does not depend on the device
  * arrays: lengths are clamped to max_kv, pages to the cache, cu_q to
  * [0, tokens].
  *

@@ -276,7 +276,7 @@ ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan*
   if (st != QL_OK) return st;
   if (s->causal != 0 && s->causal != 1) return fail(QL_E_INVALID, "causal must be 0 or 1");
   if (s->window < 0 || (s->window && !s->causal)) return fail(QL_E_INVALID, "a window is >= 0 and causal");
-  if (!std::isfinite(s->scale)) return fail(QL_E_INVALID, "scale must be finite");
+  if (!std::isfinite(s->scale) || s->scale < 0.0f) return fail(QL_E_INVALID, "scale must be finite and >= 0");
   const int64_t group = s->q_heads / s->kv_heads;
   const int64_t rows = s->max_q * group;
   if (rows > (int64_t(1) << 30)) return fail(QL_E_UNSUPPORTED, "max_q * q_heads / kv_heads exceeds 2^30");
@@ -288,8 +288,8 @@ ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan*
   // there can be many of them with long contexts: to the tile kernel each is a
   // workgroup of mostly idle rows for each KV head.  By the (sequence, KV head,
   // key) triples that this would take: 48 k (one chunk of 64 and 7 x 1,000) 39.9 us
-  // apart, 26.3 us together; 84 k (attend_mixed of perf/operators.py) 110.7 and
-  // 99.3; 240 k (4 x 128 and 60 x 500) 35.3 and 51.0; 448 k (256 and 15 x 4,000) 133
+  // apart, 26.3 us together; 84 k (12 sequences, 701 new tokens in all, window
+  // 2048, heads of 64) 110.7 and 99.3; 240 k (4 x 128 and 60 x 500) 35.3 and 51.0; 448 k (256 and 15 x 4,000) 133
   // and 188; 4 M (512 and 63 x 8,000) 497 and 1031.
   const int64_t few = s->max_q > 0 ? s->batch - (s->tokens + s->max_q - 1) / s->max_q : 0;
   const bool mixed = chunks && few * s->kv_heads * tile_span(*s) > 160000;

@@ -137,4 +137,64 @@ __device__ __forceinline__ uint64_t pick(uint32_t lo, uint32_t hi, int i) {
          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, i) << 32;
 }
 
+// Sets the infinities and NaNs among 8 bf16 values to zero; true if there were any.
+__device__ __forceinline__ bool drop_nonfinite(u32x4& v) {
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const bool lo = (v[i] & 0x7f80u) == 0x7f80u, hi = (v[i] & 0x7f800000u) == 0x7f800000u;
+    v[i] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
+    any |= lo | hi;
+  }
+  return any;
+}
+
+// Infinities and NaNs in values that some rows see and others do not: in a
+// product a hidden value's weight is 0, and 0 * NaN would reach the rows that do
+// not see it.  So where a tile is hidden in part, they are dropped from the
+// product.  The stream kernel, which has the tile in registers, then makes a
+// second product of their places (1, else 0) with the rows' non-zero weights:
+// it tells which outputs they reach.
+__device__ __forceinline__ u32x4 nonfinite_places(const u32x4& v) {
+  u32x4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    x[i] = ((v[i] & 0x7f80u) == 0x7f80u ? 0x3f80u : 0u) | ((v[i] & 0x7f800000u) == 0x7f800000u ? 0x3f800000u : 0u);
+  return x;
+}
+__device__ __forceinline__ u32x4 nonzero_weights(const u32x4& p) {
+  u32x4 x;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) x[i] = ((p[i] & 0xffffu) ? 0x3f80u : 0u) | ((p[i] & 0xffff0000u) ? 0x3f800000u : 0u);
+  return x;
+}
+
+// The tile kernel, whose waves share the tile, reads the values again instead:
+// `seen(key, bad)` is called for each key of [key, key + n) with non-finite
+// values, bad[i] holding value d = 2 l + i (D = 64: l) in bit l.
+template <int D, bool E4M3, class F>
+__device__ __forceinline__ void for_nonfinite(const AttnArgs& a, const int32_t* table, int h, int key, int n, F seen) {
+  constexpr int W = D / 64;
+  const int lane = threadIdx.x & 63;
+  for (int k = key; k < key + n; ++k) {
+    const int col = page_of(k >> 4, a.page_magic);
+    const int64_t page = min((uint32_t)uniform_i32(table + col), (uint32_t)(a.num_pages - 1));
+    const uint8_t* p = a.vc.p + page * a.vc.page + (int64_t)(k - col * a.page_size) * a.vc.token + h * a.vc.head;
+    uint64_t bad[W];
+    bool any = false;
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const int d = lane * W + i;
+      bad[i] = __ballot(E4M3 ? (p[d] & 0x7f) == 0x7f : (reinterpret_cast<const uint16_t*>(p)[d] & 0x7f80) == 0x7f80);
+      any |= bad[i] != 0;
+    }
+    if (any) seen(k, bad);
+  }
+}
+
+template <int D>
+__device__ __forceinline__ bool bad_at(const uint64_t (&bad)[D / 64], int d) {
+  return D == 128 ? (bad[d & (D / 64 - 1)] >> (d >> 1)) & 1 : (bad[0] >> d) & 1;
+}
+
 }  // namespace qlk

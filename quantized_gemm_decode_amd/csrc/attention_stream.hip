@@ -320,11 +320,30 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[n][dt] *= keep;
       }
+      if (whole) {
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) {
-        const u32x4 v = v_operand<D, E4M3>(cur, dt);
+        for (int dt = 0; dt < DT; ++dt) {
+          const u32x4 v = v_operand<D, E4M3>(cur, dt);
 #pragma unroll
-        for (int n = 0; n < NR; ++n) o[n][dt] = mma_bf16(v, p[n], o[n][dt]);
+          for (int n = 0; n < NR; ++n) o[n][dt] = mma_bf16(v, p[n], o[n][dt]);
+        }
+      } else {
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt) {
+          const u32x4 all = v_operand<D, E4M3>(cur, dt);
+          u32x4 v = all;
+          const bool dropped = __any(drop_nonfinite(v));
+#pragma unroll
+          for (int n = 0; n < NR; ++n) {
+            o[n][dt] = mma_bf16(v, p[n], o[n][dt]);
+            if (dropped) {
+              const f32x4 hit = mma_bf16(nonfinite_places(all), nonzero_weights(p[n]), f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (hit[j] > 0.0f) o[n][dt][j] = __uint_as_float(0x7fc00000u);
+            }
+          }
+        }
       }
       if (more) load_v<D, E4M3>(a, at, 2 * (tile & 31), v_lane, &cur);
     }

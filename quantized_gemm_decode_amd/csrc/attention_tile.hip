@@ -119,10 +119,27 @@ __device__ __forceinline__ void store_k(const Staged<D, E4M3>& t, uint8_t* kl) {
   }
 }
 
+// drop_nonfinite for 16 E4M3 codes.
+__device__ __forceinline__ bool drop_nan_codes(u32x4& v) {
+  bool any = false;
+#pragma unroll
+  for (int w = 0; w < 4; ++w) {
+    uint32_t keep = 0xffffffffu;
+#pragma unroll
+    for (int i = 0; i < 32; i += 8)
+      if ((v[w] & (0x7fu << i)) == (0x7fu << i)) keep &= ~(0xffu << i);
+    any |= keep != 0xffffffffu;
+    v[w] &= keep;
+  }
+  return any;
+}
+
 // V rows of keys beyond the sequence are stored as zero: the cache there may
-// hold anything, and 0 * NaN would reach every row.
+// hold anything, and 0 * NaN would reach every row.  From a tile that is hidden
+// from some rows (`part`) infinities and NaNs are dropped; `mark` is then set
+// to `tile`.
 template <int D, bool E4M3>
-__device__ __forceinline__ void store_v(Staged<D, E4M3>& t, int key, int len, uint8_t* vl) {
+__device__ __forceinline__ void store_v(Staged<D, E4M3>& t, int key, int len, uint8_t* vl, bool part, int tile, int* mark) {
   using S = Staged<D, E4M3>;
   const int piece = threadIdx.x % S::CH;
   if (key + kTileKeys > len) {
@@ -131,20 +148,28 @@ __device__ __forceinline__ void store_v(Staged<D, E4M3>& t, int key, int len, ui
     for (int j = 0; j < S::PASSES; ++j)
       if (key + staged_row<D, E4M3>(j) >= len) t.x[j] = u32x4{0u, 0u, 0u, 0u};
   }
+  if (part) {
+    bool dropped = false;
+#pragma unroll
+    for (int j = 0; j < S::PASSES; ++j) {
+      pin(t.x[j]);
+      dropped |= E4M3 ? drop_nan_codes(t.x[j]) : drop_nonfinite(t.x[j]);
+    }
+    if (__any(dropped)) *mark = tile;
+  }
 #pragma unroll
   for (int j = 0; j < S::PASSES; ++j) {
     const int row = staged_row<D, E4M3>(j);
-    const u32x4 v = t.x[j];
-    if constexpr (E4M3) {
-      u32x4 x[2];
-      widen(v, &x[0], &x[1]);
+    constexpr int N = E4M3 ? 2 : 1;
+    u32x4 x[N];
+    if constexpr (E4M3)
+      widen(t.x[j], &x[0], &x[1]);
+    else
+      x[0] = t.x[j];
 #pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int c = 2 * piece + i;
-        *reinterpret_cast<u32x4*>(vl + row * D * 2 + v_block<D>(row, c / 4) * 64 + (c % 4) * 16) = x[i];
-      }
-    } else {
-      *reinterpret_cast<u32x4*>(vl + row * D * 2 + v_block<D>(row, piece / 4) * 64 + (piece % 4) * 16) = v;
+    for (int i = 0; i < N; ++i) {
+      const int c = N * piece + i;
+      *reinterpret_cast<u32x4*>(vl + row * D * 2 + v_block<D>(row, c / 4) * 64 + (c % 4) * 16) = x[i];
     }
   }
 }
@@ -275,6 +300,7 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs 
   constexpr int R = kTileRows, DT = D / 32, KS = D / 16;
   constexpr int kBytes = kTileKeys * D * 2;  // one tensor's tile
   __shared__ __align__(16) uint8_t k_lds[2][kBytes], v_lds[2][kBytes];
+  __shared__ int mark[2];  // 1 + the tile in v_lds[] that values were dropped from
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r = lane & 31, g = lane >> 5;
   int id = blockIdx.x;
@@ -356,11 +382,34 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs 
       }
     };
 
+    // whether tile T is hidden from some row
+    auto part = [&](int T) {
+      const int key = begin + T * kTileKeys;
+      return key < full_lo || key + kTileKeys > full_hi;
+    };
+    // outputs that values dropped from tile T would have reached
+    auto restore = [&](int T) {
+      if (!part(T) || mark[T & 1] != T + 1) return;
+      const int key = begin + T * kTileKeys;
+      for_nonfinite<D, E4M3>(a, table, h, key, min(kTileKeys, u.len - key), [&](int k, const uint64_t (&bad)[D / 64]) {
+        int g4 = 4 * g;
+        pin(g4);
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            if (k >= lo && k < hi && bad_at<D>(bad, 32 * dt + 8 * (i / 4) + g4 + i % 4))
+              o[dt][i] = __uint_as_float(0x7fc00000u);
+      });
+    };
+
     S staged;
+    if (threadIdx.x < 2) mark[threadIdx.x] = 0;
+    lds_barrier();
     load_k<D, E4M3>(a, at, 0, k_lane, &staged);
     store_k<D, E4M3>(staged, k_lds[0]);
     load_v<D, E4M3>(a, at, 0, v_lane, &staged);
-    store_v<D, E4M3>(staged, begin, u.len, v_lds[0]);
+    store_v<D, E4M3>(staged, begin, u.len, v_lds[0], part(0), 1, &mark[0]);
     if (tiles > 1) load_k<D, E4M3>(a, at, 1, k_lane, &staged);
     lds_barrier();
     u32x4 p0[2], p1[2];
@@ -380,11 +429,12 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs 
       const int key = begin + T * kTileKeys;
       const uint8_t* kl = k_lds[(T + 1) & 1];
       const uint8_t* vl = v_lds[T & 1];
+      restore(T);
       load_v<D, E4M3>(a, at, (T + 1) & 63, v_lane, &staged);
       mask(s1, key + 32);
       refer(s1, vl, 0, p0);
       inner_step<D>(kl, 0, vl, 0, q, s1, &w, p0, o, &s0, p1);
-      store_v<D, E4M3>(staged, key + kTileKeys, u.len, v_lds[(T + 1) & 1]);
+      store_v<D, E4M3>(staged, key + kTileKeys, u.len, v_lds[(T + 1) & 1], part(T + 1), T + 2, &mark[(T + 1) & 1]);
       if (T + 2 < tiles) {
         if (((T + 2) & 63) == 0) at = groups_at(a, table, h, ((key + 2 * kTileKeys) >> 4) + wave + 4 * lane, last_sub);
         load_k<D, E4M3>(a, at, (T + 2) & 63, k_lane, &staged);
@@ -396,6 +446,7 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs 
       lds_barrier();
     }
     const uint8_t* vl = v_lds[(tiles - 1) & 1];
+    restore(tiles - 1);
     mask(s1, begin + (tiles - 1) * kTileKeys + 32);
     refer(s1, vl, 0, p0);
     weights(s1, &w, p1);

@@ -293,6 +293,50 @@ def test_attention_plan_bounds_may_be_loose(max_q, max_kv):
     p.check(out, ls)
 
 
+def test_attention_batch_of_chunks_and_many_short_sequences():
+    """Sequences of few rows beside chunks, with contexts (by the plan's bound)
+    long enough that they get a launch of their own."""
+    new, kv = [40, 1, 9, 1, 3, 0, 1], [300, 1500, 700, 40, 65, 20, 1]
+    p = Problem(21, new, kv, 8, 2, 128, 16, True)
+    p.table = torch.nn.functional.pad(p.table, (0, 3750 - p.table.shape[1]), value=-7)
+    plan = p.plan(max_kv=60000)
+    assert plan.facts["stream_rows"] == 16 and plan.facts["tile_rows"] == 128
+    out, ls = p.run(plan)
+    p.check(out, ls)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new,kv,window", [(5, 70, 0), (40, 130, 0), (150, 200, 33), (7, 150, 40)])
+def test_non_finite_values_reach_only_rows_that_see_them(new, kv, window, D, e4m3):
+    """One infinite and some NaN entries of K and V at tokens that some new
+    tokens see: every other row stays as without them, to the bit."""
+    p = Problem(31, [new], [kv], 4, 2, D, 16, e4m3)
+    plan = p.plan(window=window)
+    clean, _ = p.run(plan)
+    bad_k, bad_v = kv - 2, kv - new // 2                    # K of the last token but one, V of one in the middle
+    nan = torch.tensor(float("nan")).to(p.k.dtype).cuda()
+    for x, at, head, dims in ((p.k, bad_k, 0, (5,)), (p.v, bad_v, 1, (3, D - 1))):
+        page = int(p.table[0, at // 16])
+        for d in dims:
+            x[page, at % 16, head, d] = nan if e4m3 or d != 3 else float("inf")
+    got, _ = p.run(plan)
+    pos = torch.arange(kv - new, kv)
+
+    def sees(at):
+        return (pos >= at) & ((pos - at < window) if window else True)
+    for t in range(new):
+        k_seen, v_seen = bool(sees(bad_k)[t]), bool(sees(bad_v)[t])
+        for h in range(4):
+            if h // 2 == 0:
+                assert torch.isnan(got[t, h]).all() if k_seen else torch.equal(got[t, h], clean[t, h]), (t, h)
+            else:
+                hit = torch.zeros(D, dtype=torch.bool, device="cuda")
+                hit[[3, D - 1]] = v_seen
+                assert not torch.isfinite(got[t, h][hit]).any(), (t, h)
+                assert torch.equal(got[t, h][~hit], clean[t, h][~hit]), (t, h)
+
+
 def test_attention_scale_and_rows_outside():
     """A given scale; rows of q that no sequence owns stay as they were."""
     p = Problem(6, [3, 2], [100, 50], 4, 2, 128, 16, False)

@@ -91,7 +91,7 @@ def test_attention_plan_refusals():
     assert plan_status() == OK and plan_status(batch=0) == OK and plan_status(max_kv=0) == OK
     for bad in (dict(batch=-1), dict(max_q=-1), dict(q_heads=30), dict(q_heads=0), dict(kv_heads=0), dict(kv_type=2),
                 dict(causal=2), dict(window=-1), dict(causal=0, window=5), dict(scale=float("inf")),
-                dict(scale=float("nan"))):
+                dict(scale=float("nan")), dict(scale=-0.1)):
         assert plan_status(**bad) == INVALID, bad
     for bad in (dict(head_dim=96), dict(head_dim=256), dict(page_size=8), dict(page_size=40), dict(max_kv=(1 << 30) + 1),
                 dict(tokens=(1 << 24) + 1), dict(batch=65537)):
@@ -115,8 +115,9 @@ def test_attention_plan_facts():
     assert facts(batch=2, tokens=10, max_q=5)["stream_rows"] == 32 and facts(batch=1, tokens=8, max_q=8)["stream_rows"] == 32
     chunk = facts(batch=1, tokens=9, max_q=9)
     assert chunk["stream_rows"] == 0 and chunk["tile_rows"] == 128 and chunk["row_blocks"] == 1
-    both = facts(batch=3, tokens=200, max_q=190)                   # single tokens beside a chunk
+    both = facts(batch=3, tokens=200, max_q=190, max_kv=100000)    # single tokens with long contexts beside a chunk
     assert both["stream_rows"] == 16 and both["tile_rows"] == 128 and both["row_blocks"] == 6
+    assert facts(batch=3, tokens=200, max_q=190)["stream_rows"] == 0           # with short ones: one launch
     cut = facts(batch=1, tokens=64, max_q=64, max_kv=100000)
     assert cut["splits"] * cut["chunk"] >= 100000 and cut["splits"] > 4
     near = facts(batch=1, tokens=64, max_q=64, max_kv=100000, window=500)      # a window bounds a unit's keys
