@@ -23,6 +23,10 @@ typedef float f32x4u __attribute__((ext_vector_type(4), aligned(4)));
 
 constexpr float kNegInf = -__builtin_huge_valf();
 
+// How far (base 2) a new maximum exceeds the one that a row's weights refer to
+// before that moves: weights stay below 2^8, exact in relative terms.
+constexpr float kRescaleAt = 8.0f;
+
 __device__ __forceinline__ f32x4 mma_bf16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
 }

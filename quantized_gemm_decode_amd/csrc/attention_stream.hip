@@ -30,6 +30,9 @@
 //     (whole rows of V per 16 lanes), and the 8 x D/16 transposition into
 //     operands stays inside the lane (one byte permutation per two values).
 //     So output value d sits in operand row d / (D/16) of product d % (D/16).
+// The maximum that a row's weights refer to moves where a new one exceeds it by
+// more than 8 (in base 2): its tests need no exchange between lanes, and most
+// tiles leave the outputs as they are.
 // P is rounded to bf16 for the product (its error, 2^-8 of a term at most,
 // averages out below the output's own rounding); the row sums take P in
 // binary32 before that, and all sums and maxima are binary32.
@@ -159,10 +162,10 @@ __device__ __forceinline__ u32x4 v_operand(const KvTile<D, E4M3>& t, int dt) {
   u32x4 o;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    if constexpr (E4M3) {
+    if constexpr (E4M3) {  // the same permutation serves products dt and dt ^ 1
       const uint32_t c = __builtin_amdgcn_perm(t.v[2 * i + 1][dt / 4], t.v[2 * i][dt / 4],
-                                               0x0c0c0000u | (uint32_t)((dt % 4) | ((4 + dt % 4) << 8)));
-      o[i] = e4m3_to_bf16<false>(c);
+                                               dt % 4 < 2 ? 0x05010400u : 0x07030602u);
+      o[i] = dt % 2 ? e4m3_to_bf16<true>(c) : e4m3_to_bf16<false>(c);
     } else {
       o[i] = __builtin_amdgcn_perm(t.v[2 * i + 1][dt / 2], t.v[2 * i][dt / 2], dt % 2 ? 0x07060302u : 0x05040100u);
     }
@@ -175,15 +178,23 @@ __device__ __forceinline__ u32x4 v_operand(const KvTile<D, E4M3>& t, int dt) {
 // heads: 30.1 and 31.3 us); 64 sequences of 4,003 .. 16,001, E4M3: 232.9 and
 // 210.9 us (64-wide: 27.9 and 22.3 us).  More requests on their way than that
 // only queue; E4M3's are half as large.  With 32 rows the sums of 128-wide heads
-// leave one workgroup its registers (E4M3: 51.5 us, 60.3 us squeezed into two;
-// 64-wide: 35.6 and 31.2 us).
+// leave one workgroup its registers (E4M3, 32 sequences of 4,000 keys: 68 us, 97
+// us squeezed into two; 64-wide: 35.6 and 31.2 us).
 constexpr int stream_workgroups(int D, bool e4m3, int row_tiles) { return e4m3 && (row_tiles == 1 || D == 64) ? 2 : 1; }
+
+// Tiles that a wave has in its registers: a compute unit's only workgroup asks
+// for a second one while it works on the first (32 sequences of 5 x 4 rows and
+// 4,000 keys, with one and two: E4M3 72.2 and 68.4 us, 64-wide bf16 56.9 and
+// 54.7); where there are two, they cover each other (64-wide E4M3, single
+// tokens, 8,000 keys: 52.0 and 55.0 us).
+constexpr int stream_depth(int D, bool e4m3, int row_tiles) { return stream_workgroups(D, e4m3, row_tiles) == 1 ? 2 : 1; }
 
 template <int D, bool E4M3, int NR>
 __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, NR)) attn_stream_kernel(AttnArgs a) {
   constexpr int R = 16 * NR, DT = D / 16;
   constexpr int KS = D / 32;  // products over D of one 16-key group
   using Tile = KvTile<D, E4M3>;
+  constexpr int DEPTH = stream_depth(D, E4M3, NR);
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int head_groups = a.kv_heads / a.heads_wg;
@@ -249,22 +260,26 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
     const int full_hi = a.causal ? min(s.len, max(0, pos0 + 1)) : s.len;
 
     f32x4 o[NR][DT];
-    float m[NR], l[NR];
+    float m[NR], l[NR], base[NR];
 #pragma unroll
     for (int n = 0; n < NR; ++n) {
       m[n] = kNegInf;
-      l[n] = 0.0f;
+      l[n] = base[n] = 0.0f;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) o[n][dt] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // K of the next tile is on its way while the weights and sums of this one
-    // are made, V while the next one's scores are: one set of registers each
-    int tile = 0;
-    Tile cur;
-    load_k<D, E4M3>(a, at, 0, k_lane, &cur);
-    load_v<D, E4M3>(a, at, 0, v_lane, &cur);
-    for (; key < end; key += 32) {
+    // K of a later tile is on its way while the weights and sums of this one
+    // are made, V while the next one's scores are
+    int tile = DEPTH - 1;
+    Tile ahead[DEPTH];
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i)
+      if (i == 0 || key + 32 * i < end) {
+        load_k<D, E4M3>(a, at, 2 * i, k_lane, &ahead[i]);
+        load_v<D, E4M3>(a, at, 2 * i, v_lane, &ahead[i]);
+      }
+    auto step = [&](Tile& cur) {
       float x[NR][8];
 #pragma unroll
       for (int v = 0; v < 2; ++v)
@@ -274,11 +289,11 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
 #pragma unroll
           for (int k = 0; k < KS; ++k) c = mma_bf16(k_operand<D, E4M3>(cur, v, k), q[n][k], c);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) x[n][4 * v + j] = c[j] * scale;
+          for (int j = 0; j < 4; ++j) x[n][4 * v + j] = c[j];
         }
-      const bool more = key + 32 < end;
+      const bool more = key + 32 * DEPTH < end;
       if (more) {
-        if ((++tile & 31) == 0) at = tile_groups(a, table, h, key + 32, last_sub);
+        if ((++tile & 31) == 0) at = tile_groups(a, table, h, key + 32 * DEPTH, last_sub);
         load_k<D, E4M3>(a, at, 2 * (tile & 31), k_lane, &cur);
       }
       if (key + 32 > s.len) {  // the cache beyond the sequence may hold anything: 0 * NaN would reach every row
@@ -304,21 +319,25 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
         float top = x[n][0];
 #pragma unroll
         for (int j = 1; j < 8; ++j) top = fmaxf(top, x[n][j]);
-        top = fmaxf(m[n], row4_max(top));
-        const float ref = top == kNegInf ? 0.0f : top;  // a row that has seen no key yet
-        const float keep = __builtin_amdgcn_exp2f(m[n] - ref);
-        m[n] = top;
+        top *= scale;
+        if (__any(top > m[n] + kRescaleAt)) {
+          top = fmaxf(m[n], row4_max(top));
+          base[n] = top == kNegInf ? 0.0f : top;  // a row that has seen no key yet
+          const float keep = __builtin_amdgcn_exp2f(m[n] - base[n]);
+          m[n] = top;
+          l[n] *= keep;
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) o[n][dt] *= keep;
+        }
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          x[n][j] = __builtin_amdgcn_exp2f(x[n][j] - ref);
+          x[n][j] = __builtin_amdgcn_exp2f(__fmaf_rn(x[n][j], scale, -base[n]));
           sum += x[n][j];
         }
-        l[n] = l[n] * keep + sum;
+        l[n] += sum;
 #pragma unroll
         for (int j = 0; j < 4; ++j) p[n][j] = bf16_pair(x[n][2 * j], x[n][2 * j + 1]);
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) o[n][dt] *= keep;
       }
       if (whole) {
 #pragma unroll
@@ -346,6 +365,14 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
         }
       }
       if (more) load_v<D, E4M3>(a, at, 2 * (tile & 31), v_lane, &cur);
+    };
+    while (key < end) {
+#pragma unroll
+      for (int i = 0; i < DEPTH; ++i)
+        if (key < end) {
+          step(ahead[i]);
+          key += 32;
+        }
     }
 
     // the sequence's output if all of it lies in this slot, else this slot's

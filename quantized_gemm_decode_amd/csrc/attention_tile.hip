@@ -24,6 +24,11 @@
 // exceeds it by more than 8 (in base 2): weights then stay below 2^8, exact in
 // relative terms, and the outputs need no rescaling for most tiles.
 //
+// Values that some rows do not see: 0 * NaN would reach them.  A tile that is
+// hidden in part loses its infinities and NaNs on the way into LDS; where there
+// were any (none, as a rule), the outputs that they reach are found by reading
+// the values again.
+//
 // Measured on MI355X, 2048 new tokens at the end of 10,240 cached ones, 32 / 8
 // heads of 128: 353 us, 877 TFLOP/s of the visible pairs' flops, against 1140-
 // 1380 that a large library product reaches here.  With the exponentials, the
@@ -39,7 +44,6 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kTileKeys = 64;
 constexpr int kTileWaves = 4;
 constexpr int kTileRows = kTileWaves * 32;
-constexpr float kRescaleAt = 8.0f;
 
 __device__ __forceinline__ f32x16 mma32(u32x4 a, u32x4 b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
