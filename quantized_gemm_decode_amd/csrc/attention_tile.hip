@@ -6,7 +6,7 @@
 //
 // 4 D flops a row and key: with hundreds of rows bound by the matrix cores.
 // Four waves share tiles of 64 keys in LDS; each holds 32 rows of Q and of the
-// output in registers, two workgroups a compute unit.  Products are 32x32x16
+// output in registers, two or three workgroups a compute unit.  Products are 32x32x16
 // bf16 (lane l = 32 g + r):
 //   S^T = K Q^T: a lane ends with 16 of 32 keys of one row, so maximum and
 //     sum of a row are in-lane, with one exchange between the lane halves;
@@ -30,11 +30,17 @@
 // the values again.
 //
 // Measured on MI355X, 2048 new tokens at the end of 10,240 cached ones, 32 / 8
-// heads of 128: 353 us, 877 TFLOP/s of the visible pairs' flops, against 1140-
+// heads of 128: 344 us, 900 TFLOP/s of the visible pairs' flops, against 1140-
 // 1380 that a large library product reaches here.  With the exponentials, the
 // LDS reads or the staging left out it is 1, 3 or 13 % faster, with all of
 // them 33 %: no single part bounds it, the products' own rate does at last.
+// (Nor the tests of the reference maximum: made behind the products instead of
+// ahead of the weights, 344 us.)  64-wide heads have half the products for the
+// same weights, and the vector unit bounds them: 512 new tokens of each of 4
+// sequences of 2,000, bf16: 55 us, 529 TFLOP/s.
 #include "attention_common.hpp"
+
+#include <type_traits>
 
 namespace qlk {
 
@@ -140,13 +146,12 @@ __device__ __forceinline__ bool drop_nan_codes(u32x4& v) {
 
 // V rows of keys beyond the sequence are stored as zero: the cache there may
 // hold anything, and 0 * NaN would reach every row.  From a tile that is hidden
-// from some rows (`part`) infinities and NaNs are dropped; `mark` is then set
-// to `tile`.
+// from some rows (`part`) infinities and NaNs are dropped; `mark` is then set.
 template <int D, bool E4M3>
-__device__ __forceinline__ void store_v(Staged<D, E4M3>& t, int key, int len, uint8_t* vl, bool part, int tile, int* mark) {
+__device__ __forceinline__ void store_v(Staged<D, E4M3>& t, int key, int len, uint8_t* vl, bool part, int* mark) {
   using S = Staged<D, E4M3>;
   const int piece = threadIdx.x % S::CH;
-  if (key + kTileKeys > len) {
+  if (part && key + kTileKeys > len) {
     pin(key);
 #pragma unroll
     for (int j = 0; j < S::PASSES; ++j)
@@ -159,7 +164,7 @@ __device__ __forceinline__ void store_v(Staged<D, E4M3>& t, int key, int len, ui
       pin(t.x[j]);
       dropped |= E4M3 ? drop_nan_codes(t.x[j]) : drop_nonfinite(t.x[j]);
     }
-    if (__any(dropped)) *mark = tile;
+    if (__any(dropped)) *mark = 1;
   }
 #pragma unroll
   for (int j = 0; j < S::PASSES; ++j) {
@@ -299,12 +304,17 @@ __device__ __forceinline__ void inner_step(const uint8_t* kl, int kt, const uint
   if (D == 128) __builtin_amdgcn_s_setprio(0);
 }
 
+// Workgroups a compute unit gets: what the registers allow.  (64-wide E4M3, 12
+// sequences with 4,327 new tokens, window 2048: 101 us with three, 109 us with two;
+// 64-wide bf16 and 128-wide heads do not fit three.)
+constexpr int tile_workgroups(int D, bool e4m3) { return D == 64 && e4m3 ? 3 : 2; }
+
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D, E4M3)) attn_tile_kernel(AttnArgs a) {
   constexpr int R = kTileRows, DT = D / 32, KS = D / 16;
   constexpr int kBytes = kTileKeys * D * 2;  // one tensor's tile
   __shared__ __align__(16) uint8_t k_lds[2][kBytes], v_lds[2][kBytes];
-  __shared__ int mark[2];  // 1 + the tile in v_lds[] that values were dropped from
+  __shared__ int dropped;  // values were, from a tile hidden in part
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r = lane & 31, g = lane >> 5;
   int id = blockIdx.x;
@@ -320,13 +330,17 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs 
   const int end = min(u.hi, begin + a.chunk);
   const int tiles = end > begin ? (end - begin + kTileKeys - 1) / kTileKeys : 0;
 
-  const int row = wave * 32 + r;
-  const int place = u.row0 + row, tok = u.first + place / a.group, head = h * a.group + place % a.group;
-  int lo, hi;
-  row_range(a, u, row, &lo, &hi);
-  if (row >= u.rows) lo = hi = 0;
+  // this lane's row, and what follows from it, is worked out again where it is
+  // used: kept through the loop its registers cost 64-wide heads a workgroup
+  auto own_row = [&]() {
+    int x = wave * 32 + r;
+    pin(x);
+    return x;
+  };
+  int row = own_row(), place = u.row0 + row;
   u32x4 q[KS];
   {
+    const int tok = u.first + place / a.group, head = h * a.group + place % a.group;
     const uint8_t* p = a.q.p + (int64_t)tok * a.q.token + (int64_t)head * a.q.head + g * 16;
 #pragma unroll
     for (int s = 0; s < KS; ++s)
@@ -345,7 +359,6 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs 
     row_range(a, u, u.rows - 1, &full_lo, &x);
     row_range(a, u, 0, &x, &full_hi);
     full_hi = min(full_hi, end);
-    hi = min(hi, end);
     const int32_t* table = a.table + b * a.table_row;
     const int last_sub = (u.len - 1) >> 4;
     using S = Staged<D, E4M3>;
@@ -354,11 +367,17 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs 
     // places of 64 tiles' groups at a time; K runs a tile ahead of V
     Groups at = groups_at(a, table, h, (begin >> 4) + wave + 4 * lane, last_sub);
 
+    auto own_range = [&](int* lo, int* hi) {
+      const int x = own_row();
+      row_range(a, u, x, lo, hi);
+      *hi = x < u.rows ? min(*hi, end) : 0;
+    };
     // masks the scores of keys [key, key + 32) where some row does not see all of them
     auto mask = [&](f32x16& s, int key) {
       if (key < full_lo || key + 32 > full_hi) {
-        int first = key + 4 * g;
+        int first = key + 4 * g, lo, hi;
         pin(first);
+        own_range(&lo, &hi);
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = first + 8 * (i / 4) + i % 4;
@@ -372,8 +391,9 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs 
       float top = s[0];
 #pragma unroll
       for (int i = 1; i < 16; ++i) top = fmaxf(top, s[i]);
-      top = half_max(top) * w.scale;
+      top *= w.scale;
       if (__any(top > w.m + kRescaleAt)) {
+        top = half_max(top);
         if (vl) pv<D>(vl, t, p, o);
         p[0] = p[1] = u32x4{0u, 0u, 0u, 0u};
         const float now = fmaxf(w.m, top);
@@ -391,29 +411,13 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs 
       const int key = begin + T * kTileKeys;
       return key < full_lo || key + kTileKeys > full_hi;
     };
-    // outputs that values dropped from tile T would have reached
-    auto restore = [&](int T) {
-      if (!part(T) || mark[T & 1] != T + 1) return;
-      const int key = begin + T * kTileKeys;
-      for_nonfinite<D, E4M3>(a, table, h, key, min(kTileKeys, u.len - key), [&](int k, const uint64_t (&bad)[D / 64]) {
-        int g4 = 4 * g;
-        pin(g4);
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            if (k >= lo && k < hi && bad_at<D>(bad, 32 * dt + 8 * (i / 4) + g4 + i % 4))
-              o[dt][i] = __uint_as_float(0x7fc00000u);
-      });
-    };
-
     S staged;
-    if (threadIdx.x < 2) mark[threadIdx.x] = 0;
+    if (threadIdx.x == 0) dropped = 0;
     lds_barrier();
     load_k<D, E4M3>(a, at, 0, k_lane, &staged);
     store_k<D, E4M3>(staged, k_lds[0]);
     load_v<D, E4M3>(a, at, 0, v_lane, &staged);
-    store_v<D, E4M3>(staged, begin, u.len, v_lds[0], part(0), 1, &mark[0]);
+    store_v<D, E4M3>(staged, begin, u.len, v_lds[0], part(0), &dropped);
     if (tiles > 1) load_k<D, E4M3>(a, at, 1, k_lane, &staged);
     lds_barrier();
     u32x4 p0[2], p1[2];
@@ -429,37 +433,66 @@ __global__ void __launch_bounds__(kTileWaves * 64, 2) attn_tile_kernel(AttnArgs 
     // step T: scores of tile T + 1, weights of keys 32 .. 95 and sums over
     // keys 0 .. 63 of tile T; meanwhile K of tile T + 2 and V of tile T + 1
     // come in, one after the other through the same registers
-    for (int T = 0; T < tiles - 1; ++T) {
+    auto step = [&](int T, auto hidden) {
+      constexpr bool HIDDEN = decltype(hidden)::value;
       const int key = begin + T * kTileKeys;
       const uint8_t* kl = k_lds[(T + 1) & 1];
       const uint8_t* vl = v_lds[T & 1];
-      restore(T);
       load_v<D, E4M3>(a, at, (T + 1) & 63, v_lane, &staged);
-      mask(s1, key + 32);
+      if (HIDDEN) mask(s1, key + 32);
       refer(s1, vl, 0, p0);
       inner_step<D>(kl, 0, vl, 0, q, s1, &w, p0, o, &s0, p1);
-      store_v<D, E4M3>(staged, key + kTileKeys, u.len, v_lds[(T + 1) & 1], part(T + 1), T + 2, &mark[(T + 1) & 1]);
+      store_v<D, E4M3>(staged, key + kTileKeys, u.len, v_lds[(T + 1) & 1], HIDDEN && part(T + 1), &dropped);
       if (T + 2 < tiles) {
         if (((T + 2) & 63) == 0) at = groups_at(a, table, h, ((key + 2 * kTileKeys) >> 4) + wave + 4 * lane, last_sub);
         load_k<D, E4M3>(a, at, (T + 2) & 63, k_lane, &staged);
       }
-      mask(s0, key + kTileKeys);
+      if (HIDDEN) mask(s0, key + kTileKeys);
       refer(s0, vl, 1, p1);
       inner_step<D>(kl, 1, vl, 1, q, s0, &w, p1, o, &s1, p0);
       if (T + 2 < tiles) store_k<D, E4M3>(staged, k_lds[T & 1]);
       lds_barrier();
-    }
+    };
+    // tiles [first, last) are seen whole; a loop each, for the hidden ones' work
+    // in the whole tiles' loop cost 3 % there (and one loop with both bodies spills)
+    const int first = max(0, full_lo - begin + kTileKeys - 1) / kTileKeys, last = max(0, full_hi - begin) / kTileKeys;
+    int T = 0;
+    for (; T < min(first, tiles - 1); ++T) step(T, std::true_type());
+    for (; T < last - 1; ++T) step(T, std::false_type());
+    for (; T < tiles - 1; ++T) step(T, std::true_type());
     const uint8_t* vl = v_lds[(tiles - 1) & 1];
-    restore(tiles - 1);
     mask(s1, begin + (tiles - 1) * kTileKeys + 32);
     refer(s1, vl, 0, p0);
     weights(s1, &w, p1);
     pv<D>(vl, 0, p0, o);
     pv<D>(vl, 1, p1, o);
+
+    // the outputs that dropped values would have reached
+    if (__builtin_amdgcn_readfirstlane(dropped)) {
+      int lo, hi;
+      own_range(&lo, &hi);
+      for (int T = 0; T < tiles; ++T) {
+        const int key = begin + T * kTileKeys;
+        if (!part(T)) continue;
+        for_nonfinite<D, E4M3>(a, table, h, key, min(kTileKeys, u.len - key), [&](int k, const uint64_t (&bad)[D / 64]) {
+          int g4 = 4 * g;
+          pin(g4);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              if (k >= lo && k < hi && bad_at<D>(bad, 32 * dt + 8 * (i / 4) + g4 + i % 4))
+                o[dt][i] = __uint_as_float(0x7fc00000u);
+        });
+      }
+    }
   }
 
   const float sum = w.l + __shfl_xor(w.l, 32, 64);
+  row = own_row();
   if (row >= u.rows) return;
+  place = u.row0 + row;
+  const int tok = u.first + place / a.group, head = h * a.group + place % a.group;
   const float v_scale = E4M3 && a.vc.scale ? a.vc.scale[h] : 1.0f;
   if (u.chunks <= 1) {
     const float inv = sum > 0.0f || sum != sum ? v_scale / sum : 0.0f;  // a row that saw no key is zero
