@@ -141,39 +141,19 @@ __device__ __forceinline__ uint64_t pick(uint32_t lo, uint32_t hi, int i) {
          (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)hi, i) << 32;
 }
 
-// Sets the infinities and NaNs among 8 bf16 values to zero; true if there were any.
-__device__ __forceinline__ bool drop_nonfinite(u32x4& v) {
-  bool any = false;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bool lo = (v[i] & 0x7f80u) == 0x7f80u, hi = (v[i] & 0x7f800000u) == 0x7f800000u;
-    v[i] &= (lo ? 0xffff0000u : 0xffffffffu) & (hi ? 0x0000ffffu : 0xffffffffu);
-    any |= lo | hi;
-  }
-  return any;
-}
-
 // Infinities and NaNs in values that some rows see and others do not: in a
 // product a hidden value's weight is 0, and 0 * NaN would reach the rows that do
-// not see it.  So where a tile is hidden in part, they are dropped from the
-// product.  The stream kernel, which has the tile in registers, then makes a
-// second product of their places (1, else 0) with the rows' non-zero weights:
-// it tells which outputs they reach.
-__device__ __forceinline__ u32x4 nonfinite_places(const u32x4& v) {
-  u32x4 x;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    x[i] = ((v[i] & 0x7f80u) == 0x7f80u ? 0x3f80u : 0u) | ((v[i] & 0x7f800000u) == 0x7f800000u ? 0x3f800000u : 0u);
-  return x;
-}
-__device__ __forceinline__ u32x4 nonzero_weights(const u32x4& p) {
-  u32x4 x;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) x[i] = ((p[i] & 0xffffu) ? 0x3f80u : 0u) | ((p[i] & 0xffff0000u) ? 0x3f800000u : 0u);
-  return x;
+// not see it.  So where a tile is hidden in part they are dropped from it, and
+// at the end the outputs that they reach are found by reading the values again.
+
+// Ones where a word's values (two bf16, or four E4M3 codes) are finite: the sum
+// has a field's top bit exactly where its exponent (its code) is all ones.
+template <bool E4M3>
+__device__ __forceinline__ uint32_t finite_mask(uint32_t w) {
+  const uint32_t top = E4M3 ? ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u : ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+  return ~((top << 1) - (top >> (E4M3 ? 7 : 15)));
 }
 
-// The tile kernel, whose waves share the tile, reads the values again instead:
 // `seen(key, bad)` is called for each key of [key, key + n) with non-finite
 // values, bad[i] holding value d = 2 l + i (D = 64: l) in bit l.
 template <int D, bool E4M3, class F>

@@ -173,6 +173,26 @@ __device__ __forceinline__ u32x4 v_operand(const KvTile<D, E4M3>& t, int dt) {
   return o;
 }
 
+// Whether a tile's values (of this lane) have infinities or NaNs: the exponent
+// (E4M3: the code's lower seven bits) all ones.  And without them.
+template <int D, bool E4M3>
+__device__ __forceinline__ bool has_nonfinite(const KvTile<D, E4M3>& t) {
+  uint32_t any = 0u;
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int w = 0; w < KvTile<D, E4M3>::VW; ++w)
+      any |= E4M3 ? (t.v[j][w] & 0x7f7f7f7fu) + 0x01010101u : (t.v[j][w] & 0x7f807f80u) + 0x00800080u;
+  return any & (E4M3 ? 0x80808080u : 0x80008000u);
+}
+template <int D, bool E4M3>
+__device__ __forceinline__ void drop_nonfinite(KvTile<D, E4M3>& t) {
+#pragma unroll
+  for (int j = 0; j < 8; ++j)
+#pragma unroll
+    for (int w = 0; w < KvTile<D, E4M3>::VW; ++w) t.v[j][w] &= finite_mask<E4M3>(t.v[j][w]);
+}
+
 // Workgroups a compute unit gets.  Measured over 32 sequences of 1,021 ..
 // 8,190 keys, bf16: 94.8 us with one, 100.3 us with two (16 sequences of 64-wide
 // heads: 30.1 and 31.3 us); 64 sequences of 4,003 .. 16,001, E4M3: 232.9 and
@@ -258,6 +278,9 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
     // keys that every row sees
     const int full_lo = a.window ? max(0, pos0 + (rows - 1) / a.group - a.window + 1) : 0;
     const int full_hi = a.causal ? min(s.len, max(0, pos0 + 1)) : s.len;
+    auto is_whole = [&](int key) { return key >= full_lo && key + 32 <= full_hi; };
+    const int key0 = key;
+    bool dropped = false;
 
     f32x4 o[NR][DT];
     float m[NR], l[NR], base[NR];
@@ -303,7 +326,11 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
 #pragma unroll
             for (int w = 0; w < Tile::VW; ++w) cur.v[j][w] = 0u;
       }
-      const bool whole = key >= full_lo && key + 32 <= full_hi;
+      const bool whole = is_whole(key);
+      if (!whole && __any(has_nonfinite<D, E4M3>(cur))) {
+        drop_nonfinite<D, E4M3>(cur);
+        dropped = true;
+      }
       u32x4 p[NR];
 #pragma unroll
       for (int n = 0; n < NR; ++n) {
@@ -339,30 +366,11 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
 #pragma unroll
         for (int j = 0; j < 4; ++j) p[n][j] = bf16_pair(x[n][2 * j], x[n][2 * j + 1]);
       }
-      if (whole) {
 #pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          const u32x4 v = v_operand<D, E4M3>(cur, dt);
+      for (int dt = 0; dt < DT; ++dt) {
+        const u32x4 v = v_operand<D, E4M3>(cur, dt);
 #pragma unroll
-          for (int n = 0; n < NR; ++n) o[n][dt] = mma_bf16(v, p[n], o[n][dt]);
-        }
-      } else {
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) {
-          const u32x4 all = v_operand<D, E4M3>(cur, dt);
-          u32x4 v = all;
-          const bool dropped = __any(drop_nonfinite(v));
-#pragma unroll
-          for (int n = 0; n < NR; ++n) {
-            o[n][dt] = mma_bf16(v, p[n], o[n][dt]);
-            if (dropped) {
-              const f32x4 hit = mma_bf16(nonfinite_places(all), nonzero_weights(p[n]), f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                if (hit[j] > 0.0f) o[n][dt][j] = __uint_as_float(0x7fc00000u);
-            }
-          }
-        }
+        for (int n = 0; n < NR; ++n) o[n][dt] = mma_bf16(v, p[n], o[n][dt]);
       }
       if (more) load_v<D, E4M3>(a, at, 2 * (tile & 31), v_lane, &cur);
     };
@@ -373,6 +381,24 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
           step(ahead[i]);
           key += 32;
         }
+    }
+
+    // the outputs that dropped values would have reached
+    if (dropped) {
+      for (key = key0; key < end; key += 32) {
+        if (is_whole(key)) continue;
+        for_nonfinite<D, E4M3>(a, table, h, key, min(32, s.len - key), [&](int k, const uint64_t (&bad)[D / 64]) {
+          int d0 = 4 * g * DT;
+          pin(d0);
+#pragma unroll
+          for (int n = 0; n < NR; ++n)
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+              for (int j = 0; j < 4; ++j)
+                if (k >= lo[n] && k < hi[n] && bad_at<D>(bad, d0 + j * DT + dt)) o[n][dt][j] = __uint_as_float(0x7fc00000u);
+        });
+      }
     }
 
     // the sequence's output if all of it lies in this slot, else this slot's

@@ -30,14 +30,14 @@
 // the values again.
 //
 // Measured on MI355X, 2048 new tokens at the end of 10,240 cached ones, 32 / 8
-// heads of 128: 344 us, 900 TFLOP/s of the visible pairs' flops, against 1140-
+// heads of 128: 326-341 us, 910-950 TFLOP/s of the visible pairs' flops, against 1140-
 // 1380 that a large library product reaches here.  With the exponentials, the
 // LDS reads or the staging left out it is 1, 3 or 13 % faster, with all of
 // them 33 %: no single part bounds it, the products' own rate does at last.
 // (Nor the tests of the reference maximum: made behind the products instead of
 // ahead of the weights, 344 us.)  64-wide heads have half the products for the
 // same weights, and the vector unit bounds them: 512 new tokens of each of 4
-// sequences of 2,000, bf16: 55 us, 529 TFLOP/s.
+// sequences of 2,000, bf16: 55 us, 534 TFLOP/s.
 #include "attention_common.hpp"
 
 #include <type_traits>
@@ -129,21 +129,6 @@ __device__ __forceinline__ void store_k(const Staged<D, E4M3>& t, uint8_t* kl) {
   }
 }
 
-// drop_nonfinite for 16 E4M3 codes.
-__device__ __forceinline__ bool drop_nan_codes(u32x4& v) {
-  bool any = false;
-#pragma unroll
-  for (int w = 0; w < 4; ++w) {
-    uint32_t keep = 0xffffffffu;
-#pragma unroll
-    for (int i = 0; i < 32; i += 8)
-      if ((v[w] & (0x7fu << i)) == (0x7fu << i)) keep &= ~(0xffu << i);
-    any |= keep != 0xffffffffu;
-    v[w] &= keep;
-  }
-  return any;
-}
-
 // V rows of keys beyond the sequence are stored as zero: the cache there may
 // hold anything, and 0 * NaN would reach every row.  From a tile that is hidden
 // from some rows (`part`) infinities and NaNs are dropped; `mark` is then set.
@@ -162,7 +147,12 @@ __device__ __forceinline__ void store_v(Staged<D, E4M3>& t, int key, int len, ui
 #pragma unroll
     for (int j = 0; j < S::PASSES; ++j) {
       pin(t.x[j]);
-      dropped |= E4M3 ? drop_nan_codes(t.x[j]) : drop_nonfinite(t.x[j]);
+#pragma unroll
+      for (int w = 0; w < 4; ++w) {
+        const uint32_t keep = finite_mask<E4M3>(t.x[j][w]);
+        dropped |= keep != 0xffffffffu;
+        t.x[j][w] &= keep;
+      }
     }
     if (__any(dropped)) *mark = 1;
   }
@@ -305,8 +295,9 @@ __device__ __forceinline__ void inner_step(const uint8_t* kl, int kt, const uint
 }
 
 // Workgroups a compute unit gets: what the registers allow.  (64-wide E4M3, 12
-// sequences with 4,327 new tokens, window 2048: 101 us with three, 109 us with two;
-// 64-wide bf16 and 128-wide heads do not fit three.)
+// sequences with 4,327 new tokens, window 2048: 101 us with three, 109 us with two.
+// 64-wide bf16 fits three with V's addresses made anew for each tile: 8 chunks of
+// 512 at 2,000 97.5 instead of 102 us, 4 of them 55.6 instead of 54.8: not taken.)
 constexpr int tile_workgroups(int D, bool e4m3) { return D == 64 && e4m3 ? 3 : 2; }
 
 template <int D, bool E4M3>
