@@ -139,12 +139,6 @@ ql_status check_rule(const ql_norm_rope* r, int64_t tokens, int32_t q_heads, int
 constexpr int64_t kStreamRows = 32;
 constexpr int64_t kMixedRows = 16;
 
-// Tiles of 32 keys that a slot of the stream kernel holds at least.  One
-// sequence of 1,000 keys: 10.6, 11.3, 12.4 us with 1, 2, 3; of 2,000: 13.5,
-// 12.7, 13.7; two of 6,000 (E4M3): 17.9, 16.6, 15.7 -- shorter slots, more
-// partial results.
-constexpr int kLeastTiles = 2;
-
 constexpr int kTileRows = 128;
 
 // Chunk of the tile kernel, bound by arithmetic: a workgroup runs at its own
@@ -365,7 +359,6 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
     const Part& x = p->stream;
     partials(x);
     a.slots = x.slots;
-    a.least_tiles = kLeastTiles;
     a.heads_wg = x.heads_wg;
     a.max_rows = x.most;
     e = qlk::launch_attn_stream(a, s.head_dim, e4m3, x.rows, hs);

@@ -57,7 +57,6 @@ struct AttnArgs {
   int min_rows;          // sequences with fewer rows are left to the stream kernel
   // stream kernel
   int slots;             // shares that all sequences' keys are cut into, for each KV head
-  int least_tiles;       // tiles of a slot at least (fewer slots otherwise)
   int heads_wg;          // KV heads of a workgroup (1, 2 or 4); its other waves take other slots
   int max_rows;          // sequences with more rows are left to the tile kernel
 };

@@ -42,6 +42,14 @@ namespace qlk {
 
 constexpr int kStreamWaves = 4;
 
+// A slot has 2^kPad tiles at least, a sequence kMostPieces slots at most: shorter
+// slots, more partial results.  One sequence of 1,000 keys: 10.6, 11.3, 12.4 us
+// with 1, 2, 3 tiles; of 2,000: 13.5, 12.7, 13.7 (30 sequences of 44 keys, 4 x 7
+// rows: 15.0, 11.0 with 1, 2).  One of 16,000, E4M3: 21.2, 17.4, 19.2 us with 256,
+// 128, 80 slots; 8 new tokens of it 24.8, 25.0, 23.7.
+constexpr int kPad = 1;
+constexpr int kMostPieces = 128;
+
 // One wave's 32 keys: K operands and V rows as they come from memory.
 template <int D, bool E4M3>
 struct KvTile {
@@ -124,21 +132,42 @@ __device__ __forceinline__ int inclusive_sum(int v) {
 __device__ __forceinline__ int lane_i32(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
 
 // All sequences' tiles, and how they are cut: `slots` slots of `each` tiles,
-// the first `more` of them one longer.
+// the first `more` of them one longer.  A sequence takes room for a multiple of
+// 2^pad tiles.
 struct Cut {
-  int slots, each, more;
+  int slots, each, more, pad;
   __device__ __forceinline__ int start(int j) const { return j * each + min(j, more); }
   __device__ __forceinline__ int slot_of(int t) const {
+    if (pad) return t >> pad;
     const int longer = more * (each + 1);
     return t < longer ? t / (each + 1) : more + (t - longer) / each;
   }
+  __device__ __forceinline__ int room(int tiles) const { return (tiles + (1 << pad) - 1) >> pad << pad; }
 };
 
-__device__ __forceinline__ Cut cut_of(const AttnArgs& a, int tiles) {
+// The cut of a batch whose first sequences the lanes hold, and the tiles up to
+// theirs.  Where the slots suffice, each lies in one sequence: a slot that
+// passes to a second one waits for its page table, then for its keys (15
+// sequences of 400 keys, E4M3: 17.5 us so, 15.1 with a sequence a slot; 8 of 30
+// keys: 11.3 and 6.9).  Else all slots are equally long.
+__device__ __forceinline__ Cut cut_of(const AttnArgs& a, const Seq& mine, int* upto) {
+  int most = a.slots;
+  if (a.batch <= 64) {
+    most = min(most, kMostPieces * a.batch);
+    const int pieces = inclusive_sum((mine.tiles + (1 << kPad) - 1) >> kPad), slots = lane_i32(pieces, 63);
+    if (slots <= most) {
+      *upto = pieces << kPad;
+      return Cut{slots, 1 << kPad, 0, kPad};
+    }
+  }
+  *upto = inclusive_sum(mine.tiles);
+  int total = lane_i32(*upto, 63);
+  for (int b0 = 64; b0 < a.batch; b0 += 64) total += lane_i32(inclusive_sum(seq_of(a, b0 + (threadIdx.x & 63)).tiles), 63);
   Cut c;
-  c.slots = max(1, min(a.slots, (tiles + a.least_tiles - 1) / a.least_tiles));
-  c.each = tiles / c.slots;
-  c.more = tiles - c.each * c.slots;
+  c.slots = min(most, (total + (1 << kPad) - 1) >> kPad);
+  c.each = total / max(1, c.slots);
+  c.more = total - c.each * c.slots;
+  c.pad = 0;
   return c;
 }
 
@@ -225,11 +254,9 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
   // the tiles of all sequences, 64 sequences at a time; `before`: of those
   // before the ones the lanes hold
   Seq mine = seq_of(a, lane);
-  int upto = inclusive_sum(mine.tiles), before = 0, base = 0;
-  int total = lane_i32(upto, 63);
-  for (int b0 = 64; b0 < a.batch; b0 += 64) total += lane_i32(inclusive_sum(seq_of(a, b0 + lane).tiles), 63);
-  const Cut cut = cut_of(a, total);
-  if (total == 0 || slot >= cut.slots) return;
+  int upto, before = 0, base = 0;
+  const Cut cut = cut_of(a, mine, &upto);
+  if (slot >= cut.slots) return;
   int t = cut.start(slot);
   const int t_begin = t, t_end = cut.start(slot + 1);
 
@@ -244,13 +271,13 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
       before += lane_i32(upto, 63);
       base += 64;
       mine = seq_of(a, base + lane);
-      upto = inclusive_sum(mine.tiles);
+      upto = inclusive_sum(mine.tiles);  // more than 64 sequences: without padding
     }
     const int i = __ffsll((unsigned long long)__ballot(before + upto > t)) - 1;
     const int b = base + i;
     const Seq s = {lane_i32(mine.first, i), lane_i32(mine.n, i), lane_i32(mine.len, i), lane_i32(mine.lo, i),
                    lane_i32(mine.tiles, i)};
-    const int seq_begin = before + lane_i32(upto, i) - s.tiles;
+    const int seq_end = before + lane_i32(upto, i), seq_begin = seq_end - cut.room(s.tiles);
     const int t_stop = min(t_end, seq_begin + s.tiles);
     const int rows = min(s.n * a.group, R), pos0 = s.len - s.n;
     int key = (s.lo & ~31) + (t - seq_begin) * 32;
@@ -441,7 +468,7 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
         }
       }
     }
-    t = t_stop;
+    t = t_stop == seq_begin + s.tiles ? seq_end : t_stop;
   }
 }
 
@@ -516,20 +543,19 @@ __global__ void __launch_bounds__(kJoinWaves * 64) attn_stream_join_kernel(AttnA
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int id = WAVES == 1 ? (int)blockIdx.x * kJoinWaves + wave : blockIdx.x;
   const int h = id % a.kv_heads, row = id / a.kv_heads, b = blockIdx.y;
-  Seq mine = {0, 0, 0, 0, 0};
-  int total = 0, seq_begin = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    const Seq s = seq_of(a, b0 + lane);
-    const int upto = inclusive_sum(s.tiles);
-    if (b >= b0 && b < b0 + 64) {
+  Seq s = seq_of(a, lane), mine = {0, 0, 0, 0, 0};
+  int upto, seq_begin = 0;
+  const Cut cut = cut_of(a, s, &upto);
+  for (int b0 = 0;; b0 += 64, s = seq_of(a, b0 + lane), upto = inclusive_sum(s.tiles)) {
+    if (b < b0 + 64) {
       const int i = b - b0;
       mine = Seq{lane_i32(s.first, i), lane_i32(s.n, i), 0, 0, lane_i32(s.tiles, i)};
-      seq_begin = total + lane_i32(upto, i) - mine.tiles;
+      seq_begin += lane_i32(upto, i) - cut.room(mine.tiles);
+      break;
     }
-    total += lane_i32(upto, 63);
+    seq_begin += lane_i32(upto, 63);
   }
   if (mine.tiles == 0 || row >= mine.n * a.group) return;
-  const Cut cut = cut_of(a, total);
   const int s0 = cut.slot_of(seq_begin), s1 = cut.slot_of(seq_begin + mine.tiles - 1);
   if (s0 == s1) return;  // written by the stream kernel
   const int64_t step = (int64_t)a.kv_heads * R;

@@ -293,6 +293,17 @@ def test_attention_plan_bounds_may_be_loose(max_q, max_kv):
     p.check(out, ls)
 
 
+@pytest.mark.parametrize("D,e4m3,batch,kv", [(64, False, 130, 90), (128, True, 200, 40), (64, False, 40, 420), (64, True, 64, 33),
+                                             (128, False, 64, 66), (128, False, 65, 66)])
+def test_attention_many_sequences(D, e4m3, batch, kv):
+    """More sequences than a wave holds, more tiles than there are slots, and
+    slots that lie in one sequence each; some sequences have no new token."""
+    new = [(0, 1, 1, 2, 3)[i % 5] for i in range(batch)]
+    p = Problem(50 + batch, new, [3 + (i * 7919) % kv for i in range(batch)], 16, 8, D, 16, e4m3)
+    out, ls = p.run(p.plan())
+    p.check(out, ls)
+
+
 def test_attention_batch_of_chunks_and_many_short_sequences():
     """Sequences of few rows beside chunks, with contexts (by the plan's bound)
     long enough that they get a launch of their own."""
