@@ -9,8 +9,10 @@ K, applied by the matrix core) and MXFP4 (E2M1 weights two a byte, same
 scales, MXFP8 activations).  All arithmetic runs in the hand-written gfx950 HIP kernels
 of ``libqlinear.so`` behind the C ABI of ``include/qlinear.h``; this module
 only marshals torch tensors (device memory) and streams into that ABI, with
-the same function names.  There is no CPU or PyTorch fallback: if the
-library is missing, or a tensor is not on the GPU, calls raise.
+the same function names.  Norm and rotation of heads, append to a paged cache,
+attention over it and draft verification are in ``serving.py``.  There is no
+CPU or PyTorch fallback: if the library is missing, or a tensor is not on the
+GPU, calls raise.
 """
 
 import ctypes
