@@ -205,8 +205,9 @@ ql_status plan_stream(const ql_attention_shape& s, int64_t rows, Part* p) {
   p->slots = qlk::attn_stream_slots(s.head_dim, s.kv_type == QL_KV_E4M3, p->rows, s.kv_heads, p->heads_wg);
   if ((int64_t)p->slots * s.kv_heads >= (int64_t(1) << 31) || rows * s.kv_heads >= (int64_t(1) << 31))
     return fail(QL_E_UNSUPPORTED, "more than 2^31 workgroups");
-  // a batch that fits one tile a sequence is never cut
-  const int64_t parts = s.max_kv > 32 ? (int64_t)p->slots * 2 * s.kv_heads * p->rows : 0;
+  // sequences that fit a slot each are never cut
+  const int64_t whole = s.batch <= std::min(64, p->slots) ? 32 << qlk::kStreamPad : 32;
+  const int64_t parts = s.max_kv > whole ? (int64_t)p->slots * 2 * s.kv_heads * p->rows : 0;
   p->splits = parts ? 2 : 1;
   p->ml_at = parts * s.head_dim * 4;
   p->end = p->ml_at + parts * 2 * 4;

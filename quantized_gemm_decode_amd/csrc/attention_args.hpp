@@ -84,6 +84,10 @@ __host__ __device__ __forceinline__ int page_of(int sub, uint64_t magic) {
   return (int)(((uint64_t)(uint32_t)sub * magic) >> kPageMagicShift);
 }
 
+// Tiles of 32 keys that a slot of the stream kernel has at least: 2^kStreamPad.
+// Up to 64 sequences, if the slots suffice for it, have slots of their own.
+constexpr int kStreamPad = 1;
+
 // Most entries of a vocabulary row that one workgroup of the verification takes.
 constexpr int kVerifySlice = 4096;
 

@@ -42,12 +42,11 @@ namespace qlk {
 
 constexpr int kStreamWaves = 4;
 
-// A slot has 2^kPad tiles at least, a sequence kMostPieces slots at most: shorter
-// slots, more partial results.  One sequence of 1,000 keys: 10.6, 11.3, 12.4 us
-// with 1, 2, 3 tiles; of 2,000: 13.5, 12.7, 13.7 (30 sequences of 44 keys, 4 x 7
-// rows: 15.0, 11.0 with 1, 2).  One of 16,000, E4M3: 21.2, 17.4, 19.2 us with 256,
-// 128, 80 slots; 8 new tokens of it 24.8, 25.0, 23.7.
-constexpr int kPad = 1;
+// A sequence has kMostPieces slots at most, a slot 2^kStreamPad tiles at least:
+// shorter slots, more partial results.  One sequence of 1,000 keys: 10.6, 11.3,
+// 12.4 us with 1, 2, 3 tiles; of 2,000: 13.5, 12.7, 13.7 (30 sequences of 44 keys,
+// 4 x 7 rows: 15.0, 11.0 with 1, 2).  One of 16,000, E4M3: 21.2, 17.4, 19.2 us with
+// 256, 128, 80 slots; 8 new tokens of it 24.8, 25.0, 23.7.
 constexpr int kMostPieces = 128;
 
 // One wave's 32 keys: K operands and V rows as they come from memory.
@@ -154,17 +153,17 @@ __device__ __forceinline__ Cut cut_of(const AttnArgs& a, const Seq& mine, int* u
   int most = a.slots;
   if (a.batch <= 64) {
     most = min(most, kMostPieces * a.batch);
-    const int pieces = inclusive_sum((mine.tiles + (1 << kPad) - 1) >> kPad), slots = lane_i32(pieces, 63);
+    const int pieces = inclusive_sum((mine.tiles + (1 << kStreamPad) - 1) >> kStreamPad), slots = lane_i32(pieces, 63);
     if (slots <= most) {
-      *upto = pieces << kPad;
-      return Cut{slots, 1 << kPad, 0, kPad};
+      *upto = pieces << kStreamPad;
+      return Cut{slots, 1 << kStreamPad, 0, kStreamPad};
     }
   }
   *upto = inclusive_sum(mine.tiles);
   int total = lane_i32(*upto, 63);
   for (int b0 = 64; b0 < a.batch; b0 += 64) total += lane_i32(inclusive_sum(seq_of(a, b0 + (threadIdx.x & 63)).tiles), 63);
   Cut c;
-  c.slots = min(most, (total + (1 << kPad) - 1) >> kPad);
+  c.slots = min(most, (total + (1 << kStreamPad) - 1) >> kStreamPad);
   c.each = total / max(1, c.slots);
   c.more = total - c.each * c.slots;
   c.pad = 0;

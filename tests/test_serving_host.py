@@ -108,6 +108,9 @@ def test_attention_plan_facts():
         return f
     one = facts(batch=1, tokens=1, max_kv=32)
     assert one["stream_rows"] == 16 and one["tile_rows"] == 0 and one["workspace_bytes"] == 0
+    # up to 64 sequences of at most two tiles of 32 keys are not cut either
+    assert facts(batch=64, tokens=64, max_kv=64)["workspace_bytes"] == 0
+    assert facts(batch=64, tokens=64, max_kv=65)["workspace_bytes"] > 0 < facts(batch=65, tokens=65, max_kv=64)["workspace_bytes"]
     long = facts(batch=1, tokens=1, max_kv=100000)
     # two partial results a slot: outputs, maxima and sums of every row of every KV head
     assert long["workspace_bytes"] == 2 * 8 * long["slots"] * 16 * (128 + 2) * 4
