@@ -141,19 +141,29 @@ constexpr int64_t kMixedRows = 16;
 
 constexpr int kTileRows = 128;
 
-// Chunk of the tile kernel, bound by arithmetic: a workgroup runs at its own
-// pace, 512 of them at a time (two a compute unit).  Measured for head_dim 128:
-// 23 ns a key while every workgroup has a compute unit to itself, 37 ns when two
-// share one, 4 us around that, and for a cut the join's launch (6 us) and
-// its traffic (0.06 us a workgroup's partial result).  Takes the number of
-// chunks that this makes cheapest.
-int64_t tile_chunk(int64_t units, int64_t span) {
+// Chunk of the tile kernel.  A workgroup runs at its own pace, 512 of them at a
+// time (two a compute unit).  Measured in ns a key: 19 while every workgroup has
+// a compute unit to itself, 33 when two share one (64-wide heads: 14 and 23.5);
+// 4 us around that; for a cut the join's launch (6 us) and its traffic (0.02 us a
+// workgroup's partial result, more where they outgrow the caches).  The plan
+// knows the longest context only: a batch is taken to have 3/4 of that on
+// average, and the last round to be half full.  Takes the number of chunks that
+// this makes cheapest.  Best and taken in us, over 1 .. 16 chunks: 9 x 475 new
+// tokens at 2,732 .. 7,023, 16 / 16 heads, 192 and 192 (1 chunk; 2: 294); 512 at 8,192
+// 85 and 85 (4; 1: 157); 64 at 8,192 25 and 26 (16); 4 x 140 at 507 .. 2,506, 64-wide, 33
+// and 33 (2; 1: 40); 8 x 1,024 at 4,096 492 and 492 (1; 2: 675).
+int64_t tile_chunk(int head_dim, int64_t batch, int64_t units, int64_t span) {
+  const double alone = head_dim == 64 ? 0.0142 : 0.019, shared = head_dim == 64 ? 0.0235 : 0.033;
   int64_t best = span;
   double least = 0;
   for (int64_t s = 1; s == 1 || (s <= 64 && span / s >= 256); ++s) {
-    const int64_t chunk = ((span + s - 1) / s + 63) / 64 * 64, groups = units * s;
-    const double rounds = groups <= 512 ? 1.0 : groups <= 4096 ? (double)((groups + 511) / 512) : groups / 512.0;
-    const double us = rounds * (4.0 + chunk * (groups <= 256 ? 0.023 : 0.037)) + (s > 1 ? 6.0 + groups * 0.03 : 0.0);
+    const int64_t chunk = ((span + s - 1) / s + 63) / 64 * 64;
+    const double groups = (double)(units * s) * (batch > 1 ? 0.75 : 1.0), x = groups / 512;
+    const double rounds = x <= 1.0 ? 1.0 : (x + std::ceil(x)) / 2;
+    // between 256 and 512 the units that share take longest, unless they are the short ones
+    const double both = batch > 1 ? std::min(1.0, std::max(0.0, groups / 256 - 1.0)) : groups > 256 ? 1.0 : 0.0;
+    const double pace = alone + (shared - alone) * both;
+    const double us = rounds * (4.0 + (double)chunk * pace) + (s > 1 ? 6.0 + groups * 0.02 : 0.0);
     if (s == 1 || us < least) {
       least = us;
       best = chunk;
@@ -176,7 +186,9 @@ ql_status plan_tile(const ql_attention_shape& s, int64_t rows, int64_t at, Part*
   const int64_t blocks = (rows + R - 1) / R;
   const int64_t units = s.batch * blocks * s.kv_heads;
   const int64_t span = tile_span(s);
-  const int64_t chunk = tile_chunk(units, span);
+  // units with rows, whatever the batch's lengths
+  const int64_t filled = std::min(s.batch * blocks, s.tokens * group / R + s.batch) * s.kv_heads;
+  const int64_t chunk = tile_chunk(s.head_dim, s.batch, filled, span);
   const int64_t splits = std::max<int64_t>(1, (span + chunk - 1) / chunk);
   if (units * splits >= (int64_t(1) << 31) || units * R / 4 >= (int64_t(1) << 31))
     return fail(QL_E_UNSUPPORTED, "more than 2^31 workgroups");
