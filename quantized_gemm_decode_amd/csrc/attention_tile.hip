@@ -294,14 +294,13 @@ __device__ __forceinline__ void inner_step(const uint8_t* kl, int kt, const uint
   if (D == 128) __builtin_amdgcn_s_setprio(0);
 }
 
-// Workgroups a compute unit gets: what the registers allow.  (64-wide E4M3, 12
-// sequences with 4,327 new tokens, window 2048: 101 us with three, 109 us with two.
-// 64-wide bf16 fits three with V's addresses made anew for each tile: 8 chunks of
-// 512 at 2,000 97.5 instead of 102 us, 4 of them 55.6 instead of 54.8: not taken.)
-constexpr int tile_workgroups(int D, bool e4m3) { return D == 64 && e4m3 ? 3 : 2; }
+// Workgroups a compute unit gets: what the registers allow.  (64-wide heads, 12
+// sequences with 4,327 new tokens, window 2048, E4M3: 101 us with three, 109 us
+// with two; 8 chunks of 512 at 2,000, bf16: 96 and 102 us.)
+constexpr int tile_workgroups(int D) { return D == 64 ? 3 : 2; }
 
 template <int D, bool E4M3>
-__global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D, E4M3)) attn_tile_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile_kernel(AttnArgs a) {
   constexpr int R = kTileRows, DT = D / 32, KS = D / 16;
   constexpr int kBytes = kTileKeys * D * 2;  // one tensor's tile
   __shared__ __align__(16) uint8_t k_lds[2][kBytes], v_lds[2][kBytes];
@@ -411,6 +410,24 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D, E4M3)) att
     store_v<D, E4M3>(staged, begin, u.len, v_lds[0], part(0), &dropped);
     if (tiles > 1) load_k<D, E4M3>(a, at, 1, k_lane, &staged);
     lds_barrier();
+    // a wave without rows only brings in its share of the tiles (64 x 9 tokens of 4
+    // heads at 3,000: 145 -> 140 us; 24 x 8 of 5 at 500: 19.5 -> 16.9)
+    if (wave * 32 >= u.rows) {
+      if (tiles > 1) store_k<D, E4M3>(staged, k_lds[1]);
+      lds_barrier();
+      for (int T = 0; T < tiles - 1; ++T) {
+        const int key = begin + (T + 1) * kTileKeys;
+        load_v<D, E4M3>(a, at, (T + 1) & 63, v_lane, &staged);
+        store_v<D, E4M3>(staged, key, u.len, v_lds[(T + 1) & 1], part(T + 1), &dropped);
+        if (T + 2 < tiles) {
+          if (((T + 2) & 63) == 0) at = groups_at(a, table, h, ((key + kTileKeys) >> 4) + wave + 4 * lane, last_sub);
+          load_k<D, E4M3>(a, at, (T + 2) & 63, k_lane, &staged);
+          store_k<D, E4M3>(staged, k_lds[T & 1]);
+        }
+        lds_barrier();
+      }
+      return;
+    }
     u32x4 p0[2], p1[2];
     p1[0] = p1[1] = u32x4{0u, 0u, 0u, 0u};
     f32x16 s0 = qk<D>(k_lds[0], 0, q);
