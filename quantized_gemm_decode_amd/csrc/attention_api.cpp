@@ -133,8 +133,8 @@ ql_status check_rule(const ql_norm_rope* r, int64_t tokens, int32_t q_heads, int
 
 // Rows (new tokens x query heads of a KV head) of a sequence up to which the
 // stream kernel serves it; in a batch that has longer ones too, up to which
-// sequences get a stream launch of their own.  16 sequences of 4,000 keys: 61 us
-// with 32 rows each here; with 64 rows the tile kernel takes 66 us and the
+// sequences get a stream launch of their own.  16 sequences of 4,000 keys, 32
+// rows each: 58 us here, 61 us in the tile kernel, which takes 66 us for 64 rows; the
 // stream kernel would not hold their sums in registers.
 constexpr int64_t kStreamRows = 32;
 constexpr int64_t kMixedRows = 16;
@@ -294,10 +294,11 @@ ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan*
   // Sequences of few rows among longer ones get a launch of their own where
   // there can be many of them with long contexts: to the tile kernel each is a
   // workgroup of mostly idle rows for each KV head.  By the (sequence, KV head,
-  // key) triples that this would take: 48 k (one chunk of 64 and 7 x 1,000) 39.9 us
-  // apart, 26.3 us together; 84 k (12 sequences, 701 new tokens in all, window
-  // 2048, heads of 64) 110.7 and 99.3; 240 k (4 x 128 and 60 x 500) 35.3 and 51.0; 448 k (256 and 15 x 4,000) 133
-  // and 188; 4 M (512 and 63 x 8,000) 497 and 1031.
+  // key) triples that this would take, apart and together, us: 48 k (a chunk of 64
+  // and 7 x 1,000) 34 and 24; 84 k (12 sequences, 701 new tokens at most, window
+  // 2048, 64-wide) 103 and 93; 240 k (4 x 128 and 60 x 500, 64-wide) 35 and 35; 480 k
+  // (256 and 15 x 4,000) 116 and 112; 504 k (100 and 63 x 1,000) 76 and 118; 744 k
+  // (1,024 and 31 x 3,000) 116 and 227; 4 M (512 and 63 x 8,000) 491 and 974.
   const int64_t few = s->max_q > 0 ? s->batch - (s->tokens + s->max_q - 1) / s->max_q : 0;
   const bool mixed = chunks && few * s->kv_heads * tile_span(*s) > 160000;
   p->tile_from = mixed ? kMixedRows + 1 : 0;

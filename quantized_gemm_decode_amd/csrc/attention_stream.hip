@@ -221,20 +221,20 @@ __device__ __forceinline__ void drop_nonfinite(KvTile<D, E4M3>& t) {
     for (int w = 0; w < KvTile<D, E4M3>::VW; ++w) t.v[j][w] &= finite_mask<E4M3>(t.v[j][w]);
 }
 
-// Workgroups a compute unit gets.  Measured over 32 sequences of 1,021 ..
-// 8,190 keys, bf16: 94.8 us with one, 100.3 us with two (16 sequences of 64-wide
-// heads: 30.1 and 31.3 us); 64 sequences of 4,003 .. 16,001, E4M3: 232.9 and
-// 210.9 us (64-wide: 27.9 and 22.3 us).  More requests on their way than that
-// only queue; E4M3's are half as large.  With 32 rows the sums of 128-wide heads
-// leave one workgroup its registers (E4M3, 32 sequences of 4,000 keys: 68 us, 97
-// us squeezed into two; 64-wide: 35.6 and 31.2 us).
+// Workgroups a compute unit gets.  Measured, one and two: 32 sequences of 4,600
+// keys, 64 / 8 heads, bf16 98.5 and 105.6 us (16 of 4,000, 64-wide heads: 29.6 and
+// 31.8); 64 of 9,000, E4M3 216 and 201 us (3,000, 64-wide: 51 and 41; 5 x 4 rows:
+// 45.8 and 39.6).  More requests on their way than that only queue; E4M3's are
+// half as large.  With 32 rows the sums of 128-wide heads leave one workgroup its
+// registers (32 sequences of 5 x 4 rows, 4,000 keys: 65.8 us, 66.8 with two; 16 of
+// them: 39.7 and 45.6).
 constexpr int stream_workgroups(int D, bool e4m3, int row_tiles) { return e4m3 && (row_tiles == 1 || D == 64) ? 2 : 1; }
 
 // Tiles that a wave has in its registers: a compute unit's only workgroup asks
 // for a second one while it works on the first (32 sequences of 5 x 4 rows and
-// 4,000 keys, with one and two: E4M3 72.2 and 68.4 us, 64-wide bf16 56.9 and
-// 54.7); where there are two, they cover each other (64-wide E4M3, single
-// tokens, 8,000 keys: 52.0 and 55.0 us).
+// 4,000 keys, with one and two: E4M3 67.1 and 65.7 us, 64-wide bf16 55.7 and
+// 54.0); where there are two, they cover each other (64-wide E4M3, single
+// tokens, 8,000 keys: 51.6 and 54.8 us).
 constexpr int stream_depth(int D, bool e4m3, int row_tiles) { return stream_workgroups(D, e4m3, row_tiles) == 1 ? 2 : 1; }
 
 template <int D, bool E4M3, int NR>
