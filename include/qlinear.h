@@ -616,7 +616,7 @@ ql_status qlinear_qkv_append(const ql_norm_rope* rule, int64_t tokens, int32_t q
  * beyond a sequence's length may be anything, NaN included, and an infinity or
  * NaN in a key or value never reaches a row that does not see it (a row that
  * sees one gets non-finite outputs); page-table entries beyond a sequence's
- * pages are not read.  Memory safety does not depend on the device
+ * pages do not matter.  Memory safety does not depend on the device
  * arrays: lengths are clamped to max_kv, pages to the cache, cu_q to
  * [0, tokens].
  *
@@ -625,9 +625,9 @@ ql_status qlinear_qkv_append(const ql_norm_rope* rule, int64_t tokens, int32_t q
  * one that shares tiles of them between many rows; both for batches that mix
  * such sequences with ones of up to 16 rows.  max_q, max_kv: upper bounds of a
  * sequence's new and cached tokens (the page table holds at least
- * ceil(max_kv / page_size) columns); rows of a sequence beyond max_q are not
- * computed.  q_heads a multiple of kv_heads; head_dim 64 or 128; scale 0 =
- * 1 / sqrt(head_dim).  Partial results are joined by a second launch (no atomics:
+ * ceil(max_kv / page_size) columns; NULL where max_kv is 0); a sequence with
+ * more than max_q new tokens is computed in part or not at all.  q_heads a
+ * multiple of kv_heads; head_dim 64 or 128; scale 0 = 1 / sqrt(head_dim).  Partial results are joined by a second launch (no atomics:
  * results do not depend on timing).  The workspace needs no initialisation;
  * concurrent calls need distinct ones.
  */

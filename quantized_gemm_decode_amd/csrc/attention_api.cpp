@@ -337,15 +337,17 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
     return fail(QL_E_INVALID, "the cache is not of the plan's type, heads, head_dim and page_size");
   if (s.batch == 0 || s.tokens == 0 || s.max_q == 0) return QL_OK;
   if ((st = check_rows(q, "q", s.q_heads, &a.q)) != QL_OK || (st = check_rows(out, "out", s.q_heads, &a.out)) != QL_OK) return st;
-  if (!page_table || !seq_lens || !cu_q) return fail(QL_E_INVALID, "page_table, seq_lens or cu_q is NULL");
+  if ((!page_table && s.max_kv > 0) || !seq_lens || !cu_q) return fail(QL_E_INVALID, "page_table, seq_lens or cu_q is NULL");
   if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(lse, 4))
     return fail(QL_E_ALIGN, "page_table, seq_lens, cu_q and lse must be 4-byte aligned");
   if (s.batch > 1 && table_stride < (s.max_kv + s.page_size - 1) / s.page_size)
     return fail(QL_E_INVALID, "page_table rows hold fewer than ceil(max_kv / page_size) entries");
   if (qlinear_attention_workspace_bytes(p) > 0 && !workspace) return fail(QL_E_INVALID, "this plan needs a workspace");
   if (!aligned16(workspace)) return fail(QL_E_ALIGN, "workspace is not 16-byte aligned");
-  a.table = page_table;
-  a.table_row = table_stride;
+  // without any context the table may have no entry, but the decode kernel looks
+  // up a page for every sequence (and clamps it)
+  a.table = s.max_kv > 0 ? page_table : seq_lens;
+  a.table_row = s.max_kv > 0 ? table_stride : 0;
   a.seq_lens = seq_lens;
   a.cu_q = cu_q;
   a.lse = lse;

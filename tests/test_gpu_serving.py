@@ -293,6 +293,15 @@ def test_attention_plan_bounds_may_be_loose(max_q, max_kv):
     p.check(out, ls)
 
 
+@pytest.mark.parametrize("new", [[1, 2], [40, 1]])
+def test_attention_without_any_context(new):
+    """max_kv = 0: a page table without columns; every row is zero, its lse -inf."""
+    p = Problem(9, new, [0, 0], 4, 2, 64, 16, False)
+    p.table = torch.zeros(2, 0, dtype=torch.int32)
+    out, ls = p.run(p.plan(max_kv=0))
+    assert not out.any() and torch.isneginf(ls).all()
+
+
 @pytest.mark.parametrize("D,e4m3,batch,kv", [(64, False, 130, 90), (128, True, 200, 40), (64, False, 40, 420), (64, True, 64, 33),
                                              (128, False, 64, 66), (128, False, 65, 66)])
 def test_attention_many_sequences(D, e4m3, batch, kv):
