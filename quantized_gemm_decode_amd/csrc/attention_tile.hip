@@ -30,7 +30,7 @@
 // the values again.
 //
 // Measured on MI355X, 2048 new tokens at the end of 10,240 cached ones, 32 / 8
-// heads of 128: 324-375 us by card, 820-950 TFLOP/s of the visible pairs' flops,
+// heads of 128: 304-375 us by card, 820-1020 TFLOP/s of the visible pairs' flops,
 // against 1140-1380 that a large library product reaches.  With the exponentials, the
 // LDS reads or the staging left out it is 1, 3 or 13 % faster, with all of
 // them 33 %: no single part bounds it, the products' own rate does at last.
