@@ -565,7 +565,7 @@ typedef struct {
  * of the first rot_dim values; the rest of n is kept.  cos_sin is binary32
  * [max_pos, rot_dim], a position's rot_dim/2 cosines followed by its sines.
  * rot_dim is a multiple of 16 up to head_dim, 0 for no rotation (cos_sin may
- * then be NULL).  Weights are bf16 [head_dim].  All arithmetic in binary32,
+ * then be NULL, as for max_pos 0, where no position is known).  Weights are bf16 [head_dim].  All arithmetic in binary32,
  * rounded once.
  */
 typedef struct {

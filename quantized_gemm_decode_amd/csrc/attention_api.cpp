@@ -113,7 +113,7 @@ ql_status check_rule(const ql_norm_rope* r, int64_t tokens, int32_t q_heads, int
   if (!aligned16(r->q_weight) || !aligned16(r->k_weight))
     return fail(QL_E_ALIGN, "norm weights must be 16-byte aligned");
   if (tokens > 0 && (q_heads > 0 || kv_heads > 0)) {
-    if (r->rot_dim > 0 && !r->cos_sin) return fail(QL_E_INVALID, "cos_sin is NULL");
+    if (r->rot_dim > 0 && r->max_pos > 0 && !r->cos_sin) return fail(QL_E_INVALID, "cos_sin is NULL");
     if (!positions) return fail(QL_E_INVALID, "positions is NULL");
   }
   if (!aligned(r->cos_sin, 4) || !aligned(positions, 8)) return fail(QL_E_ALIGN, "cos_sin or positions misaligned");

@@ -150,8 +150,8 @@ __global__ void __launch_bounds__(kHeadThreads) heads_kernel(HeadArgs a, int par
   // y = inv (x A + x' B) with x' the pair's other half: A = w cos, B = w' sin
   // with the sign of this lane's side, once a token for its queries and keys
   float c[8], s[8];
-  if (turned) {
-    const float* row = a.table + (known ? pos : 0) * a.rot;
+  if (turned && known) {
+    const float* row = a.table + pos * a.rot;
     if (a.interleaved) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

@@ -556,3 +556,14 @@ def test_verify_draft_follows_the_target():
     freq = np.bincount(out[:, 0], minlength=V) / B
     # five standard deviations of a frequency near 0.35 over 40,000 draws
     assert np.abs(freq - p.numpy()).max() < 5 * np.sqrt(0.35 * 0.65 / B), freq
+
+
+# ------------------------------------------------------------------ edges of the arguments and of the values
+
+def test_an_empty_table_gives_nan_rows():
+    """No position is known where the table has no row: every rotated row is NaN, and nothing is read."""
+    q, k, _, qw, kw = head_inputs(2, 3, 2, 1, 64, True)
+    pos = torch.tensor([0, 5, -1]).cuda()
+    qo, ko = torch.zeros_like(q).contiguous(), torch.zeros_like(k).contiguous()
+    ql.qlinear_qk_norm_rope(q, k, pos, ql.rope_table(0, 64), qo, ko, qw, kw)
+    assert torch.isnan(qo).all() and torch.isnan(ko).all()
