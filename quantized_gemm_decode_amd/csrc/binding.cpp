@@ -8,6 +8,8 @@
 // arguments by position (serving.py gives them names and defaults), raise
 // ValueError for tensors that do not fit and return the library's status.
 #include <torch/csrc/autograd/python_variable.h>
+#include <c10/hip/HIPFunctions.h>
+#include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 
 #include "../../include/qlinear.h"
@@ -20,6 +22,12 @@ struct Refused {};
 [[noreturn]] void refuse(const char* name, const char* what) {
   PyErr_Format(PyExc_ValueError, "%s %s", name, what);
   throw Refused();
+}
+
+int64_t number(PyObject* o) {
+  const int64_t v = PyLong_AsLongLong(o);
+  if (v == -1 && PyErr_Occurred()) throw Refused();
+  return v;
 }
 
 // One call's tensors: all on the GPU that the first one names.
@@ -80,6 +88,12 @@ struct Call {
     return ql_rows{t.data_ptr(), t.stride(0), t.stride(1)};
   }
 
+  // A cache's descriptor; `index` is the device of its tensors.
+  const ql_kv_cache* cache(PyObject* address, PyObject* index) {
+    if (number(index) != device) refuse("cache", "is on another device than the call's first tensor");
+    return static_cast<const ql_kv_cache*>(number_ptr(address));
+  }
+
   void* stream(PyObject* o) {
     if (o == Py_None) return c10::hip::getCurrentHIPStream(static_cast<c10::DeviceIndex>(device)).stream();
     return number_ptr(o);
@@ -92,11 +106,15 @@ struct Call {
   }
 };
 
-int64_t number(PyObject* o) {
-  const int64_t v = PyLong_AsLongLong(o);
-  if (v == -1 && PyErr_Occurred()) throw Refused();
-  return v;
-}
+// Launches go to the process's current device: makes that the call's for a
+// scope.  As a rule it is already, and then only asking costs anything (0.1 us
+// of host time, a guard that sets it and sets it back 0.3).
+struct OnDevice {
+  c10::hip::OptionalHIPGuard guard;
+  explicit OnDevice(const Call& c) {
+    if (c10::hip::current_device() != c.device) guard.set_index(static_cast<c10::DeviceIndex>(c.device));
+  }
+};
 
 ql_norm_rope rule_of(Call& c, PyObject* table, PyObject* q_weight, PyObject* k_weight, int64_t dim, PyObject* eps,
                      PyObject* interleaved) {
@@ -125,11 +143,12 @@ int64_t qk_norm_rope(PyObject* const* a) {
   const ql_rows q_out = c.rows(a[4], "q_out", tokens, q_heads, dim), k_out = c.rows(a[5], "k_out", tokens, kv_heads, dim);
   const ql_norm_rope r = rule_of(c, a[3], a[6], a[7], dim, a[8], a[9]);
   const int64_t* positions = c.i64(a[2], "positions", tokens);
+  const OnDevice on(c);
   return qlinear_qk_norm_rope(&r, tokens, static_cast<int32_t>(q_heads), static_cast<int32_t>(kv_heads),
                               static_cast<int32_t>(dim), &q, &k, positions, &q_out, &k_out, c.stream(a[10]));
 }
 
-// q, k, v, positions, slots, cos_sin, q_out, cache, q_weight, k_weight, eps, interleaved, stream
+// q, k, v, positions, slots, cos_sin, q_out, cache, cache device, q_weight, k_weight, eps, interleaved, stream
 int64_t qkv_append(PyObject* const* a) {
   Call c;
   const ql_kv_cache* cache = static_cast<const ql_kv_cache*>(Call::number_ptr(a[7]));
@@ -142,38 +161,41 @@ int64_t qkv_append(PyObject* const* a) {
   } else {
     q_heads = 0;
   }
-  const ql_norm_rope r = rule_of(c, a[5], a[8], a[9], dim, a[10], a[11]);
+  c.cache(a[7], a[8]);
+  const ql_norm_rope r = rule_of(c, a[5], a[9], a[10], dim, a[11], a[12]);
   const int64_t* positions = c.i64(a[3], "positions", tokens);
   const int64_t* slots = c.i64(a[4], "slots", tokens);
+  const OnDevice on(c);
   return qlinear_qkv_append(&r, tokens, static_cast<int32_t>(q_heads), &q, &k, &v, positions, slots, &q_out, cache,
-                            c.stream(a[12]));
+                            c.stream(a[13]));
 }
 
-// plan, batch, tokens, q_heads, head_dim, columns, workspace bytes, q, cache, page_table, seq_lens, cu_q, out, lse,
-// workspace, stream
+// plan, batch, tokens, q_heads, head_dim, columns, workspace bytes, q, cache, cache device, page_table, seq_lens, cu_q,
+// out, lse, workspace, stream
 int64_t attention(PyObject* const* a) {
   Call c;
   const int64_t batch = number(a[1]), columns = number(a[5]), need = number(a[6]);
   int64_t tokens = number(a[2]), q_heads = number(a[3]), dim = number(a[4]);
-  const ql_rows q = c.rows(a[7], "q", tokens, q_heads, dim), out = c.rows(a[12], "out", tokens, q_heads, dim);
-  const int32_t* table = c.i32(a[9], "page_table", 0);
-  const at::Tensor& t = THPVariable_Unpack(a[9]);
+  const ql_rows q = c.rows(a[7], "q", tokens, q_heads, dim), out = c.rows(a[13], "out", tokens, q_heads, dim);
+  const ql_kv_cache* cache = c.cache(a[8], a[9]);
+  const int32_t* table = c.i32(a[10], "page_table", 0);
+  const at::Tensor& t = THPVariable_Unpack(a[10]);
   if (t.dim() != 2 || t.size(0) < batch || t.size(1) < columns) {
     PyErr_Format(PyExc_ValueError, "page_table must be a [batch, columns] tensor of at least (%lld, %lld)",
                  (long long)batch, (long long)columns);
     throw Refused();
   }
-  const int32_t* lens = c.i32(a[10], "seq_lens", batch);
-  const int32_t* cu = c.i32(a[11], "cu_q", batch + 1);
-  float* lse = a[13] == Py_None ? nullptr : c.f32(a[13], "lse", tokens * q_heads);
+  const int32_t* lens = c.i32(a[11], "seq_lens", batch);
+  const int32_t* cu = c.i32(a[12], "cu_q", batch + 1);
+  float* lse = a[14] == Py_None ? nullptr : c.f32(a[14], "lse", tokens * q_heads);
   void* workspace = nullptr;
-  if (a[14] != Py_None)
-    workspace = c.bytes(a[14], "workspace", need);
+  if (a[15] != Py_None)
+    workspace = c.bytes(a[15], "workspace", need);
   else if (need > 0)
     refuse("workspace", "is required by this plan");
-  return qlinear_attention(static_cast<ql_attention_plan>(Call::number_ptr(a[0])), &q,
-                           static_cast<const ql_kv_cache*>(Call::number_ptr(a[8])), table, t.size(1), lens, cu, &out, lse,
-                           workspace, c.stream(a[15]));
+  const OnDevice on(c);
+  return qlinear_attention(static_cast<ql_attention_plan>(Call::number_ptr(a[0])), &q, cache, table, t.size(1), lens, cu,
+                           &out, lse, workspace, c.stream(a[16]));
 }
 
 // target_probs, draft_probs, draft_tokens, cu_drafts, uniforms, noise, out_tokens, accepted, workspace, stream
@@ -194,6 +216,7 @@ int64_t verify_draft(PyObject* const* a) {
   const float* uniforms = c.f32(a[4], "uniforms", n);
   int32_t* accepted = c.i32(a[7], "accepted", batch);
   void* workspace = c.bytes(a[8], "workspace", qlinear_verify_workspace_bytes(batch, vocab));
+  const OnDevice on(c);
   return qlinear_verify_draft(batch, n, o.size(1) - 1, vocab, target, draft, tokens, cu, uniforms, noise, out, accepted,
                               workspace, c.stream(a[9]));
 }
@@ -219,8 +242,8 @@ PyMethodDef method(const char* name) {
   return PyMethodDef{name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(&entry<F, N>)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef kMethods[] = {method<qk_norm_rope, 11>("qk_norm_rope"), method<qkv_append, 13>("qkv_append"),
-                          method<attention, 16>("attention"), method<verify_draft, 10>("verify_draft"),
+PyMethodDef kMethods[] = {method<qk_norm_rope, 11>("qk_norm_rope"), method<qkv_append, 14>("qkv_append"),
+                          method<attention, 17>("attention"), method<verify_draft, 10>("verify_draft"),
                           {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", "Serving operators on torch tensors", -1, kMethods,

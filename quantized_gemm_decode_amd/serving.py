@@ -80,7 +80,7 @@ class PagedCache:
         self.struct = QLKvCache(*ptr, *k.stride()[:3], *v.stride()[:3], self.num_pages, self.kv_type, self.page_size,
                                 self.kv_heads, self.head_dim)
         self.address = ctypes.addressof(self.struct)
-        self.on_gpu = k.is_cuda
+        self.on_gpu, self.device_index = k.is_cuda, k.get_device()
 
 
 def rope_table(max_pos, rot_dim, base=1e4, device="cuda"):
@@ -106,8 +106,8 @@ def qlinear_qkv_append(q, k, v, positions, slots, cos_sin, q_out, cache, q_weigh
     cache, v into the cache as it is, at slots (page * page_size + place)."""
     if not cache.on_gpu:
         raise ValueError("the cache must be on the GPU")
-    st = (_module or _binding()).qkv_append(q, k, v, positions, slots, cos_sin, q_out, cache.address, q_weight, k_weight,
-                                            eps, interleaved, _stream(stream))
+    st = (_module or _binding()).qkv_append(q, k, v, positions, slots, cos_sin, q_out, cache.address, cache.device_index,
+                                            q_weight, k_weight, eps, interleaved, _stream(stream))
     if st:
         _lib_check(st, "qlinear_qkv_append")
 
@@ -157,8 +157,8 @@ def qlinear_attention(plan, q, cache, page_table, seq_lens, cu_q, out, lse=None,
     page_table int32 [batch, columns], seq_lens int32 [batch], cu_q int32 [batch + 1]."""
     if not cache.on_gpu:
         raise ValueError("the cache must be on the GPU")
-    st = (_module or _binding()).attention(*plan._args, q, cache.address, page_table, seq_lens, cu_q, out, lse, workspace,
-                                           _stream(stream))
+    st = (_module or _binding()).attention(*plan._args, q, cache.address, cache.device_index, page_table, seq_lens, cu_q, out,
+                                           lse, workspace, _stream(stream))
     if st:
         _lib_check(st, "qlinear_attention")
 

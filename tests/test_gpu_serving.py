@@ -567,3 +567,19 @@ def test_an_empty_table_gives_nan_rows():
     qo, ko = torch.zeros_like(q).contiguous(), torch.zeros_like(k).contiguous()
     ql.qlinear_qk_norm_rope(q, k, pos, ql.rope_table(0, 64), qo, ko, qw, kw)
     assert torch.isnan(qo).all() and torch.isnan(ko).all()
+
+
+def test_a_cache_on_another_device_is_refused():
+    q, k, v, qw, kw = head_inputs(1, 2, 4, 2, 64, True)
+    p = Problem(1, [1, 1], [90, 40], 4, 2, 64, 16, False)
+    plan = p.plan()
+    out = torch.zeros(2, 4, 64, dtype=BF16, device="cuda")
+    pos, slots, table = torch.zeros(2, dtype=torch.int64).cuda(), torch.tensor([0, 1]).cuda(), ql.rope_table(8, 64)
+    p.cache.device_index = torch.cuda.current_device() + 1
+    with pytest.raises(ValueError, match="cache"):
+        ql.qlinear_qkv_append(q, k, v, pos, slots, table, torch.zeros_like(q), p.cache, qw, kw)
+    with pytest.raises(ValueError, match="cache"):
+        ql.qlinear_qkv_append(None, k, v, pos, slots, table, None, p.cache, qw, kw)
+    with pytest.raises(ValueError, match="cache"):
+        ql.qlinear_attention(plan, p.q, p.cache, p.table.cuda(), p.lens.cuda(), p.cu.cuda(), out,
+                             workspace=plan.new_workspace())
