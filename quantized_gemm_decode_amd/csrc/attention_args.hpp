@@ -45,14 +45,15 @@ struct AttnArgs {
   const int32_t* seq_lens;
   const int32_t* cu_q;
   float* lse;            // [tokens, q_heads] or null
-  float* part_o;         // partial outputs of head_dim values a row: [units, splits, R] rows of the tile
-                         // kernel, [slots, 2, kv_heads, R] rows of the stream kernel
+  float* part_o;         // partial outputs of head_dim values a row: [kv_heads, splits, tokens * group] rows of
+                         // the tile kernel, [slots, 2, kv_heads, R] rows of the stream kernel
   float* part_ml;        // their rows' maxima (base 2) and sums
   uint64_t page_magic;
   float scale_log2;      // softmax scale * log2(e)
   int batch, tokens, q_heads, kv_heads, group, page_size, num_pages, max_kv, causal, window;
   // tile kernel
-  int row_blocks;        // blocks of R (token, head of the group) rows of a sequence and KV head
+  int row_blocks;        // most blocks of R (token, head of the group) rows of a sequence and KV head
+  int by_rows;           // numbering of the units (see unit_at)
   int splits, chunk;     // most chunks of keys of a unit, and their length
   int min_rows;          // sequences with fewer rows are left to the stream kernel
   // stream kernel
@@ -97,7 +98,7 @@ int attn_stream_slots(int head_dim, bool e4m3, int rows, int kv_heads, int heads
 hipError_t launch_attn_stream(const AttnArgs& a, int head_dim, bool e4m3, int rows, hipStream_t s);
 hipError_t launch_attn_stream_join(const AttnArgs& a, int head_dim, int rows, int most_rows, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, bool e4m3, int units, hipStream_t s);
-hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, int batch, hipStream_t s);
+hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
 
 }  // namespace qlk

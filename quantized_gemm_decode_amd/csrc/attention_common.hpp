@@ -71,29 +71,57 @@ __device__ __forceinline__ float row4_sum(float v) {
 // A table or length entry at a wave-uniform address.
 __device__ __forceinline__ int uniform_i32(const int32_t* p) { return __builtin_amdgcn_readfirstlane(*p); }
 
+__device__ __forceinline__ int lane_i32(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
+
+// Sequence b of the batch: its new tokens [first, end) of q and its cached
+// length; every field is wave-uniform.  b < 0: none.
+struct Sequence {
+  int b, first, end, len;
+};
+
+// The last sequence with start(b, its first token) <= n, for starts that do
+// not fall from one sequence to the next: 64 probes at once, so one round of
+// loads for up to 64 sequences, two up to 4,096.  Whatever cu_q holds, the
+// answer is a sequence of the batch or none.
+template <class F>
+__device__ __forceinline__ Sequence sequence_at(const AttnArgs& a, int n, F start) {
+  const int lane = threadIdx.x & 63;
+  for (int lo = 0, width = a.batch;;) {
+    const int step = (width + 63) >> 6, b = min(lo + lane * step, a.batch - 1);
+    const int q0 = min(max(a.cu_q[b], 0), a.tokens), q1 = min(max(a.cu_q[b + 1], q0), a.tokens);
+    const int len = min(max(a.seq_lens[b], 0), a.max_kv);
+    const unsigned long long before = __ballot(lane * step < width && start(b, q0) <= n);
+    if (before == 0) return Sequence{-1, 0, 0, 0};
+    const int i = 63 - __clzll((long long)before);
+    if (step == 1) return Sequence{lo + i, lane_i32(q0, i), lane_i32(q1, i), lane_i32(len, i)};
+    lo += i * step;
+    width = min(step, width - i * step);
+  }
+}
+
 // The rows and keys of one unit; every field is wave-uniform.
 struct Unit {
+  int b;         // its sequence
   int first;     // the sequence's first token in q
-  int rows;      // rows of this block
+  int rows;      // rows of this block (0: nothing to do)
   int row0;      // first row of the block
   int pos0;      // position of the sequence's first new token
   int len;       // cached length (keys beyond it are never read)
   int lo, hi;    // keys any row of the block sees: [lo, hi)
   int chunks;    // chunks of keys, from lo rounded down to 64
-  int all;       // rows of the sequence
 };
 
-__device__ __forceinline__ Unit unit_of(const AttnArgs& a, int b, int block, int R) {
+// Block `block` of sequence s.  Sequences that are left to the stream kernel,
+// and blocks beyond the plan's, have no rows.
+__device__ __forceinline__ Unit unit_of(const AttnArgs& a, const Sequence& s, int block, int R) {
   Unit u;
-  int q0 = uniform_i32(a.cu_q + b), q1 = uniform_i32(a.cu_q + b + 1);
-  q0 = min(max(q0, 0), a.tokens);
-  q1 = min(max(q1, q0), a.tokens);
-  u.len = min(max(uniform_i32(a.seq_lens + b), 0), a.max_kv);
-  u.first = q0;
-  u.all = (q1 - q0) * a.group;
+  const int n = s.end - s.first, all = n * a.group;
+  u.b = s.b;
+  u.len = s.len;
+  u.first = s.first;
   u.row0 = block * R;
-  u.rows = min(max(u.all - u.row0, 0), R);
-  u.pos0 = u.len - (q1 - q0);
+  u.rows = s.b < 0 || all < a.min_rows || block < 0 || block >= a.row_blocks ? 0 : min(max(all - u.row0, 0), R);
+  u.pos0 = u.len - n;
   u.hi = u.len;
   u.lo = 0;
   if (u.rows > 0) {
@@ -106,6 +134,31 @@ __device__ __forceinline__ Unit unit_of(const AttnArgs& a, int b, int block, int
   const int lo64 = u.lo & ~63;
   u.chunks = u.hi > u.lo ? (u.hi - lo64 + a.chunk - 1) / a.chunk : 0;
   return u;
+}
+
+// Unit n of the batch, in one of two numberings, a sequence's last block (the
+// longest) first.  Sequence by sequence, row_blocks numbers each.  Or by the
+// rows before them (a.by_rows): sequence b's numbers follow from floor(rows
+// before it / R) + b, which leaves room for every sequence's ceil(rows / R)
+// blocks in rows / R + batch numbers, whatever the lengths, and a number's
+// sequence is found by search.
+__device__ __forceinline__ Unit unit_at(const AttnArgs& a, int n, int R) {
+  if (!a.by_rows) {
+    const int b = n / a.row_blocks;
+    const int q0 = min(max(uniform_i32(a.cu_q + b), 0), a.tokens), q1 = min(max(uniform_i32(a.cu_q + b + 1), q0), a.tokens);
+    const Sequence s = {b, q0, q1, min(max(uniform_i32(a.seq_lens + b), 0), a.max_kv)};
+    return unit_of(a, s, a.row_blocks - 1 - n % a.row_blocks, R);
+  }
+  auto start = [&](int b, int q0) { return q0 * a.group / R + b; };
+  const Sequence s = sequence_at(a, n, start);
+  const int blocks = min(((s.end - s.first) * a.group + R - 1) / R, a.row_blocks);
+  return unit_of(a, s, blocks - 1 - (n - start(s.b, s.first)), R);
+}
+
+// Where the partial results of one row over chunk `split` lie: rows of all
+// tokens, for each chunk and KV head.
+__device__ __forceinline__ int64_t part_at(const AttnArgs& a, int h, int split, int row) {
+  return ((int64_t)h * a.splits + split) * ((int64_t)a.tokens * a.group) + row;
 }
 
 // Keys [lo, hi) that row r of the block sees.

@@ -134,8 +134,6 @@ __device__ __forceinline__ int inclusive_sum(int v) {
   return v;
 }
 
-__device__ __forceinline__ int lane_i32(int v, int i) { return __builtin_amdgcn_readlane(v, i); }
-
 // All sequences' tiles, and how they are cut: `slots` slots of `each` tiles,
 // the first `more` of them one longer.  A sequence takes room for a multiple of
 // 2^pad tiles.
@@ -569,24 +567,19 @@ __global__ void __launch_bounds__(kJoinWaves * 64) attn_stream_join_kernel(AttnA
                      mine.first + row / a.group, h * a.group + row % a.group);
 }
 
-// The tile kernel's units that were cut into chunks: one wave a row.
+// The tile kernel's units that were cut into chunks: one wave a row of a KV
+// head (new token, query head of the group).
 template <int D>
 __global__ void __launch_bounds__(kJoinWaves * 64) attn_join_kernel(AttnArgs a, int R) {
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  int id = blockIdx.x;
-  const int h = id % a.kv_heads;
-  id /= a.kv_heads;
-  const int per = R / kJoinWaves;
-  const int row = (id % per) * kJoinWaves + wave;
-  id /= per;
-  const int block = id % a.row_blocks, b = id / a.row_blocks;
-  const Unit u = unit_of(a, b, block, R);
-  if (row >= u.rows || u.chunks <= 1 || u.all < a.min_rows) return;
-  const int64_t unit = ((int64_t)b * a.row_blocks + block) * a.kv_heads + h;
-  const int64_t first = unit * a.splits * R + row;
-  const int place = u.row0 + row;
-  join_row<D, 1>(a, first, first + R, R, min(u.chunks, a.splits), u.first + place / a.group,
-                 h * a.group + place % a.group);
+  const int h = (int)blockIdx.x % a.kv_heads, at = (int)blockIdx.x / a.kv_heads * kJoinWaves + wave;
+  if (at >= a.tokens * a.group) return;
+  const Sequence s = sequence_at(a, at, [&](int, int q0) { return q0 * a.group; });
+  const int row = at - s.first * a.group;  // of the sequence
+  const Unit u = unit_of(a, s, row / R, R);
+  if (row - u.row0 >= u.rows || u.chunks <= 1) return;
+  const int64_t first = part_at(a, h, 0, at), step = (int64_t)a.tokens * a.group;
+  join_row<D, 1>(a, first, first + step, step, min(u.chunks, a.splits), at / a.group, h * a.group + at % a.group);
 }
 
 template <int D, bool E4M3, int NR>
@@ -632,8 +625,8 @@ hipError_t launch_attn_stream_join(const AttnArgs& a, int head_dim, int rows, in
   return hipGetLastError();
 }
 
-hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, int batch, hipStream_t s) {
-  const unsigned grid = (unsigned)batch * (unsigned)a.row_blocks * (unsigned)a.kv_heads * (unsigned)(rows / kJoinWaves);
+hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, hipStream_t s) {
+  const unsigned grid = (unsigned)((a.tokens * a.group + kJoinWaves - 1) / kJoinWaves) * (unsigned)a.kv_heads;
   if (head_dim == 64)
     hipLaunchKernelGGL((attn_join_kernel<64>), dim3(grid), dim3(kJoinWaves * 64), 0, s, a, rows);
   else

@@ -311,10 +311,8 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
   const int h = id % a.kv_heads;
   id /= a.kv_heads;
   const int split = id % a.splits;
-  id /= a.splits;
-  const int block = a.row_blocks - 1 - id % a.row_blocks, b = id / a.row_blocks;  // the longest first
-  const Unit u = unit_of(a, b, block, R);
-  if (u.rows == 0 || u.all < a.min_rows) return;
+  const Unit u = unit_at(a, id / a.splits, R);
+  if (u.rows == 0) return;
   if (u.chunks == 0 ? split != 0 : split >= u.chunks) return;
   const int begin = (u.lo & ~63) + split * a.chunk;
   const int end = min(u.hi, begin + a.chunk);
@@ -349,7 +347,7 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
     row_range(a, u, u.rows - 1, &full_lo, &x);
     row_range(a, u, 0, &x, &full_hi);
     full_hi = min(full_hi, end);
-    const int32_t* table = a.table + b * a.table_row;
+    const int32_t* table = a.table + u.b * a.table_row;
     const int last_sub = (u.len - 1) >> 4;
     using S = Staged<D, E4M3>;
     const uint32_t k_lane = (uint32_t)(lane / S::CH * (int)a.kc.token + lane % S::CH * 16);
@@ -516,8 +514,7 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
     if (a.lse && g == 0)
       a.lse[(int64_t)tok * a.q_heads + head] = w.m == kNegInf ? kNegInf : (w.m + log2f(sum)) * 0.6931471805599453f;
   } else {
-    const int64_t unit = ((int64_t)b * a.row_blocks + block) * a.kv_heads + h;
-    const int64_t part = (unit * a.splits + split) * R + row;
+    const int64_t part = part_at(a, h, split, u.first * a.group + place);
     float* out = a.part_o + part * D + 4 * g;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)

@@ -583,3 +583,18 @@ def test_a_cache_on_another_device_is_refused():
     with pytest.raises(ValueError, match="cache"):
         ql.qlinear_attention(plan, p.q, p.cache, p.table.cuda(), p.lens.cuda(), p.cu.cuda(), out,
                              workspace=plan.new_workspace())
+
+
+@pytest.mark.parametrize("batch,D,e4m3,max_q,max_kv", [(130, 64, False, None, None), (70, 128, True, 500, 3000),
+                                                       (5, 64, False, 2000, 9000), (200, 64, True, 41, 4000)])
+def test_attention_of_chunks_in_ragged_batches(batch, D, e4m3, max_q, max_kv):
+    """Many sequences of none, few and many new tokens, bounds far above them,
+    with keys in one chunk and in several."""
+    new = [(0, 40, 1, 9, 0, 33, 130 if max_q != 41 else 41)[i % 7] for i in range(batch)]
+    p = Problem(90 + batch, new, [max(3, n) + (i * 7919) % 200 for i, n in enumerate(new)], 4, 2, D, 16, e4m3)
+    cols = -(-(max_kv or 0) // 16)
+    p.table = torch.nn.functional.pad(p.table, (0, max(0, cols - p.table.shape[1])), value=-7)
+    plan = p.plan(max_q=max_q, max_kv=max_kv)
+    assert plan.facts["tile_rows"] == 128
+    out, ls = p.run(plan)
+    p.check(out, ls)

@@ -198,3 +198,19 @@ def test_struct_sizes_match_the_header(tmp_path):
                     str(tmp_path / "s")], check=True)
     got = subprocess.run([str(tmp_path / "s")], capture_output=True, text=True, check=True).stdout.split()
     assert [int(x) for x in got] == [ctypes.sizeof(s) for s in names.values()]
+
+
+def test_attention_workspace_follows_the_rows_there_are():
+    """Partial results are kept for rows that exist: a binary32 output, maximum
+    and sum for each chunk, whatever the longest sequence's bound is."""
+    def facts(**kw):
+        return ql.AttentionPlan(shape(**kw)).facts
+    for kw in (dict(batch=32, tokens=2079, max_q=2048, max_kv=32768), dict(batch=16, tokens=2367, max_q=2048, max_kv=32768),
+               dict(batch=256, tokens=8447, max_q=8192, max_kv=65536), dict(batch=1, tokens=64, max_q=64, max_kv=32768)):
+        f = facts(**kw)
+        decode = 2 * 8 * f["slots"] * 16 * (128 + 2) * 4 if f["stream_rows"] else 0
+        tile = kw["tokens"] * 32 * f["splits"] * (128 + 2) * 4 if f["splits"] > 1 else 0
+        assert f["workspace_bytes"] == decode + tile, kw
+    # a bound of more new tokens than the call has tokens is that many
+    assert facts(batch=1, tokens=64, max_q=8192, max_kv=32768) == facts(batch=1, tokens=64, max_q=64, max_kv=32768)
+    assert facts(batch=1, tokens=5, max_q=100)["tile_rows"] == 0
