@@ -142,6 +142,9 @@ constexpr int64_t kMixedRows = 16;
 
 constexpr int kTileRows = 128;
 
+// A grid's extent is a 32-bit number of threads, 256 a workgroup.
+constexpr int64_t kMaxWorkgroups = int64_t(1) << 24;
+
 // Chunk of the tile kernel.  A workgroup runs at its own pace, 512 of them at a
 // time (two a compute unit).  Measured in ns a key: 19 while every workgroup has
 // a compute unit to itself, 33 when two share one (64-wide heads: 14 and 23.5);
@@ -198,9 +201,11 @@ ql_status plan_tile(const ql_attention_shape& s, int64_t rows, int64_t at, Part*
   const int64_t span = tile_span(s);
   const int64_t chunk = tile_chunk(s.head_dim, s.batch, units, span);
   const int64_t splits = std::max<int64_t>(1, (span + chunk - 1) / chunk);
-  if (units * splits >= (int64_t(1) << 31) || s.tokens * s.q_heads >= (int64_t(1) << 31))
-    return fail(QL_E_UNSUPPORTED, "more than 2^31 workgroups");
+  if (s.tokens * s.q_heads >= (int64_t(1) << 31)) return fail(QL_E_UNSUPPORTED, "tokens * q_heads exceeds 2^31");
   const int64_t parts = splits > 1 ? s.tokens * s.q_heads * splits : 0;
+  // both launches fit a grid (the join's: a wave a row), or neither is made
+  if (units * splits >= kMaxWorkgroups || (parts && s.tokens * s.q_heads / 4 + s.kv_heads >= kMaxWorkgroups))
+    return fail(QL_E_UNSUPPORTED, "2^24 workgroups or more");
   p->used = true;
   p->rows = (int)R;
   p->row_blocks = (int)blocks;

@@ -214,3 +214,11 @@ def test_attention_workspace_follows_the_rows_there_are():
     # a bound of more new tokens than the call has tokens is that many
     assert facts(batch=1, tokens=64, max_q=8192, max_kv=32768) == facts(batch=1, tokens=64, max_q=64, max_kv=32768)
     assert facts(batch=1, tokens=5, max_q=100)["tile_rows"] == 0
+
+
+def test_attention_plans_that_no_grid_holds_are_refused():
+    """2^24 workgroups of 256 threads are 2^32 threads, one more than a launch takes."""
+    most = dict(tokens=1 << 18, max_q=128, max_kv=64, q_heads=4096, kv_heads=4096)
+    assert plan_status(batch=4095, **most) == OK
+    assert plan_status(batch=4096, **most) == UNSUPPORTED
+    assert "workgroups" in ql.lib().qlinear_last_error().decode()
