@@ -610,13 +610,15 @@ ql_status qlinear_qkv_append(const ql_norm_rope* rule, int64_t tokens, int32_t q
  * only); not causal: all of them.  Query head h reads KV head h / (q_heads /
  * kv_heads):
  *   out[t, h] = sum_j softmax_j(scale q[t, h] . k_j) v_j
- * A row that sees nothing is 0 with lse -inf.  lse (binary32 [tokens,
- * q_heads], natural logarithm of the sum of exponentials) may be NULL.  Rows of
- * q outside [cu_q[0], cu_q[batch]) are not written.  What the cache holds
- * beyond a sequence's length may be anything, NaN included, and an infinity or
- * NaN in a key or value never reaches a row that does not see it (a row that
- * sees one gets non-finite outputs); page-table entries beyond a sequence's
- * pages do not matter.  Memory safety does not depend on the device
+ * A row without a score above -inf (as a rule, one that sees nothing) is 0 with
+ * lse -inf.  lse (binary32 [tokens, q_heads], natural logarithm of the sum of
+ * exponentials) may be NULL.  Rows of q outside [cu_q[0], cu_q[batch]) are not
+ * written.  What the cache holds beyond a sequence's length may be anything, NaN
+ * included, and an infinity or NaN in a key or value never reaches a row that
+ * does not see it.  A row that sees one has non-finite outputs: of a value, in
+ * the value's place; of a key, everywhere, with NaN for lse, unless the score is
+ * -inf, which only has no weight.  Page-table entries beyond a sequence's pages
+ * do not matter.  Memory safety does not depend on the device
  * arrays: lengths are clamped to max_kv, pages to the cache, cu_q to
  * [0, tokens].
  *

@@ -68,6 +68,12 @@ __device__ __forceinline__ float row4_sum(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
+// A row's lse from its maximum (base 2, -inf: no score above -inf) and sum.  Where
+// all scores are NaN the maximum has not moved either, but the sum is NaN.
+__device__ __forceinline__ float lse_of(float m, float sum) {
+  return m == kNegInf && sum == sum ? kNegInf : (m + log2f(sum)) * 0.6931471805599453f;
+}
+
 // A table or length entry at a wave-uniform address.
 __device__ __forceinline__ int uniform_i32(const int32_t* p) { return __builtin_amdgcn_readfirstlane(*p); }
 

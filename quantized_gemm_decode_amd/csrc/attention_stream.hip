@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
             a.part_ml[(part + row) * 2] = m[n];
             a.part_ml[(part + row) * 2 + 1] = sum;
           } else if (a.lse) {
-            a.lse[(int64_t)tok * a.q_heads + head] = m[n] == kNegInf ? kNegInf : (m[n] + log2f(sum)) * 0.6931471805599453f;
+            a.lse[(int64_t)tok * a.q_heads + head] = lse_of(m[n], sum);
           }
         }
       }
@@ -534,7 +534,7 @@ __device__ __forceinline__ void join_row(const AttnArgs& a, int64_t first, int64
     *reinterpret_cast<u32x2*>(a.out.p + (int64_t)tok * a.out.token + (int64_t)head * a.out.head + d0 * 2) =
         u32x2{bf16_pair(p.x[0] * inv, p.x[1] * inv), bf16_pair(p.x[2] * inv, p.x[3] * inv)};
   if (a.lse && id == 0)
-    a.lse[(int64_t)tok * a.q_heads + head] = p.m == kNegInf ? kNegInf : (p.m + log2f(p.l)) * 0.6931471805599453f;
+    a.lse[(int64_t)tok * a.q_heads + head] = lse_of(p.m, p.l);
 }
 
 constexpr int kJoinWaves = 4;

@@ -512,7 +512,7 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
             u32x2{bf16_pair(c[4 * i] * inv, c[4 * i + 1] * inv), bf16_pair(c[4 * i + 2] * inv, c[4 * i + 3] * inv)};
       }
     if (a.lse && g == 0)
-      a.lse[(int64_t)tok * a.q_heads + head] = w.m == kNegInf ? kNegInf : (w.m + log2f(sum)) * 0.6931471805599453f;
+      a.lse[(int64_t)tok * a.q_heads + head] = lse_of(w.m, sum);
   } else {
     const int64_t part = part_at(a, h, split, u.first * a.group + place);
     float* out = a.part_o + part * D + 4 * g;

@@ -598,3 +598,40 @@ def test_attention_of_chunks_in_ragged_batches(batch, D, e4m3, max_q, max_kv):
     assert plan.facts["tile_rows"] == 128
     out, ls = p.run(plan)
     p.check(out, ls)
+
+
+NAN_SCORE_CASES = [(2, 40, 40, 0), (3, 3000, 3000, 0), (40, 200, 200, 0), (40, 9000, 9000, 0), (6, 300, 300, 20)]
+
+
+@pytest.mark.parametrize("new,kv,max_kv,window", NAN_SCORE_CASES)
+def test_lse_of_rows_whose_scores_are_nan(new, kv, max_kv, window):
+    """A row of NaN scores has a NaN output and a NaN lse (-inf says that a row
+    sees nothing); the other rows keep theirs."""
+    p = Problem(61, [new], [kv], 4, 2, 64, 16, False)
+    plan = p.plan(window=window, max_kv=max_kv)
+    clean, clean_lse = p.run(plan)
+    q = p.q
+    p.q = q.clone()
+    p.q[new - 1, 1, 7] = float("nan")
+    out, lse = p.run(plan)
+    p.q = q
+    hit = torch.zeros(new, 4, dtype=torch.bool, device="cuda")
+    hit[new - 1, 1] = True
+    assert torch.isnan(out[hit]).all() and torch.isnan(lse[hit]).all()
+    out[hit], lse[hit] = clean[hit], clean_lse[hit]
+    p.check(out, lse, window=window)
+
+
+@pytest.mark.parametrize("new,kv", [(5, 70), (6, 3000), (40, 130), (40, 9000)])
+def test_lse_of_rows_that_see_a_nan_key(new, kv):
+    p = Problem(62, [new], [kv], 4, 2, 128, 16, True)
+    plan = p.plan()
+    out, clean = p.run(plan)
+    at = kv - 2
+    p.k[int(p.table[0, at // 16]), at % 16, 1, 9] = torch.tensor(float("nan")).to(E4M3).cuda()
+    _, lse = p.run(plan)
+    hit = torch.zeros(new, 4, dtype=torch.bool, device="cuda")
+    hit[new - 2:, 2:] = True
+    assert torch.isnan(lse[hit]).all()
+    lse[hit] = clean[hit]
+    p.check(out, lse)
