@@ -79,8 +79,10 @@ def attention(q, k, v, page_table, seq_lens, cu_q, page_size, scale, causal=True
 def verify(target, draft, tokens, cu, uniforms, noise, max_drafts):
     """-> (out_tokens [batch, max_drafts + 1], accepted [batch]).  The
     comparisons are those of the binary32 definition: one rounded product,
-    difference and quotient each."""
+    difference and quotient each.  A NaN probability counts as 0."""
     f32 = np.float32
+    target = np.where(np.isnan(target), f32(0), target)
+    draft = None if draft is None else np.where(np.isnan(draft), f32(0), draft)
     batch, vocab = noise.shape
     out, accepted = np.full((batch, max_drafts + 1), -1, np.int32), np.zeros(batch, np.int32)
     for b in range(batch):

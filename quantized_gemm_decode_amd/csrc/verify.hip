@@ -28,6 +28,10 @@ namespace qlk {
 
 constexpr int kVerifyThreads = 256;
 
+// A draft's probability; NaN counts as 0.  (The target's needs no test: as 0 it
+// accepts nothing and leaves no weight, and so do the comparisons with NaN.)
+__device__ __forceinline__ float draft_prob(float q) { return q == q ? q : 0.0f; }
+
 // Accepted drafts of a sequence, by the lanes of a wave: drafts in groups of
 // 64, one a lane, the first rejection by ballot.
 __device__ __forceinline__ int accepted_drafts(const VerifyArgs& a, int64_t first, int n, int b) {
@@ -39,7 +43,7 @@ __device__ __forceinline__ int accepted_drafts(const VerifyArgs& a, int64_t firs
       const int64_t x = a.tokens[first + i];
       const bool known = x >= 0 && x < a.vocab;  // a token outside the vocabulary is rejected
       const float p = known ? a.target[(first + i + b) * a.vocab + x] : 0.0f;
-      const float q = known && a.draft ? a.draft[(first + i) * a.vocab + x] : 1.0f;
+      const float q = known && a.draft ? draft_prob(a.draft[(first + i) * a.vocab + x]) : 1.0f;
       ok = __fmul_rn(a.uniforms[first + i], q) < p;
     }
     const unsigned long long no = __ballot(!ok);
@@ -60,8 +64,7 @@ __device__ __forceinline__ int draft_range(const VerifyArgs& a, int b, int64_t* 
 // A weight's score and index as one word whose maximum is the larger score
 // and, between equals, the lower index; 0 for no positive score.  Positive
 // binary32 values order as their bit patterns.
-__device__ __forceinline__ uint64_t score_key(float weight, float noise, uint32_t v) {
-  const float s = __fdiv_rn(weight, noise);
+__device__ __forceinline__ uint64_t score_key(float s, uint32_t v) {
   return s > 0.0f ? ((uint64_t)__float_as_uint(s) << 32) | (0xffffffffu - v) : 0u;
 }
 
@@ -77,7 +80,9 @@ struct Weights {
   const float* p;
   const float* q;  // null: nothing is subtracted but `certain`
   int certain;     // a certain draft (q = 1), else -1
-  __device__ __forceinline__ float at(float p, float q, int v) const { return fmaxf(p - (v == certain ? 1.0f : q), 0.0f); }
+  __device__ __forceinline__ float at(float p, float q, int v) const {
+    return fmaxf(p - (v == certain ? 1.0f : draft_prob(q)), 0.0f);
+  }
 };
 
 __device__ __forceinline__ Weights weights_of(const VerifyArgs& a, int64_t first, int n, int k, int b, bool diff) {
@@ -133,7 +138,9 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_scan_kernel(VerifyArgs 
       if (i != k) out[i] = i < k ? a.tokens[first + i] : -1;
     if (threadIdx.x == 0) a.accepted[b] = k;
   }
-  uint64_t best = 0;
+  // a thread's entries come in rising order: the first of the largest is kept
+  float top = 0.0f;
+  int top_at = 0;
 #pragma unroll
   for (int i = 0; i < U; ++i) {
     const int v = v0 + (i * kVerifyThreads + (int)threadIdx.x) * 4;
@@ -141,10 +148,14 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_scan_kernel(VerifyArgs 
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int at = min(v, last) + j;
-      if (at < a.vocab) best = max_u64(best, score_key(w.at(p[i][j], w.q ? q[i][j] : 0.0f, at), noise[i][j], (uint32_t)at));
+      const float s = __fdiv_rn(w.at(p[i][j], w.q ? q[i][j] : 0.0f, at), noise[i][j]);
+      if (at < a.vocab && s > top) {
+        top = s;
+        top_at = at;
+      }
     }
   }
-  best = wave_max_u64(best);
+  uint64_t best = wave_max_u64(score_key(top, (uint32_t)top_at));
   __shared__ uint64_t part[kVerifyThreads / 64];
   if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = best;
   __syncthreads();
@@ -166,7 +177,7 @@ __global__ void __launch_bounds__(64) verify_pick_kernel(VerifyArgs a) {
     const int n = draft_range(a, b, &first);
     const Weights w = weights_of(a, first, n, k, b, false);
     for (int v = lane; v < a.vocab; v += 64)
-      best = max_u64(best, score_key(w.at(w.p[v], 0.0f, v), a.noise[(int64_t)b * a.vocab + v], (uint32_t)v));
+      best = max_u64(best, score_key(__fdiv_rn(w.at(w.p[v], 0.0f, v), a.noise[(int64_t)b * a.vocab + v]), (uint32_t)v));
     best = wave_max_u64(best);
   }
   if (lane == 0)

@@ -635,3 +635,29 @@ def test_lse_of_rows_that_see_a_nan_key(new, kv):
     assert torch.isnan(lse[hit]).all()
     lse[hit] = clean[hit]
     p.check(out, lse)
+
+
+def test_verify_draft_counts_nan_draft_probabilities_as_zero():
+    """At the drafted token (accepted where the target's is positive), elsewhere
+    in a rejected row (the whole of p is left there), and with certain drafts after it."""
+    V = 300
+    nan, zero = float("nan"), np.array([0, 1], np.int32)
+    flat, ones = torch.full((2, V), 1.0 / V), torch.ones(1, V)
+    q = flat[:1].clone()
+    q[0, 7] = nan
+    x = (flat, q, torch.tensor([7], dtype=torch.int32), zero, torch.tensor([0.999]), ones)
+    out, acc = run_verify(*x, 1)
+    assert acc.tolist() == [1] and out.tolist() == [[7, 0]]
+    t = flat.clone()
+    t[0, 7] = 0.0                                            # 0 < 0 is false: rejected
+    assert run_verify(t, *x[1:], 1)[1].tolist() == [0]
+    t, q = flat.clone(), flat[:1].clone()
+    t[0, 3], t[0, 250], q[0, 250] = 0.0, 1.5 / V, nan        # left: 1.5 / V at 250, nothing elsewhere
+    out, acc = run_verify(t, q, torch.tensor([3], dtype=torch.int32), zero, torch.tensor([0.5]), ones, 1)
+    assert acc.tolist() == [0] and out.tolist() == [[250, -1]]
+    for seed in range(3):
+        target, draft, tokens, cu, u, noise = verify_inputs(seed, [3, 2, 4], 801, spread=0.8)
+        draft[torch.rand(draft.shape, generator=torch.Generator().manual_seed(seed)) < 0.2] = nan
+        want = ref.verify(*(np.asarray(y) for y in (target, draft, tokens, cu, u, noise)), 4)
+        got = run_verify(target, draft, tokens, cu, u, noise, 4)
+        assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0]), (seed, got, want)
