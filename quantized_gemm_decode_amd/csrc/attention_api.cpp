@@ -305,6 +305,9 @@ ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan*
   ql_attention_plan_s* p = new (std::nothrow) ql_attention_plan_s();
   if (!p) return fail(QL_E_INVALID, "out of host memory");
   p->shape = *s;
+  // as long as any context: no window (and no position minus the window leaves 32 bits)
+  if (s->window >= s->max_kv) p->shape.window = 0;
+  s = &p->shape;
   const bool chunks = rows > kStreamRows;
   // Sequences of few rows among longer ones get a launch of their own where
   // there can be many of them with long contexts: to the tile kernel each is a

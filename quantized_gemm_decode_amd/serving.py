@@ -149,7 +149,8 @@ def qlinear_attention_plan(cache, q_heads, batch, tokens, max_q, max_kv, causal=
     """Plan for `tokens` new tokens of `batch` sequences, at most max_q of one
     sequence, over contexts of at most max_kv tokens (the new ones included)."""
     return AttentionPlan(QLAttentionShape(batch, tokens, max_q, max_kv, q_heads, cache.kv_heads, cache.head_dim,
-                                          cache.page_size, cache.kv_type, bool(causal), window, scale or 0.0))
+                                          cache.page_size, cache.kv_type, bool(causal),
+                                          max(-1, min(window, 2 ** 31 - 1)), scale or 0.0))
 
 
 def qlinear_attention(plan, q, cache, page_table, seq_lens, cu_q, out, lse=None, workspace=None, stream=None):

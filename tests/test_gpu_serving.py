@@ -661,3 +661,12 @@ def test_verify_draft_counts_nan_draft_probabilities_as_zero():
         want = ref.verify(*(np.asarray(y) for y in (target, draft, tokens, cu, u, noise)), 4)
         got = run_verify(target, draft, tokens, cu, u, noise, 4)
         assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0]), (seed, got, want)
+
+
+@pytest.mark.parametrize("new,kv", [([8], [5]), ([6, 1], [3, 900]), ([200, 4], [100, 700])])
+def test_a_window_as_long_as_can_be_is_no_window(new, kv):
+    """More new tokens than cached ones beside it: positions below zero minus the window do not wrap."""
+    p = Problem(71, new, kv, 4, 2, 64, 16, False)
+    for window in (2 ** 31 - 1, 2 ** 31 - 6, 2 ** 40 + 5):
+        out, ls = p.run(p.plan(window=window))
+        p.check(out, ls)
