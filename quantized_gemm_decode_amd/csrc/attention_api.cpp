@@ -416,7 +416,7 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
 // sequences, at least 1024 entries (4 a thread) each, at most kVerifySlice.
 static int verify_slices(int64_t batch, int64_t vocab) {
   const int64_t most = std::max<int64_t>(1, vocab / 1024), least = (vocab + qlk::kVerifySlice - 8) / (qlk::kVerifySlice - 4);
-  return (int)std::max(least, std::min<int64_t>(most, 1024 / std::max<int64_t>(1, batch)));
+  return (int)std::max<int64_t>({1, least, std::min<int64_t>(most, 1024 / std::max<int64_t>(1, batch))});
 }
 
 int64_t qlinear_verify_workspace_bytes(int64_t batch, int64_t vocab) {

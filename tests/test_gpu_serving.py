@@ -670,3 +670,11 @@ def test_a_window_as_long_as_can_be_is_no_window(new, kv):
     for window in (2 ** 31 - 1, 2 ** 31 - 6, 2 ** 40 + 5):
         out, ls = p.run(p.plan(window=window))
         p.check(out, ls)
+
+
+def test_verify_many_sequences_of_a_tiny_vocabulary():
+    counts, V = [i % 3 for i in range(1500)], 3
+    x = verify_inputs(5, counts, V, spread=0.8)
+    want = ref.verify(*(np.asarray(t) for t in x), 2)
+    got = run_verify(*x, 2)
+    assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])

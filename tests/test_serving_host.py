@@ -222,3 +222,10 @@ def test_attention_plans_that_no_grid_holds_are_refused():
     assert plan_status(batch=4095, **most) == OK
     assert plan_status(batch=4096, **most) == UNSUPPORTED
     assert "workgroups" in ql.lib().qlinear_last_error().decode()
+
+
+def test_verify_workspace_of_tiny_vocabularies():
+    """Every row has a slice, however many sequences there are and short the row is."""
+    for batch in (1, 1024, 1025, 65535):
+        for vocab in (1, 3, 4, 1023):
+            assert ql.qlinear_verify_workspace_bytes(batch, vocab) >= 8 * batch, (batch, vocab)
