@@ -62,6 +62,17 @@ struct Call {
     }
     return static_cast<T*>(t.data_ptr());
   }
+  // The same for rows of `width` elements each (or the elements in one row).
+  float* f32_rows(PyObject* o, const char* name, int64_t n, int64_t width) {
+    float* p = f32(o, name, n * width);
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.dim() > 1 && t.size(-1) != width) {
+      PyErr_Format(PyExc_ValueError, "%s has rows of %lld elements, expected %lld", name, (long long)t.size(-1),
+                   (long long)width);
+      throw Refused();
+    }
+    return p;
+  }
   int32_t* i32(PyObject* o, const char* name, int64_t n) { return flat<int32_t>(o, name, at::kInt, "torch.int32", n); }
   int64_t* i64(PyObject* o, const char* name, int64_t n) { return flat<int64_t>(o, name, at::kLong, "torch.int64", n); }
   float* f32(PyObject* o, const char* name, int64_t n) { return flat<float>(o, name, at::kFloat, "torch.float32", n); }
@@ -187,7 +198,7 @@ int64_t attention(PyObject* const* a) {
   }
   const int32_t* lens = c.i32(a[11], "seq_lens", batch);
   const int32_t* cu = c.i32(a[12], "cu_q", batch + 1);
-  float* lse = a[14] == Py_None ? nullptr : c.f32(a[14], "lse", tokens * q_heads);
+  float* lse = a[14] == Py_None ? nullptr : c.f32_rows(a[14], "lse", tokens, q_heads);
   void* workspace = nullptr;
   if (a[15] != Py_None)
     workspace = c.bytes(a[15], "workspace", need);
@@ -210,8 +221,8 @@ int64_t verify_draft(PyObject* const* a) {
   const int64_t batch = e.size(0), vocab = e.size(1), n = THPVariable_Unpack(a[2]).numel();
   if (o.dim() != 2 || o.size(0) < batch || o.size(1) < 1)
     refuse("out_tokens", "must be a [batch, max_drafts + 1] tensor");
-  const float* target = c.f32(a[0], "target_probs", (n + batch) * vocab);
-  const float* draft = a[1] == Py_None ? nullptr : c.f32(a[1], "draft_probs", n * vocab);
+  const float* target = c.f32_rows(a[0], "target_probs", n + batch, vocab);
+  const float* draft = a[1] == Py_None ? nullptr : c.f32_rows(a[1], "draft_probs", n, vocab);
   const int32_t* cu = c.i32(a[3], "cu_drafts", batch + 1);
   const float* uniforms = c.f32(a[4], "uniforms", n);
   int32_t* accepted = c.i32(a[7], "accepted", batch);

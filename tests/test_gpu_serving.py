@@ -678,3 +678,24 @@ def test_verify_many_sequences_of_a_tiny_vocabulary():
     want = ref.verify(*(np.asarray(t) for t in x), 2)
     got = run_verify(*x, 2)
     assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])
+
+
+def test_rows_of_another_length_are_refused():
+    """Probabilities of a padded vocabulary, and an lse of other heads, hold
+    enough elements but not where the call would read or write them."""
+    target, draft, tokens, cu, u, noise = verify_inputs(3, [2, 1], 50)
+    dev = [torch.nn.functional.pad(target, (0, 14)).cuda(), torch.nn.functional.pad(draft, (0, 14)).cuda(), tokens.cuda(),
+           torch.from_numpy(cu).cuda(), u.cuda(), noise.cuda()]
+    out, acc = torch.zeros(2, 3, dtype=torch.int32).cuda(), torch.zeros(2, dtype=torch.int32).cuda()
+    ws = ql.verify_workspace(2, 50)
+    for i, name in ((0, "target_probs"), (1, "draft_probs")):
+        x = list(dev)
+        x[1 - i] = (target, draft)[1 - i].cuda()
+        with pytest.raises(ValueError, match=name):
+            ql.qlinear_verify_draft(*x, out, acc, ws)
+    p = Problem(1, [3, 2], [90, 40], 4, 2, 64, 16, False)
+    plan = p.plan()
+    with pytest.raises(ValueError, match="lse"):
+        ql.qlinear_attention(plan, p.q, p.cache, p.table.cuda(), p.lens.cuda(), p.cu.cuda(),
+                             torch.zeros(5, 4, 64, dtype=BF16, device="cuda"), torch.zeros(4, 5, device="cuda"),
+                             plan.new_workspace())
