@@ -189,13 +189,15 @@ int64_t attention(PyObject* const* a) {
   int64_t tokens = number(a[2]), q_heads = number(a[3]), dim = number(a[4]);
   const ql_rows q = c.rows(a[7], "q", tokens, q_heads, dim), out = c.rows(a[13], "out", tokens, q_heads, dim);
   const ql_kv_cache* cache = c.cache(a[8], a[9]);
-  const int32_t* table = c.i32(a[10], "page_table", 0);
-  const at::Tensor& t = THPVariable_Unpack(a[10]);
+  // rows may lie apart (the columns of a larger table), a row's entries not
+  const at::Tensor& t = c.tensor(a[10], "page_table", at::kInt, "torch.int32");
   if (t.dim() != 2 || t.size(0) < batch || t.size(1) < columns) {
     PyErr_Format(PyExc_ValueError, "page_table must be a [batch, columns] tensor of at least (%lld, %lld)",
                  (long long)batch, (long long)columns);
     throw Refused();
   }
+  if (t.size(1) > 1 && t.stride(1) != 1) refuse("page_table", "must have contiguous rows");
+  const int32_t* table = static_cast<const int32_t*>(t.data_ptr());
   const int32_t* lens = c.i32(a[11], "seq_lens", batch);
   const int32_t* cu = c.i32(a[12], "cu_q", batch + 1);
   float* lse = a[14] == Py_None ? nullptr : c.f32_rows(a[14], "lse", tokens, q_heads);
@@ -205,7 +207,7 @@ int64_t attention(PyObject* const* a) {
   else if (need > 0)
     refuse("workspace", "is required by this plan");
   const OnDevice on(c);
-  return qlinear_attention(static_cast<ql_attention_plan>(Call::number_ptr(a[0])), &q, cache, table, t.size(1), lens, cu,
+  return qlinear_attention(static_cast<ql_attention_plan>(Call::number_ptr(a[0])), &q, cache, table, t.stride(0), lens, cu,
                            &out, lse, workspace, c.stream(a[16]));
 }
 

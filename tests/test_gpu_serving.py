@@ -699,3 +699,17 @@ def test_rows_of_another_length_are_refused():
         ql.qlinear_attention(plan, p.q, p.cache, p.table.cuda(), p.lens.cuda(), p.cu.cuda(),
                              torch.zeros(5, 4, 64, dtype=BF16, device="cuda"), torch.zeros(4, 5, device="cuda"),
                              plan.new_workspace())
+
+
+def test_page_table_as_columns_of_a_wider_one():
+    p = Problem(12, [1, 2, 40], [500, 33, 90], 8, 2, 128, 16, False)
+    want, lse = p.run(p.plan())
+    wide = torch.full((3, p.table.shape[1] + 5), -9, dtype=torch.int32)
+    wide[:, 2:-3] = p.table
+    out, got = torch.zeros_like(want), torch.zeros_like(lse)
+    plan = p.plan()
+    args = (p.lens.cuda(), p.cu.cuda(), out, got, plan.new_workspace())
+    ql.qlinear_attention(plan, p.q, p.cache, wide.cuda()[:, 2:-3], *args)
+    assert torch.equal(out, want) and torch.equal(got, lse)
+    with pytest.raises(ValueError, match="page_table"):
+        ql.qlinear_attention(plan, p.q, p.cache, p.table.cuda().T.contiguous().T, *args)
