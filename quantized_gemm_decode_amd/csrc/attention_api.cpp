@@ -318,7 +318,8 @@ ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan*
   // (256 and 15 x 4,000) 116 and 112; 504 k (100 and 63 x 1,000) 76 and 118; 744 k
   // (1,024 and 31 x 3,000) 116 and 227; 4 M (512 and 63 x 8,000) 491 and 974.
   const int64_t few = max_q > 0 ? s->batch - (s->tokens + max_q - 1) / max_q : 0;
-  const bool mixed = chunks && few * s->kv_heads * tile_span(*s) > 160000;
+  // (More query heads a KV head than that launch takes rows: none would go there.)
+  const bool mixed = chunks && group <= kMixedRows && few * s->kv_heads * tile_span(*s) > 160000;
   p->tile_from = mixed ? kMixedRows + 1 : 0;
   if (!chunks || mixed) st = plan_stream(*s, mixed ? kMixedRows : rows, &p->stream);
   if (st == QL_OK && chunks) st = plan_tile(*s, rows, p->stream.end, &p->tile);

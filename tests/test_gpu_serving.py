@@ -713,3 +713,11 @@ def test_page_table_as_columns_of_a_wider_one():
     assert torch.equal(out, want) and torch.equal(got, lse)
     with pytest.raises(ValueError, match="page_table"):
         ql.qlinear_attention(plan, p.q, p.cache, p.table.cuda().T.contiguous().T, *args)
+
+
+def test_attention_mixed_batch_of_wide_groups():
+    """More query heads a KV head than the decode share of a mixed batch takes rows."""
+    p = Problem(23, [50, 1, 1, 2, 0, 1], [300, 1500, 40, 65, 20, 1], 24, 1, 64, 16, False)
+    p.table = torch.nn.functional.pad(p.table, (0, 3750 - p.table.shape[1]), value=-7)
+    out, ls = p.run(p.plan(max_kv=60000))
+    p.check(out, ls)

@@ -229,3 +229,12 @@ def test_verify_workspace_of_tiny_vocabularies():
     for batch in (1, 1024, 1025, 65535):
         for vocab in (1, 3, 4, 1023):
             assert ql.qlinear_verify_workspace_bytes(batch, vocab) >= 8 * batch, (batch, vocab)
+
+
+def test_attention_plan_of_wide_groups_in_mixed_batches():
+    """A token of more query heads a KV head than the decode share takes rows has
+    nothing to do there: no launch and no workspace for it."""
+    mixed = dict(batch=32, tokens=231, max_q=200, max_kv=80000)
+    wide = ql.AttentionPlan(shape(q_heads=32, kv_heads=1, **mixed)).facts
+    assert wide["stream_rows"] == 0 and wide["slots"] == 0 and wide["tile_rows"] == 128
+    assert ql.AttentionPlan(shape(q_heads=16, kv_heads=1, **mixed)).facts["stream_rows"] == 16
