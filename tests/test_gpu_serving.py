@@ -721,3 +721,19 @@ def test_attention_mixed_batch_of_wide_groups():
     p.table = torch.nn.functional.pad(p.table, (0, 3750 - p.table.shape[1]), value=-7)
     out, ls = p.run(p.plan(max_kv=60000))
     p.check(out, ls)
+
+
+@pytest.mark.parametrize("D,e4m3", [(64, False), (128, False), (64, True), (128, True)])
+@pytest.mark.parametrize("new,kv", [([1, 1, 1], [17, 60, 2000]), ([5, 2, 4], [40, 300, 25]), ([1], [4001])])
+def test_decode_weights_are_not_held_in_bf16(new, kv, D, e4m3):
+    """The decode kernel's weights enter the product with V to 2^-16 of a
+    weight: only the output's own rounding is bf16's."""
+    p = Problem(81 + D, new, kv, 8, 2, D, 16, e4m3)
+    out, _ = p.run(p.plan())
+    assert p.plan().facts["tile_rows"] == 0
+    r = ref.attention(f64(p.q), p.k_host, p.v_host, p.table.numpy(), p.kv, p.cu.numpy(), 16, D ** -0.5, True, 0,
+                      None if p.ks is None else f64(p.ks), None if p.vs is None else f64(p.vs))
+    d = 2 * D * U * r["reach"] + 8 * U * (r["reach"] + 1)
+    tol = r["weight"] * (2.0 ** -16 + 2 * d + 2 * max(kv) * U)[..., None] + 2.0 ** -8 * (1 + 2.0 ** -6) * np.abs(r["out"]) + 1e-38
+    err = np.abs(f64(out) - r["out"])
+    assert (err <= tol).all(), (int((err > tol).sum()), err.size, float((err / tol).max()))
