@@ -737,3 +737,35 @@ def test_decode_weights_are_not_held_in_bf16(new, kv, D, e4m3):
     tol = r["weight"] * (2.0 ** -16 + 2 * d + 2 * max(kv) * U)[..., None] + 2.0 ** -8 * (1 + 2.0 ** -6) * np.abs(r["out"]) + 1e-38
     err = np.abs(f64(out) - r["out"])
     assert (err <= tol).all(), (int((err > tol).sum()), err.size, float((err / tol).max()))
+
+
+def test_decode_and_append_beyond_32_bit_offsets():
+    """The decode kernel, and rows appended to the last pages, in a cache of more than 4 GiB a tensor."""
+    page, hk, D, pages = 64, 8, 128, (1 << 32) // (64 * 8 * 128 * 2) + 40
+    k = torch.empty(pages, page, hk, D, dtype=BF16, device="cuda")
+    v = torch.empty(pages, page, hk, D, dtype=BF16, device="cuda")
+    p = Problem(8, [1, 4], [500, 70], 16, hk, D, page, False)
+    first = pages - p.k.shape[0]
+    k[first:], v[first:] = p.k, p.v
+    p.table[p.table >= 0] += first
+    p.cache = ql.PagedCache(k, v)
+    plan = p.plan()
+    assert plan.facts["tile_rows"] == 0 and k.element_size() * k.stride(0) * first > 1 << 32
+    out, ls = p.run(plan)
+    p.table[p.table >= 0] -= first
+    p.check(out, ls)
+    q, nk, nv, qw, kw = head_inputs(4, 3, 2, hk, D, True)
+    slots = torch.tensor([pages * page - 1, (pages - 1) * page, first * page + 5])
+    table, pos = ql.rope_table(16, D), torch.tensor([3, 15, 0])
+    before = [x[first:].clone() for x in (k, v)]
+    ql.qlinear_qkv_append(None, nk, nv, pos.cuda(), slots.cuda(), table, None, p.cache, qw, kw)
+    torch.cuda.synchronize()
+    y, size = ref.norm_rope(f64(nk), f64(kw), pos.numpy(), f64(table), D, False, 1e-6)
+    at = (slots - first * page).cuda()
+    check_rounded(f64(k[first:].flatten(0, 1)[at]), y, size, D, "k")
+    assert torch.equal(v[first:].flatten(0, 1)[at], nv)
+    rest = torch.ones((pages - first) * page, dtype=torch.bool, device="cuda")
+    rest[at] = False
+    for x, old in zip((k, v), before):
+        got, old = (t.flatten(0, 1).view(torch.int16)[rest] for t in (x[first:], old))
+        assert torch.equal(got, old), "slots that were not given changed"
