@@ -179,34 +179,38 @@ __device__ __forceinline__ void store_v(Staged<D, E4M3>& t, int key, int len, ui
   }
 }
 
+// One K operand (values 16 i .. 16 i + 15 of 32 keys of half t) and one V
+// operand (16 keys c / DT of half t, values 32 (c % DT) ..).
+template <int D>
+__device__ __forceinline__ u32x4 k_operand(const uint8_t* kl, int t, int i) {
+  const int row = t * 32 + (threadIdx.x & 31), g = (threadIdx.x >> 5) & 1;
+  return *reinterpret_cast<const u32x4*>(kl + row * D * 2 + k_piece<D>(row, 2 * i + g) * 16);
+}
+template <int D>
+__device__ __forceinline__ u32x4 v_operand(const uint8_t* vl, int t, int c) {
+  const int lane = threadIdx.x & 63, g = lane >> 5, j = (lane & 15) >> 2;
+  const uint8_t* vp = vl + (t * 32 + c / (D / 32) * 16 + 4 * g + j) * D * 2 +
+                      v_block<D>(4 * g + j, c % (D / 32)) * 64 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
+  const u32x2 v0 = read_transposed(vp), v1 = read_transposed(vp + 8 * D * 2);
+  return u32x4{v0.x, v0.y, v1.x, v1.y};
+}
+
 // S^T of 32 keys (half t of a K tile) and the wave's 32 rows.
 template <int D>
 __device__ __forceinline__ f32x16 qk(const uint8_t* kl, int t, const u32x4 (&q)[D / 16]) {
-  const int r = threadIdx.x & 31, g = (threadIdx.x >> 5) & 1;
   f32x16 s;
 #pragma unroll
   for (int i = 0; i < 16; ++i) s[i] = 0.0f;
 #pragma unroll
-  for (int i = 0; i < D / 16; ++i) {
-    const int row = t * 32 + r;
-    s = mma32(*reinterpret_cast<const u32x4*>(kl + row * D * 2 + k_piece<D>(row, 2 * i + g) * 16), q[i], s);
-  }
+  for (int i = 0; i < D / 16; ++i) s = mma32(k_operand<D>(kl, t, i), q[i], s);
   return s;
 }
 
 // O^T += V^T P^T over the 32 keys of half t of a V tile.
 template <int D>
 __device__ __forceinline__ void pv(const uint8_t* vl, int t, const u32x4 (&p)[2], f32x16 (&o)[D / 32]) {
-  const int lane = threadIdx.x & 63, g = lane >> 5, j = (lane & 15) >> 2;
-  const uint8_t* vp = vl + (t * 32 + 4 * g + j) * D * 2 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int dt = 0; dt < D / 32; ++dt) {
-      const u32x2 v0 = read_transposed(vp + i * 16 * D * 2 + v_block<D>(4 * g + j, dt) * 64);
-      const u32x2 v1 = read_transposed(vp + (i * 16 + 8) * D * 2 + v_block<D>(4 * g + j, dt) * 64);
-      o[dt] = mma32(u32x4{v0.x, v0.y, v1.x, v1.y}, p[i], o[dt]);
-    }
+  for (int c = 0; c < D / 16; ++c) o[c % (D / 32)] = mma32(v_operand<D>(vl, t, c), p[c / (D / 32)], o[c % (D / 32)]);
 }
 
 // One row's running softmax (row = lane & 31; the lane halves hold different
@@ -229,22 +233,6 @@ __device__ __forceinline__ void weights(const f32x16& s, Soft* w, u32x4 (&p)[2])
   for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) p[i][k] = bf16_pair(e[8 * i + 2 * k], e[8 * i + 2 * k + 1]);
-}
-
-// One K operand (values 16 i .. 16 i + 15 of 32 keys of half t) and one V
-// operand (16 keys c / DT of half t, values 32 (c % DT) ..).
-template <int D>
-__device__ __forceinline__ u32x4 k_operand(const uint8_t* kl, int t, int i) {
-  const int row = t * 32 + (threadIdx.x & 31), g = (threadIdx.x >> 5) & 1;
-  return *reinterpret_cast<const u32x4*>(kl + row * D * 2 + k_piece<D>(row, 2 * i + g) * 16);
-}
-template <int D>
-__device__ __forceinline__ u32x4 v_operand(const uint8_t* vl, int t, int c) {
-  const int lane = threadIdx.x & 63, g = lane >> 5, j = (lane & 15) >> 2;
-  const uint8_t* vp = vl + (t * 32 + c / (D / 32) * 16 + 4 * g + j) * D * 2 +
-                      v_block<D>(4 * g + j, c % (D / 32)) * 64 + ((lane >> 4) & 1) * 32 + (lane & 3) * 8;
-  const u32x2 v0 = read_transposed(vp), v1 = read_transposed(vp + 8 * D * 2);
-  return u32x4{v0.x, v0.y, v1.x, v1.y};
 }
 
 // The inner step: next = S^T of half kt of the K tile kl, O^T += V^T P^T over
