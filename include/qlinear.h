@@ -628,11 +628,12 @@ ql_status qlinear_qkv_append(const ql_norm_rope* rule, int64_t tokens, int32_t q
  * such sequences with ones of up to 16 rows.  max_q, max_kv: upper bounds of a
  * sequence's new and cached tokens (the page table holds at least
  * ceil(max_kv / page_size) columns; NULL where max_kv is 0); a sequence with
- * more than max_q new tokens is computed in part or not at all.  q_heads a
- * multiple of kv_heads; head_dim 64 or 128; scale 0 = 1 / sqrt(head_dim).
- * Partial results are joined by a second launch (no atomics: results do not
- * depend on timing).  The workspace needs no initialisation; concurrent calls
- * need distinct ones.
+ * more than max_q new tokens is computed in part or not at all.  The kernel that
+ * streams cuts the keys by the lengths it finds; the other's chunks of keys follow
+ * from max_kv, so a bound near the lengths serves it best.  q_heads a multiple of
+ * kv_heads; head_dim 64 or 128; scale 0 = 1 / sqrt(head_dim).  Partial results
+ * are joined by a second launch (no atomics: results do not depend on timing).
+ * The workspace needs no initialisation; concurrent calls need distinct ones.
  *
  * Scores, sums, maxima and outputs in progress are binary32.  The weights enter
  * their product with V to 2^-16 of a weight in the kernel that streams the keys,

@@ -134,9 +134,15 @@ ql_status check_rule(const ql_norm_rope* r, int64_t tokens, int32_t q_heads, int
 
 // Rows (new tokens x query heads of a KV head) of a sequence up to which the
 // stream kernel serves it; in a batch that has longer ones too, up to which
-// sequences get a stream launch of their own.  16 sequences of 4,000 keys, 32
-// rows each: 58 us here, 61 us in the tile kernel, which takes 66 us for 64 rows; the
-// stream kernel would not hold their sums in registers.
+// sequences get a stream launch of their own.  More than 32 rows it would not hold
+// in registers.  With 17 to 32 rows the tile kernel is the faster one where all
+// sequences are about as long as the plan's bound, the slower one where they are
+// not, as in a server's batches and captured steps.  Stream and tile kernel, us, 5
+// new tokens of 32 / 8 heads of 128: 16 sequences of 500 keys 19.7 and 13.7 (bf16),
+// of 4,000 60.1 and 56.8 (E4M3: 40.4 and 46.7); 64 of 1,000 59.5 and 50.6; with 8
+// new tokens 64.9 and 51.6.  16 of 515 .. 4,099 38.7 and 50.0, 64 of 200 .. 8,000 192
+// and 240 (64-wide: 110 and 181); 16 of 4,000 under a bound of 32,768 59.8 and 106.
+// The stream kernel also holds the weights more exactly.
 constexpr int64_t kStreamRows = 32;
 constexpr int64_t kMixedRows = 16;
 
@@ -414,7 +420,9 @@ ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_c
 }
 
 // Slices of a vocabulary row: enough workgroups for the card with few
-// sequences, at least 1024 entries (4 a thread) each, at most kVerifySlice.
+// sequences, at least 1024 entries (4 a thread) each, at most kVerifySlice.  With
+// 512, 1,024 and 2,048 workgroups, us: 4 x 151,936 entries 7.4, 7.9, 7.9; 16 x 151,936
+// 10.9, 10.2, 10.5; 64 x 32,001 9.8, 9.4, 10.1.
 static int verify_slices(int64_t batch, int64_t vocab) {
   const int64_t most = std::max<int64_t>(1, vocab / 1024), least = (vocab + qlk::kVerifySlice - 8) / (qlk::kVerifySlice - 4);
   return (int)std::max<int64_t>({1, least, std::min<int64_t>(most, 1024 / std::max<int64_t>(1, batch))});

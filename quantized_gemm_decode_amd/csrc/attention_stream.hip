@@ -41,10 +41,10 @@
 // Row sums take P in binary32, and all sums and maxima are binary32.
 //
 // Measured on MI355X, against 7.05 TB/s of a streaming read: 32 sequences of
-// 1,021 .. 8,190 keys, 64 / 8 heads of 128, bf16 (605 MB) 96 us and the join's 5; 64
+// 1,021 .. 8,190 keys, 64 / 8 heads of 128, bf16 (605 MB) 97 us and the join's 5; 64
 // of 4,003 .. 16,001, 40 / 8 heads, E4M3 (1.31 GB) 210 and 6; 5 x 4 rows of each of 16
-// sequences of 515 .. 4,099, bf16 (153 MB) 31 and 6; one of 1,031 keys 6.8 and 3.3,
-// all of it latency.
+// sequences of 515 .. 4,099, bf16 (153 MB) 33 and 6; one of 1,031 keys 7 and 4, all
+// of it latency.
 #include "attention_common.hpp"
 
 namespace qlk {
@@ -229,19 +229,19 @@ __device__ __forceinline__ void drop_nonfinite(KvTile<D, E4M3>& t) {
 }
 
 // Workgroups a compute unit gets.  Measured, one and two: 32 sequences of 4,600
-// keys, 64 / 8 heads, bf16 98.5 and 105.6 us (16 of 4,000, 64-wide heads: 29.6 and
-// 31.8); 64 of 9,000, E4M3 216 and 201 us (3,000, 64-wide: 51 and 41; 5 x 4 rows:
-// 45.8 and 39.6).  More requests on their way than that only queue; E4M3's are
-// half as large.  With 32 rows the sums of 128-wide heads leave one workgroup its
-// registers (32 sequences of 5 x 4 rows, 4,000 keys: 65.8 us, 66.8 with two; 16 of
-// them: 39.7 and 45.6).
+// keys, 64 / 8 heads, bf16 99.2 and 106.0 us (16 of 4,000, 64-wide heads: 29.3 and
+// 31.2); E4M3, 64 of 9,000 200.3 and 201.0 us, 64-wide heads of 3,000 56.4 and 47.0,
+// of 8,000 134.8 and 109.7, 5 x 4 rows of 32 of 4,000 46.1 and 43.0.  More requests on
+// their way than that only queue; E4M3's are half as large.  With 32 rows the sums
+// of 128-wide heads leave one workgroup its registers (32 sequences of 5 x 4 rows,
+// 4,000 keys, E4M3: 71.6 us, 72.7 with two; bf16 100.6 and 118.1).
 constexpr int stream_workgroups(int D, bool e4m3, int row_tiles) { return e4m3 && (row_tiles == 1 || D == 64) ? 2 : 1; }
 
 // Tiles that a wave has in its registers: a compute unit's only workgroup asks
 // for a second one while it works on the first (32 sequences of 5 x 4 rows and
-// 4,000 keys, with one and two: E4M3 67.1 and 65.7 us, 64-wide bf16 55.7 and
-// 54.0); where there are two, they cover each other (64-wide E4M3, single
-// tokens, 8,000 keys: 51.6 and 54.8 us).
+// 4,000 keys, with one and two: E4M3 75.0 and 71.6 us, 64-wide bf16 62.2 and
+// 58.8); where there are two, they cover each other (64-wide E4M3, 64 single tokens:
+// 3,000 keys 47.0 and 47.9 us, 8,000 keys 109.7 and 109.6).
 constexpr int stream_depth(int D, bool e4m3, int row_tiles) { return stream_workgroups(D, e4m3, row_tiles) == 1 ? 2 : 1; }
 
 template <int D, bool E4M3, int NR>
@@ -618,7 +618,12 @@ int attn_stream_slots(int head_dim, bool e4m3, int rows, int kv_heads, int heads
 template <int D>
 static void launch_stream_join(const AttnArgs& a, int rows, int most_rows, hipStream_t s) {
   const unsigned all = (unsigned)(most_rows * a.kv_heads);
-  // sequences in more than 16 slots on average: a workgroup a row, else a wave
+  // Sequences in more than 16 slots on average: a workgroup a row, else a wave.  A
+  // wave's and a workgroup's join, 32 / 8 heads, bf16, us: 1 x 16,000 keys 31.9 and
+  // 21.2, 4 x 4,000 22.9 and 20.1, 7 x 4,000 28.4 and 26.9, 8 x 4,000 (16 slots) 29.8
+  // and 28.6, 16 x 4,000 50.6 and 50.1, 24 x 2,000 39.5 and 40.0, 64 x 1,000 49.2 and
+  // 50.8; 16 x 5 tokens at 515 .. 4,099 38.5 and 40.4; 200 x 300, 64 / 8 heads, 64.8
+  // and 82.7.
   if (a.slots > 16 * a.batch)
     hipLaunchKernelGGL((attn_stream_join_kernel<D, kJoinWaves>), dim3(all, (unsigned)a.batch), dim3(kJoinWaves * 64), 0, s,
                        a, rows);

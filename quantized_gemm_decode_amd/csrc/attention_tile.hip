@@ -36,14 +36,16 @@
 // the values again.
 //
 // Measured on MI355X, 2048 new tokens at the end of 10,240 cached ones, 32 / 8
-// heads of 128: 304-375 us by card, 820-1020 TFLOP/s of the visible pairs' flops,
+// heads of 128: 304-375 us by card, 820-1020 TFLOP/s of the visible pairs' flops
+// (a traced run's median 335),
 // against 1140-1380 that a large library product reaches.  With the exponentials, the
 // LDS reads or the staging left out it is 1, 3 or 13 % faster, with all of
 // them 33 %: no single part bounds it, the products' own rate does at last.
 // (Nor the tests of the reference maximum: made behind the products instead of
 // ahead of the weights, 344 us.)  64-wide heads have half the products for the
-// same weights, and the vector unit bounds them: 512 new tokens of each of 4
-// sequences of 2,000, bf16: 55 us, 534 TFLOP/s.
+// same weights: 512 new tokens of each of 4 sequences of 2,000, bf16: 49 us, 597
+// TFLOP/s.  No unit bounds them alone (12 sequences with 4,327 new tokens, window
+// 2048, E4M3: vector unit busy 56 % of the time, matrix cores 27 %).
 #include "attention_common.hpp"
 
 #include <type_traits>

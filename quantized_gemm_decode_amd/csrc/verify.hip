@@ -18,8 +18,8 @@
 // then p and q are requested at once.  Every workgroup walks its sequence's
 // drafts itself instead of waiting for a launch that would.  A second launch
 // takes the maximum over the slices.
-// Measured: 64 sequences of 5 drafts, 151,936 entries: 21.8 us
-// (107 MB, 4.9 TB/s with both launches); 24.6 and 27.1 us with 8,192 and 10,240
+// Measured: 64 sequences of 5 drafts, 151,936 entries: 21.3 us
+// (107 MB, 5.0 TB/s with both launches); 24.6 and 27.1 us with 8,192 and 10,240
 // entries a workgroup, which leave too few of them a compute unit.
 #include "attention_args.hpp"
 #include "attention_common.hpp"
@@ -165,7 +165,10 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_scan_kernel(VerifyArgs 
   }
 }
 
-// One wave a sequence: the maximum over the slices is the next token.
+// One wave a sequence: the maximum over the slices is the next token.  Where p - q
+// is nowhere positive this wave reads the whole of p by itself: 333 us for a
+// sequence of 151,936 entries, 1.1 ms for 64 of them.  Rounding alone leads there,
+// or a drafted token outside the vocabulary with p = q.
 __global__ void __launch_bounds__(64) verify_pick_kernel(VerifyArgs a) {
   const int b = blockIdx.x, lane = threadIdx.x;
   const int k = a.accepted[b];
