@@ -695,6 +695,91 @@ ql_status qlinear_verify_draft(int64_t batch, int64_t n_drafts, int64_t max_draf
                                int32_t* out_tokens, int32_t* accepted, void* workspace, void* stream);
 
 /*
+ * Low-rank adapters of many requests beside a shared projection:
+ *   out[t, n] = y[t, n] + s_i sum_r B_i[n, r] sum_k A_i[j R + r, k] x[t, k],
+ * i = adapter[t] (int32 [tokens], device memory; outside [0, adapters): out = y
+ * as it stands) and j the slice that column n lies in.  A merged projection (query, key
+ * and value; gate and up) has up to 4 slices of widths[j] columns, each with its
+ * own A; an unmerged one has one.  y is the projection's bf16 output.
+ *   x    bf16 [tokens, in_features]
+ *   a    bf16 [adapters, slices * rank, in_features], rows contiguous
+ *   b    bf16 [adapters, sum of widths, rank], rows contiguous
+ *   scales  binary32 [adapters], device memory, NULL = 1
+ *   y, out  bf16 [tokens, sum of widths]; out may be y, but must not overlap it
+ *        otherwise
+ * Strides are in elements, multiples of 8, data 16-byte aligned: rows of x, y
+ * and out may lie in wider buffers, adapters (a_adapter_stride, b_adapter_stride)
+ * in a pool of all layers.  rank: a multiple of 8 up to 128 (adapters of a lower
+ * one are padded with zeros); in_features and widths multiples of 8 up to 2^20.
+ * Tokens of one adapter need not be neighbours; a batch of more than 64 tokens
+ * runs best where they mostly are, as the tokens of a request.  What one adapter's
+ * weights hold reaches only its own tokens.
+ *
+ * Sums are binary32; the inner sum enters its product to 2^-16 of it, and out is
+ * rounded to bf16 once.  The workspace (qlinear_lora_workspace_bytes; 0 for sizes
+ * that qlinear_lora refuses) needs no initialisation; concurrent calls need
+ * distinct ones.  Enqueue-only; no atomics.
+ */
+typedef struct {
+  const void* a;
+  const void* b;
+  const float* scales;
+  int64_t a_adapter_stride, b_adapter_stride;
+  int64_t in_features;
+  int64_t widths[4];
+  int32_t adapters, rank, slices;
+} ql_lora;
+
+int64_t qlinear_lora_workspace_bytes(const ql_lora* lora, int64_t tokens);
+ql_status qlinear_lora(const ql_lora* lora, int64_t tokens, const void* x, int64_t x_stride, const void* y,
+                       int64_t y_stride, const int32_t* adapter, void* out, int64_t out_stride, void* workspace,
+                       void* stream);
+
+/*
+ * Sampling: a token from each row of logits, with given random numbers.
+ * Entries are ordered by falling logit, equal ones by rising index.  With
+ * w_v = exp((l_v - max) / temperature) an entry is kept if
+ *   fewer than top_k entries are before it,
+ *   the sum of w before it is below top_p times the sum over the first top_k, and
+ *   w_v >= min_p;
+ * the first always is.  tokens[row] = argmax w_v / noise[row, v] over the kept
+ * entries, ties to the lowest index: with noise drawn from the exponential
+ * distribution (as for qlinear_verify_draft) that draws v in proportion to w_v.
+ *   logits  binary32 or bf16 [rows, vocab], rows logits_stride elements apart
+ *   noise   binary32 [rows, vocab], positive and finite; read at kept entries only
+ *   tokens  int32 [rows]
+ *   logprobs  binary32 [rows] or NULL: logarithm of the token's probability
+ *           among the kept entries
+ *   probs   binary32 [rows, vocab] or NULL: w over the sum of the kept, 0 for the
+ *           others (what qlinear_verify_draft takes)
+ * The rules are device arrays of one value a row, each NULL where no row has it
+ * (rules NULL: none): temperature binary32 (0 or below, NaN: greedy, the first
+ * entry of the order), top_k int32 (0 or below: off), top_p binary32 (1 or above,
+ * NaN: off), min_p binary32 (0 or below, NaN: off).  A logit of -inf or NaN is no
+ * entry; without any the token is -1, its logarithm -inf and the probabilities 0.
+ * Logits of +inf share the probability.
+ *
+ * What is kept does not depend on rounding in binary32: weights are computed in
+ * binary64 and summed as integers in steps of 2^-36 of the largest.  Results do
+ * not depend on timing.  The workspace (qlinear_sample_workspace_bytes, 16-byte
+ * aligned; about 8 bytes an entry) needs no initialisation; concurrent calls need
+ * distinct ones.  Up to 65535 rows and 2^24 entries a row.  Enqueue-only.
+ */
+typedef enum { QL_LOGITS_F32 = 0, QL_LOGITS_BF16 = 1 } ql_logits_type;
+
+typedef struct {
+  const float* temperature;
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+} ql_sampling;
+
+int64_t qlinear_sample_workspace_bytes(int64_t rows, int64_t vocab);
+ql_status qlinear_sample(const ql_sampling* rules, int64_t rows, int64_t vocab, const void* logits,
+                         int64_t logits_stride, int32_t logits_type, const float* noise, int32_t* tokens,
+                         float* logprobs, float* probs, void* workspace, void* stream);
+
+/*
  * hipGraph dispatch for the small-M path ([Summary] "Hybrid dispatch
  * addresses runtime overhead": the tuned kernels run only under graph
  * replay, which removes the host launch cost).  qlinear_graph_begin starts

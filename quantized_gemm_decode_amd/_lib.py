@@ -45,6 +45,16 @@ class QLAttentionFacts(ctypes.Structure):
     _fields_ = [(n, c_i32) for n in ("stream_rows", "slots", "tile_rows", "row_blocks", "splits", "chunk")] + [("workspace_bytes", c_i64)]
 
 
+class QLLora(ctypes.Structure):
+    _fields_ = ([(n, c_vp) for n in ("a", "b", "scales")]
+                + [(n, c_i64) for n in ("a_adapter_stride", "b_adapter_stride", "in_features")] + [("widths", c_i64 * 4)]
+                + [(n, c_i32) for n in ("adapters", "rank", "slices")])
+
+
+class QLSampling(ctypes.Structure):
+    _fields_ = [(n, c_vp) for n in ("temperature", "top_k", "top_p", "min_p")]
+
+
 c_rows, c_cache = ctypes.POINTER(QLRows), ctypes.POINTER(QLKvCache)
 
 # name -> (restype, argtypes); exactly the functions declared in include/qlinear.h
@@ -96,6 +106,10 @@ SIGNATURES = {
     "qlinear_attention": (c_i32, [c_vp, c_rows, c_cache, c_vp, c_i64, c_vp, c_vp, c_rows, c_vp, c_vp, c_vp]),
     "qlinear_verify_workspace_bytes": (c_i64, [c_i64, c_i64]),
     "qlinear_verify_draft": (c_i32, [c_i64] * 4 + [c_vp] * 10),
+    "qlinear_lora_workspace_bytes": (c_i64, [ctypes.POINTER(QLLora), c_i64]),
+    "qlinear_lora": (c_i32, [ctypes.POINTER(QLLora), c_i64, c_vp, c_i64, c_vp, c_i64, c_vp, c_vp, c_i64, c_vp, c_vp]),
+    "qlinear_sample_workspace_bytes": (c_i64, [c_i64, c_i64]),
+    "qlinear_sample": (c_i32, [ctypes.POINTER(QLSampling), c_i64, c_i64, c_vp, c_i64, c_i32] + [c_vp] * 6),
     "qlinear_graph_begin": (c_i32, [c_vp]),
     "qlinear_graph_end": (c_i32, [c_vp, ctypes.POINTER(c_vp)]),
     "qlinear_graph_launch": (c_i32, [c_vp, c_vp]),

@@ -99,6 +99,22 @@ struct Call {
     return ql_rows{t.data_ptr(), t.stride(0), t.stride(1)};
   }
 
+  // bf16 [rows, width] with contiguous rows; sizes below 0 are taken from the
+  // tensor.
+  const at::Tensor& matrix(PyObject* o, const char* name, int64_t& rows, int64_t& width) {
+    const at::Tensor& t = tensor(o, name, at::kBFloat16, "torch.bfloat16");
+    if (t.dim() != 2) refuse(name, "must be a matrix");
+    if (rows < 0) rows = t.size(0);
+    if (width < 0) width = t.size(1);
+    if (t.size(0) != rows || t.size(1) != width) {
+      PyErr_Format(PyExc_ValueError, "%s has shape (%lld, %lld), expected (%lld, %lld)", name, (long long)t.size(0),
+                   (long long)t.size(1), (long long)rows, (long long)width);
+      throw Refused();
+    }
+    if (t.stride(1) != 1 && width > 1) refuse(name, "must have contiguous rows");
+    return t;
+  }
+
   // A cache's descriptor; `index` is the device of its tensors.
   const ql_kv_cache* cache(PyObject* address, PyObject* index) {
     if (number(index) != device) refuse("cache", "is on another device than the call's first tensor");
@@ -234,6 +250,46 @@ int64_t verify_draft(PyObject* const* a) {
                               workspace, c.stream(a[9]));
 }
 
+// stack, stack device, out features, x, y, adapters, out, workspace, stream
+int64_t lora(PyObject* const* a) {
+  Call c;
+  const ql_lora* stack = static_cast<const ql_lora*>(Call::number_ptr(a[0]));
+  int64_t tokens = -1, k = stack->in_features, wide = number(a[2]);
+  const at::Tensor& x = c.matrix(a[3], "x", tokens, k);
+  const at::Tensor& y = c.matrix(a[4], "y", tokens, wide);
+  const at::Tensor& out = a[6] == Py_None ? y : c.matrix(a[6], "out", tokens, wide);
+  if (number(a[1]) != c.device) refuse("stack", "is on another device than the call's first tensor");
+  const int32_t* adapters = c.i32(a[5], "adapters", tokens);
+  void* workspace = c.bytes(a[7], "workspace", qlinear_lora_workspace_bytes(stack, tokens));
+  const OnDevice on(c);
+  return qlinear_lora(stack, tokens, x.data_ptr(), x.stride(0), y.data_ptr(), y.stride(0), adapters, out.data_ptr(),
+                      out.stride(0), workspace, c.stream(a[8]));
+}
+
+// logits, noise, tokens, workspace, temperature, top_k, top_p, min_p, logprobs, probs, stream
+int64_t sample(PyObject* const* a) {
+  Call c;
+  if (!THPVariable_Check(a[0])) refuse("logits", "must be a CUDA (HIP) tensor");
+  const bool bf16 = THPVariable_Unpack(a[0]).scalar_type() == at::kBFloat16;
+  const at::Tensor& logits = c.tensor(a[0], "logits", bf16 ? at::kBFloat16 : at::kFloat, "torch.float32 or torch.bfloat16");
+  if (logits.dim() != 2) refuse("logits", "must be a [rows, vocab] tensor");
+  const int64_t rows = logits.size(0), vocab = logits.size(1);
+  if (logits.stride(1) != 1 && vocab > 1) refuse("logits", "must have contiguous rows");
+  const float* noise = c.f32_rows(a[1], "noise", rows, vocab);
+  int32_t* tokens = c.i32(a[2], "tokens", rows);
+  void* workspace = c.bytes(a[3], "workspace", qlinear_sample_workspace_bytes(rows, vocab));
+  ql_sampling rules{};
+  if (a[4] != Py_None) rules.temperature = c.f32(a[4], "temperature", rows);
+  if (a[5] != Py_None) rules.top_k = c.i32(a[5], "top_k", rows);
+  if (a[6] != Py_None) rules.top_p = c.f32(a[6], "top_p", rows);
+  if (a[7] != Py_None) rules.min_p = c.f32(a[7], "min_p", rows);
+  float* logprobs = a[8] == Py_None ? nullptr : c.f32(a[8], "logprobs", rows);
+  float* probs = a[9] == Py_None ? nullptr : c.f32_rows(a[9], "probs", rows, vocab);
+  const OnDevice on(c);
+  return qlinear_sample(&rules, rows, vocab, logits.data_ptr(), logits.stride(0), bf16 ? QL_LOGITS_BF16 : QL_LOGITS_F32,
+                        noise, tokens, logprobs, probs, workspace, c.stream(a[10]));
+}
+
 template <int64_t (*F)(PyObject* const*), int N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
   if (n != N) {
@@ -257,6 +313,7 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef kMethods[] = {method<qk_norm_rope, 11>("qk_norm_rope"), method<qkv_append, 14>("qkv_append"),
                           method<attention, 17>("attention"), method<verify_draft, 10>("verify_draft"),
+                          method<lora, 9>("lora"), method<sample, 11>("sample"),
                           {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", "Serving operators on torch tensors", -1, kMethods,

@@ -1,0 +1,84 @@
+// Launch arguments of the operators of a server of many requests: low-rank
+// adapters beside a projection, and sampling.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace qlk {
+
+constexpr int kLoraSlices = 4;      // most slices of a merged projection
+constexpr int kLoraBlock = 64;      // tokens among which equal adapters are looked for: one a lane
+constexpr int kLoraMostRank = 128;
+
+struct LoraArgs {
+  const uint8_t* x;        // bf16 [tokens, K]; strides in bytes
+  const uint8_t* y;        // bf16 [tokens, N]
+  uint8_t* out;            // bf16 [tokens, N]
+  const uint8_t* a;        // bf16 [adapters, slices * rank, K]
+  const uint8_t* b;        // bf16 [adapters, N, rank]
+  const float* scales;     // [adapters] or null
+  const int32_t* adapter;  // [tokens]; outside [0, adapters): none
+  float* part;             // [chunks, tokens, slices * rank]: sums over chunks of K
+  int64_t x_row, y_row, out_row, a_step, b_step;
+  int tokens, adapters, rank, k, slices;
+  int width[kLoraSlices];
+  int chunk, chunks;       // K of a partial sum (a multiple of 64), their number
+  int down_slots;          // waves that share a block's adapters, first product
+  int up_slots;            // the same, second product
+  int tiles_wave;          // 64-wide column tiles of a wave of the second product
+  int ranges;              // of all slices together
+};
+
+// What a slice of a vocabulary row leaves for the others: its largest logit,
+// that one's bucket, and its entries' number and mass.
+struct SampleSlice {
+  float top;
+  int bucket;
+  uint64_t all;
+};
+
+// What is settled of a row before its candidates are looked at.
+struct SampleRow {
+  float top;               // largest logit; -inf: no entry
+  int bucket;              // its bucket
+  int lo, hi;              // buckets before lo are kept whole, those after hi are not; between them the candidates
+  int count;               // entries of the buckets before lo
+  int greedy;
+  uint64_t mass;           // and their mass
+  double rate;             // log2(e) / temperature
+  double limit;            // top-p: mass that ends the kept entries; of all, or with top-k of its entries' share
+  int top_k;               // 0: off
+  float top_p, min_p;      // 1, 0: off
+  // known at the end
+  uint64_t least;          // smallest kept candidate
+  uint64_t total;          // mass of the kept entries
+};
+
+struct SampleArgs {
+  const void* logits;      // binary32 or bf16 [rows, vocab]
+  int64_t row;             // entries between rows
+  const float* noise;      // [rows, vocab]
+  const float* temperature;  // [rows] each, or null
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  int32_t* tokens;         // [rows]
+  float* logprobs;         // [rows] or null
+  float* probs;            // [rows, vocab] or null
+  uint64_t* hist;          // [rows, slices, kSampleBuckets]: entries (high bits) and their mass
+  SampleSlice* slice;      // [rows, slices]
+  SampleRow* state;        // [rows]
+  uint64_t* best;          // [rows, slices]: best score among a slice's surely kept entries
+  int32_t* found;          // [rows, slices]: candidates of a slice
+  uint64_t* cand;          // [rows, slices, entries]: they themselves
+  int rows, vocab, slices, entries;
+};
+
+constexpr int kSampleBuckets = 256;
+constexpr int kSampleWide = 8192, kSampleNarrow = 2048;   // entries of a slice
+
+hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
+hipError_t launch_sample(const SampleArgs& a, bool bf16, hipStream_t s);
+
+}  // namespace qlk

@@ -1,6 +1,7 @@
 """The serving operators around the linears (C ABI section "Serving operators"
 of ``include/qlinear.h``): norm and rotation of the query and key heads, append
-to a paged cache, attention over it, verification of drafted tokens.
+to a paged cache, attention over it, verification of drafted tokens, low-rank
+adapters beside a projection, sampling.
 
 Tensors keep torch's shapes and strides: heads are ``[tokens, heads,
 head_dim]`` views (the query columns of a QKV projection's output as they
@@ -15,7 +16,7 @@ import os
 import torch
 
 from . import _lib
-from ._lib import QLAttentionFacts, QLAttentionShape, QLKvCache
+from ._lib import QLAttentionFacts, QLAttentionShape, QLKvCache, QLLora
 
 KV_BF16, KV_E4M3 = 0, 1
 KV_DTYPES = {torch.bfloat16: KV_BF16, torch.float8_e4m3fn: KV_E4M3}
@@ -181,3 +182,74 @@ def qlinear_verify_draft(target_probs, draft_probs, draft_tokens, cu_drafts, uni
                                               out_tokens, accepted, workspace, _stream(stream))
     if st:
         _lib_check(st, "qlinear_verify_draft")
+
+
+class LoraStack:
+    """Low-rank adapters of one projection.
+
+    a: [adapters, slices * rank, in_features], b: [adapters, out_features,
+    rank], bf16 with contiguous adapters (views of a pool of all layers may
+    have any stride between adapters); scales: binary32 [adapters] or None = 1;
+    widths: the columns of each slice of a merged projection (query, key and
+    value; gate and up), None: one slice.  The tensors stay the owner's.
+    """
+
+    def __init__(self, a, b, scales=None, widths=None):
+        for t, name in ((a, "a"), (b, "b")):
+            if not isinstance(t, torch.Tensor) or t.dim() != 3 or t.dtype != torch.bfloat16:
+                raise ValueError("%s must be a bfloat16 tensor of three dimensions" % name)
+            if t.numel() and not t[0].is_contiguous():
+                raise ValueError("%s must have contiguous adapters" % name)
+        widths = [b.shape[1]] if widths is None else [int(w) for w in widths]
+        if not 1 <= len(widths) <= 4 or sum(widths) != b.shape[1]:
+            raise ValueError("widths must be 1 to 4 numbers that add up to b's %d rows" % b.shape[1])
+        if a.shape[0] != b.shape[0] or a.shape[1] != len(widths) * b.shape[2] or a.device != b.device:
+            raise ValueError("a and b differ in adapters, rank or device")
+        if scales is not None and (scales.dtype != torch.float32 or not scales.is_contiguous()
+                                   or scales.numel() != a.shape[0] or scales.device != a.device):
+            raise ValueError("scales must be a contiguous float32 [adapters] tensor on a's device")
+        self.a, self.b, self.scales, self.widths = a, b, scales, widths
+        self.struct = QLLora(a.data_ptr(), b.data_ptr(), None if scales is None else scales.data_ptr(), a.stride(0),
+                             b.stride(0), a.shape[2], (ctypes.c_int64 * 4)(*widths), a.shape[0], b.shape[2], len(widths))
+        self.address = ctypes.addressof(self.struct)
+        self.on_gpu, self.device_index, self.out_features = a.is_cuda, a.get_device(), b.shape[1]
+
+
+def qlinear_lora_workspace_bytes(stack, tokens):
+    return int(_lib.load().qlinear_lora_workspace_bytes(ctypes.byref(stack.struct), tokens))
+
+
+def lora_workspace(stack, tokens, device="cuda"):
+    """Device memory for qlinear_lora with `tokens` tokens (any contents)."""
+    return torch.empty(max(16, qlinear_lora_workspace_bytes(stack, tokens)), dtype=torch.uint8, device=device)
+
+
+def qlinear_lora(stack, x, y, adapters, workspace, out=None, stream=None):
+    """out (None: y itself) = y + scale B A x of each token's adapter (int32
+    [tokens]; outside the stack, as -1: y as it is)."""
+    if not stack.on_gpu:
+        raise ValueError("the stack must be on the GPU")
+    st = (_module or _binding()).lora(stack.address, stack.device_index, stack.out_features, x, y, adapters, out, workspace,
+                                      _stream(stream))
+    if st:
+        _lib_check(st, "qlinear_lora")
+
+
+def qlinear_sample_workspace_bytes(rows, vocab):
+    return int(_lib.load().qlinear_sample_workspace_bytes(rows, vocab))
+
+
+def sample_workspace(rows, vocab, device="cuda"):
+    """Device memory for qlinear_sample (any contents)."""
+    return torch.empty(max(16, qlinear_sample_workspace_bytes(rows, vocab)), dtype=torch.uint8, device=device)
+
+
+def qlinear_sample(logits, noise, tokens, workspace, temperature=None, top_k=None, top_p=None, min_p=None, logprobs=None,
+                   probs=None, stream=None):
+    """tokens (int32 [rows]) drawn from logits (float32 or bfloat16 [rows,
+    vocab]) with exponential noise under each row's rules (see qlinear.h);
+    logprobs and probs of the kept entries where given."""
+    st = (_module or _binding()).sample(logits, noise, tokens, workspace, temperature, top_k, top_p, min_p, logprobs, probs,
+                                        _stream(stream))
+    if st:
+        _lib_check(st, "qlinear_sample")
