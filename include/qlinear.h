@@ -669,6 +669,53 @@ ql_status qlinear_attention(ql_attention_plan plan, const ql_rows* q, const ql_k
                             const int32_t* cu_q, const ql_rows* out, float* lse, void* workspace, void* stream);
 
 /*
+ * Attention for trees of drafted tokens.  As qlinear_attention, but a sequence's
+ * new tokens are the nodes of a tree: each sees all cached tokens before them, and
+ * of the new tokens those that its bits name -- bit i % 64 of word i / 64 of row t
+ * of sees (uint64 [tokens, sees_words], device memory) for new token i of the
+ * sequence of token t.  As a rule those are itself and the nodes above it, but any
+ * set is taken: a token whose bits are 0 sees the context alone, and is 0 with lse
+ * -inf where there is none.  sees_words >= ceil(max_q / 64); a new token beyond
+ * them is seen by none.  Keys were rotated at the positions of their nodes (context
+ * + depth) and appended in the nodes' order.  Plans: causal, no window.  A plan of
+ * either kind serves only its own call.
+ */
+ql_status qlinear_tree_attention_plan(const ql_attention_shape* shape, ql_attention_plan* out_plan);
+ql_status qlinear_tree_attention(ql_attention_plan plan, const ql_rows* q, const ql_kv_cache* cache,
+                                 const int32_t* page_table, int64_t table_stride, const int32_t* seq_lens,
+                                 const int32_t* cu_q, const uint64_t* sees, int64_t sees_words, const ql_rows* out,
+                                 float* lse, void* workspace, void* stream);
+
+/*
+ * Commit of a drafted tree's accepted branch.  Sequence b has the nodes cu_q[b] ..
+ * cu_q[b+1] - 1 (int32 [batch + 1], cu_q[0] = 0; as in the attention before) of
+ * node_tokens, parents and sampled (int32 [tokens]): a node's token, its parent's
+ * number in the sequence (below its own; node 0 is the root, the newest token that
+ * is already given out, parent -1) and the token drawn at it.  From the root the
+ * walk goes to the lowest-numbered child whose token is the one drawn, while there
+ * is one and fewer than max_depth (up to 1024) are accepted.
+ *   out_tokens int32 [batch, max_depth + 1]: the tokens drawn along the branch --
+ *     the accepted drafts and the next token -- then -1;
+ *   accepted int32 [batch]: the number of accepted drafts;
+ *   new_lens int32 [batch] or NULL: the cached length without the rejected nodes,
+ *     seq_lens[b] - nodes + 1 + accepted (not seq_lens itself).
+ * A sequence without nodes has accepted 0, no token and its own length.
+ * In each of the n_caches caches (host array of descriptors, all layers in one
+ * launch for up to 32 of them; pages of one size, found by one page table; n_caches
+ * 0: none) the d-th accepted node's keys and values move to the place d behind the
+ * root's; what lies behind them stays.  Caches must not overlap.  Drafts drawn from
+ * the sequence's own distribution at each node keep that distribution: whatever the
+ * drafts are, the tokens given out are the ones drawn.
+ * Memory safety does not depend on the device arrays: a move from or to a page or
+ * position outside the cache, max_kv or the table is not made.  Enqueue-only.
+ */
+ql_status qlinear_tree_commit(int64_t batch, int64_t tokens, int64_t max_depth, int64_t max_kv, const ql_kv_cache* caches,
+                              int32_t n_caches, const int32_t* page_table, int64_t table_stride, const int32_t* seq_lens,
+                              const int32_t* cu_q, const int32_t* node_tokens, const int32_t* parents,
+                              const int32_t* sampled, int32_t* out_tokens, int32_t* accepted, int32_t* new_lens,
+                              void* stream);
+
+/*
  * Verification of drafted tokens.  Sequence b has the drafts cu_drafts[b] ..
  * cu_drafts[b+1] - 1 (int32 [batch + 1], cu_drafts[0] = 0; at most max_drafts
  * of them) of draft_tokens, of the draft's probabilities draft_probs [n_drafts,

@@ -578,8 +578,9 @@ def load_default_table():
 
 # ----------------------------------------------------------------- serving operators around the linears
 
-from .serving import (KV_BF16, KV_E4M3, AttentionPlan, LoraStack, PagedCache, lora_workspace,  # noqa: E402
-                      qlinear_attention, qlinear_attention_plan, qlinear_lora, qlinear_lora_workspace_bytes,
-                      qlinear_qk_norm_rope, qlinear_qkv_append, qlinear_sample, qlinear_sample_workspace_bytes,
-                      qlinear_verify_draft, qlinear_verify_workspace_bytes, rope_table, sample_workspace,
-                      verify_workspace)
+from .serving import (KV_BF16, KV_E4M3, AttentionPlan, LoraStack, PagedCache, TreeAttentionPlan,  # noqa: E402
+                      lora_workspace, qlinear_attention, qlinear_attention_plan, qlinear_lora,
+                      qlinear_lora_workspace_bytes, qlinear_qk_norm_rope, qlinear_qkv_append, qlinear_sample,
+                      qlinear_sample_workspace_bytes, qlinear_tree_attention, qlinear_tree_attention_plan,
+                      qlinear_tree_commit, qlinear_verify_draft, qlinear_verify_workspace_bytes, rope_table,
+                      sample_workspace, verify_workspace)

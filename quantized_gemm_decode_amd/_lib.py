@@ -104,6 +104,9 @@ SIGNATURES = {
     "qlinear_attention_workspace_bytes": (c_i64, [c_vp]),
     "qlinear_attention_plan_destroy": (None, [c_vp]),
     "qlinear_attention": (c_i32, [c_vp, c_rows, c_cache, c_vp, c_i64, c_vp, c_vp, c_rows, c_vp, c_vp, c_vp]),
+    "qlinear_tree_attention_plan": (c_i32, [ctypes.POINTER(QLAttentionShape), ctypes.POINTER(c_vp)]),
+    "qlinear_tree_attention": (c_i32, [c_vp, c_rows, c_cache, c_vp, c_i64, c_vp, c_vp, c_vp, c_i64, c_rows, c_vp, c_vp, c_vp]),
+    "qlinear_tree_commit": (c_i32, [c_i64] * 4 + [c_cache, c_i32, c_vp, c_i64] + [c_vp] * 9),
     "qlinear_verify_workspace_bytes": (c_i64, [c_i64, c_i64]),
     "qlinear_verify_draft": (c_i32, [c_i64] * 4 + [c_vp] * 10),
     "qlinear_lora_workspace_bytes": (c_i64, [ctypes.POINTER(QLLora), c_i64]),

@@ -33,6 +33,7 @@ struct Part {
 struct ql_attention_plan_s {
   ql_attention_shape shape;
   Part stream, tile;
+  bool tree;      // of drafted tokens: rows see what their token's bits name
   int tile_from;  // rows of a sequence from which it goes to the tile kernel
 };
 
@@ -246,6 +247,138 @@ ql_status plan_stream(const ql_attention_shape& s, int64_t rows, Part* p) {
   return QL_OK;
 }
 
+// A plan for either kind of attention.
+ql_status new_plan(const ql_attention_shape* s, bool tree, ql_attention_plan* out) {
+  if (!out) return fail(QL_E_INVALID, "out_plan is NULL");
+  *out = nullptr;
+  if (!s) return fail(QL_E_INVALID, "shape is NULL");
+  if (s->batch < 0 || s->tokens < 0 || s->max_q < 0 || s->max_kv < 0) return fail(QL_E_INVALID, "negative size");
+  if (s->tokens > kMaxTokens || s->max_q > kMaxTokens || s->batch > 65536 || s->max_kv > (int64_t(1) << 30))
+    return fail(QL_E_UNSUPPORTED, "more than 2^24 new tokens, 2^16 sequences or 2^30 cached tokens");
+  if (s->kv_heads < 1 || s->q_heads < 1 || s->q_heads % s->kv_heads)
+    return fail(QL_E_INVALID, "q_heads %d must be a positive multiple of kv_heads %d", s->q_heads, s->kv_heads);
+  if (s->q_heads > 65536) return fail(QL_E_UNSUPPORTED, "more than 2^16 heads");
+  if (s->head_dim != 64 && s->head_dim != 128) return fail(QL_E_UNSUPPORTED, "head_dim %d must be 64 or 128", s->head_dim);
+  if (s->kv_type != QL_KV_BF16 && s->kv_type != QL_KV_E4M3) return fail(QL_E_INVALID, "unknown cache type %d", s->kv_type);
+  ql_status st = check_page_size(s->page_size);
+  if (st != QL_OK) return st;
+  if (s->causal != 0 && s->causal != 1) return fail(QL_E_INVALID, "causal must be 0 or 1");
+  if (s->window < 0 || (s->window && !s->causal)) return fail(QL_E_INVALID, "a window is >= 0 and causal");
+  if (tree && (!s->causal || s->window)) return fail(QL_E_INVALID, "a tree is causal and has no window");
+  if (!std::isfinite(s->scale) || s->scale < 0.0f) return fail(QL_E_INVALID, "scale must be finite and >= 0");
+  const int64_t group = s->q_heads / s->kv_heads;
+  const int64_t max_q = std::min(s->max_q, s->tokens);  // no sequence has more new tokens than there are
+  const int64_t rows = max_q * group;
+  if (rows > (int64_t(1) << 30)) return fail(QL_E_UNSUPPORTED, "max_q * q_heads / kv_heads exceeds 2^30");
+  ql_attention_plan_s* p = new (std::nothrow) ql_attention_plan_s();
+  if (!p) return fail(QL_E_INVALID, "out of host memory");
+  p->shape = *s;
+  p->tree = tree;
+  // as long as any context: no window (and no position minus the window leaves 32 bits)
+  if (s->window >= s->max_kv) p->shape.window = 0;
+  s = &p->shape;
+  const bool chunks = rows > kStreamRows;
+  // Sequences of few rows among longer ones get a launch of their own where
+  // there can be many of them with long contexts: to the tile kernel each is a
+  // workgroup of mostly idle rows for each KV head.  By the (sequence, KV head,
+  // key) triples that this would take, apart and together, us: 48 k (a chunk of 64
+  // and 7 x 1,000) 34 and 24; 84 k (12 sequences, 701 new tokens at most, window
+  // 2048, 64-wide) 103 and 93; 240 k (4 x 128 and 60 x 500, 64-wide) 35 and 35; 480 k
+  // (256 and 15 x 4,000) 116 and 112; 504 k (100 and 63 x 1,000) 76 and 118; 744 k
+  // (1,024 and 31 x 3,000) 116 and 227; 4 M (512 and 63 x 8,000) 491 and 974.
+  const int64_t few = max_q > 0 ? s->batch - (s->tokens + max_q - 1) / max_q : 0;
+  // (More query heads a KV head than that launch takes rows: none would go there.)
+  const bool mixed = chunks && group <= kMixedRows && few * s->kv_heads * tile_span(*s) > 160000;
+  p->tile_from = mixed ? kMixedRows + 1 : 0;
+  if (!chunks || mixed) st = plan_stream(*s, mixed ? kMixedRows : rows, &p->stream);
+  if (st == QL_OK && chunks) st = plan_tile(*s, rows, p->stream.end, &p->tile);
+  if (st != QL_OK) {
+    delete p;
+    return st;
+  }
+  *out = p;
+  return QL_OK;
+}
+
+// One call of a plan; sees, words: trees only.
+ql_status run_plan(ql_attention_plan p, const ql_rows* q, const ql_kv_cache* cache, const int32_t* page_table,
+                   int64_t table_stride, const int32_t* seq_lens, const int32_t* cu_q, const uint64_t* sees, int64_t words,
+                   const ql_rows* out, float* lse, void* workspace, void* stream) {
+  if (!p) return fail(QL_E_INVALID, "plan is NULL");
+  const ql_attention_shape& s = p->shape;
+  qlk::AttnArgs a{};
+  ql_status st = check_cache(cache, &a.kc, &a.vc);
+  if (st != QL_OK) return st;
+  if (cache->type != s.kv_type || cache->kv_heads != s.kv_heads || cache->head_dim != s.head_dim ||
+      cache->page_size != s.page_size)
+    return fail(QL_E_INVALID, "the cache is not of the plan's type, heads, head_dim and page_size");
+  if (s.batch == 0 || s.tokens == 0 || s.max_q == 0) return QL_OK;
+  if ((st = check_rows(q, "q", s.q_heads, &a.q)) != QL_OK || (st = check_rows(out, "out", s.q_heads, &a.out)) != QL_OK) return st;
+  if ((!page_table && s.max_kv > 0) || !seq_lens || !cu_q) return fail(QL_E_INVALID, "page_table, seq_lens or cu_q is NULL");
+  if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(lse, 4))
+    return fail(QL_E_ALIGN, "page_table, seq_lens, cu_q and lse must be 4-byte aligned");
+  if (s.batch > 1 && table_stride < (s.max_kv + s.page_size - 1) / s.page_size)
+    return fail(QL_E_INVALID, "page_table rows hold fewer than ceil(max_kv / page_size) entries");
+  if (p->tree) {
+    if (!sees) return fail(QL_E_INVALID, "sees is NULL");
+    if (!aligned(sees, 8)) return fail(QL_E_ALIGN, "sees is not 8-byte aligned");
+    if (words < (std::min(s.max_q, s.tokens) + 63) / 64 || words > (int64_t(1) << 20))
+      return fail(QL_E_INVALID, "rows of sees hold fewer bits than max_q");
+  }
+  if (qlinear_attention_workspace_bytes(p) > 0 && !workspace) return fail(QL_E_INVALID, "this plan needs a workspace");
+  if (!aligned16(workspace)) return fail(QL_E_ALIGN, "workspace is not 16-byte aligned");
+  // without any context the table may have no entry, but the decode kernel looks
+  // up a page for every sequence (and clamps it)
+  a.table = s.max_kv > 0 ? page_table : seq_lens;
+  a.table_row = s.max_kv > 0 ? table_stride : 0;
+  a.seq_lens = seq_lens;
+  a.cu_q = cu_q;
+  a.lse = lse;
+  a.page_magic = page_magic(s.page_size);
+  const float scale = s.scale != 0.0f ? s.scale : 1.0f / std::sqrt((float)s.head_dim);
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.batch = (int)s.batch;
+  a.tokens = (int)s.tokens;
+  a.q_heads = s.q_heads;
+  a.kv_heads = s.kv_heads;
+  a.group = s.q_heads / s.kv_heads;
+  a.page_size = s.page_size;
+  a.num_pages = (int)cache->num_pages;
+  a.max_kv = (int)s.max_kv;
+  a.sees = sees;
+  a.words = (int)words;
+  a.causal = p->tree ? 0 : s.causal;   // a tree's rows end where their bits do
+  a.window = s.window;
+  hipStream_t hs = static_cast<hipStream_t>(stream);
+  const bool e4m3 = s.kv_type == QL_KV_E4M3;
+  auto partials = [&](const Part& x) {
+    a.part_o = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x.o_at) : nullptr;
+    a.part_ml = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x.ml_at) : nullptr;
+  };
+  hipError_t e = hipSuccess;
+  if (p->stream.used) {
+    const Part& x = p->stream;
+    partials(x);
+    a.slots = x.slots;
+    a.heads_wg = x.heads_wg;
+    a.max_rows = x.most;
+    e = qlk::launch_attn_stream(a, s.head_dim, e4m3, x.rows, hs);
+    if (e == hipSuccess && x.splits > 1) e = qlk::launch_attn_stream_join(a, s.head_dim, x.rows, x.most, hs);
+  }
+  if (e == hipSuccess && p->tile.used) {
+    const Part& x = p->tile;
+    partials(x);
+    a.row_blocks = x.row_blocks;
+    a.by_rows = x.by_rows;
+    a.splits = x.splits;
+    a.chunk = x.chunk;
+    a.min_rows = p->tile_from;
+    e = qlk::launch_attn_tile(a, s.head_dim, e4m3, x.units, hs);
+    if (e == hipSuccess && x.splits > 1) e = qlk::launch_attn_join(a, s.head_dim, x.rows, hs);
+  }
+  return e == hipSuccess ? QL_OK : hip_fail(e, "attention launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -287,55 +420,9 @@ ql_status qlinear_qkv_append(const ql_norm_rope* rule, int64_t tokens, int32_t q
   return e == hipSuccess ? QL_OK : hip_fail(e, "cache append launch");
 }
 
-ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan* out) {
-  if (!out) return fail(QL_E_INVALID, "out_plan is NULL");
-  *out = nullptr;
-  if (!s) return fail(QL_E_INVALID, "shape is NULL");
-  if (s->batch < 0 || s->tokens < 0 || s->max_q < 0 || s->max_kv < 0) return fail(QL_E_INVALID, "negative size");
-  if (s->tokens > kMaxTokens || s->max_q > kMaxTokens || s->batch > 65536 || s->max_kv > (int64_t(1) << 30))
-    return fail(QL_E_UNSUPPORTED, "more than 2^24 new tokens, 2^16 sequences or 2^30 cached tokens");
-  if (s->kv_heads < 1 || s->q_heads < 1 || s->q_heads % s->kv_heads)
-    return fail(QL_E_INVALID, "q_heads %d must be a positive multiple of kv_heads %d", s->q_heads, s->kv_heads);
-  if (s->q_heads > 65536) return fail(QL_E_UNSUPPORTED, "more than 2^16 heads");
-  if (s->head_dim != 64 && s->head_dim != 128) return fail(QL_E_UNSUPPORTED, "head_dim %d must be 64 or 128", s->head_dim);
-  if (s->kv_type != QL_KV_BF16 && s->kv_type != QL_KV_E4M3) return fail(QL_E_INVALID, "unknown cache type %d", s->kv_type);
-  ql_status st = check_page_size(s->page_size);
-  if (st != QL_OK) return st;
-  if (s->causal != 0 && s->causal != 1) return fail(QL_E_INVALID, "causal must be 0 or 1");
-  if (s->window < 0 || (s->window && !s->causal)) return fail(QL_E_INVALID, "a window is >= 0 and causal");
-  if (!std::isfinite(s->scale) || s->scale < 0.0f) return fail(QL_E_INVALID, "scale must be finite and >= 0");
-  const int64_t group = s->q_heads / s->kv_heads;
-  const int64_t max_q = std::min(s->max_q, s->tokens);  // no sequence has more new tokens than there are
-  const int64_t rows = max_q * group;
-  if (rows > (int64_t(1) << 30)) return fail(QL_E_UNSUPPORTED, "max_q * q_heads / kv_heads exceeds 2^30");
-  ql_attention_plan_s* p = new (std::nothrow) ql_attention_plan_s();
-  if (!p) return fail(QL_E_INVALID, "out of host memory");
-  p->shape = *s;
-  // as long as any context: no window (and no position minus the window leaves 32 bits)
-  if (s->window >= s->max_kv) p->shape.window = 0;
-  s = &p->shape;
-  const bool chunks = rows > kStreamRows;
-  // Sequences of few rows among longer ones get a launch of their own where
-  // there can be many of them with long contexts: to the tile kernel each is a
-  // workgroup of mostly idle rows for each KV head.  By the (sequence, KV head,
-  // key) triples that this would take, apart and together, us: 48 k (a chunk of 64
-  // and 7 x 1,000) 34 and 24; 84 k (12 sequences, 701 new tokens at most, window
-  // 2048, 64-wide) 103 and 93; 240 k (4 x 128 and 60 x 500, 64-wide) 35 and 35; 480 k
-  // (256 and 15 x 4,000) 116 and 112; 504 k (100 and 63 x 1,000) 76 and 118; 744 k
-  // (1,024 and 31 x 3,000) 116 and 227; 4 M (512 and 63 x 8,000) 491 and 974.
-  const int64_t few = max_q > 0 ? s->batch - (s->tokens + max_q - 1) / max_q : 0;
-  // (More query heads a KV head than that launch takes rows: none would go there.)
-  const bool mixed = chunks && group <= kMixedRows && few * s->kv_heads * tile_span(*s) > 160000;
-  p->tile_from = mixed ? kMixedRows + 1 : 0;
-  if (!chunks || mixed) st = plan_stream(*s, mixed ? kMixedRows : rows, &p->stream);
-  if (st == QL_OK && chunks) st = plan_tile(*s, rows, p->stream.end, &p->tile);
-  if (st != QL_OK) {
-    delete p;
-    return st;
-  }
-  *out = p;
-  return QL_OK;
-}
+ql_status qlinear_attention_plan(const ql_attention_shape* s, ql_attention_plan* out) { return new_plan(s, false, out); }
+
+ql_status qlinear_tree_attention_plan(const ql_attention_shape* s, ql_attention_plan* out) { return new_plan(s, true, out); }
 
 ql_status qlinear_attention_plan_info(ql_attention_plan p, ql_attention_facts* facts) {
   if (!p || !facts) return fail(QL_E_INVALID, "NULL argument");
@@ -352,71 +439,16 @@ void qlinear_attention_plan_destroy(ql_attention_plan p) { delete p; }
 ql_status qlinear_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_cache* cache,
                             const int32_t* page_table, int64_t table_stride, const int32_t* seq_lens,
                             const int32_t* cu_q, const ql_rows* out, float* lse, void* workspace, void* stream) {
-  if (!p) return fail(QL_E_INVALID, "plan is NULL");
-  const ql_attention_shape& s = p->shape;
-  qlk::AttnArgs a{};
-  ql_status st = check_cache(cache, &a.kc, &a.vc);
-  if (st != QL_OK) return st;
-  if (cache->type != s.kv_type || cache->kv_heads != s.kv_heads || cache->head_dim != s.head_dim ||
-      cache->page_size != s.page_size)
-    return fail(QL_E_INVALID, "the cache is not of the plan's type, heads, head_dim and page_size");
-  if (s.batch == 0 || s.tokens == 0 || s.max_q == 0) return QL_OK;
-  if ((st = check_rows(q, "q", s.q_heads, &a.q)) != QL_OK || (st = check_rows(out, "out", s.q_heads, &a.out)) != QL_OK) return st;
-  if ((!page_table && s.max_kv > 0) || !seq_lens || !cu_q) return fail(QL_E_INVALID, "page_table, seq_lens or cu_q is NULL");
-  if (!aligned(page_table, 4) || !aligned(seq_lens, 4) || !aligned(cu_q, 4) || !aligned(lse, 4))
-    return fail(QL_E_ALIGN, "page_table, seq_lens, cu_q and lse must be 4-byte aligned");
-  if (s.batch > 1 && table_stride < (s.max_kv + s.page_size - 1) / s.page_size)
-    return fail(QL_E_INVALID, "page_table rows hold fewer than ceil(max_kv / page_size) entries");
-  if (qlinear_attention_workspace_bytes(p) > 0 && !workspace) return fail(QL_E_INVALID, "this plan needs a workspace");
-  if (!aligned16(workspace)) return fail(QL_E_ALIGN, "workspace is not 16-byte aligned");
-  // without any context the table may have no entry, but the decode kernel looks
-  // up a page for every sequence (and clamps it)
-  a.table = s.max_kv > 0 ? page_table : seq_lens;
-  a.table_row = s.max_kv > 0 ? table_stride : 0;
-  a.seq_lens = seq_lens;
-  a.cu_q = cu_q;
-  a.lse = lse;
-  a.page_magic = page_magic(s.page_size);
-  const float scale = s.scale != 0.0f ? s.scale : 1.0f / std::sqrt((float)s.head_dim);
-  a.scale_log2 = scale * 1.4426950408889634f;
-  a.batch = (int)s.batch;
-  a.tokens = (int)s.tokens;
-  a.q_heads = s.q_heads;
-  a.kv_heads = s.kv_heads;
-  a.group = s.q_heads / s.kv_heads;
-  a.page_size = s.page_size;
-  a.num_pages = (int)cache->num_pages;
-  a.max_kv = (int)s.max_kv;
-  a.causal = s.causal;
-  a.window = s.window;
-  hipStream_t hs = static_cast<hipStream_t>(stream);
-  const bool e4m3 = s.kv_type == QL_KV_E4M3;
-  auto partials = [&](const Part& x) {
-    a.part_o = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x.o_at) : nullptr;
-    a.part_ml = workspace ? reinterpret_cast<float*>(static_cast<char*>(workspace) + x.ml_at) : nullptr;
-  };
-  hipError_t e = hipSuccess;
-  if (p->stream.used) {
-    const Part& x = p->stream;
-    partials(x);
-    a.slots = x.slots;
-    a.heads_wg = x.heads_wg;
-    a.max_rows = x.most;
-    e = qlk::launch_attn_stream(a, s.head_dim, e4m3, x.rows, hs);
-    if (e == hipSuccess && x.splits > 1) e = qlk::launch_attn_stream_join(a, s.head_dim, x.rows, x.most, hs);
-  }
-  if (e == hipSuccess && p->tile.used) {
-    const Part& x = p->tile;
-    partials(x);
-    a.row_blocks = x.row_blocks;
-    a.by_rows = x.by_rows;
-    a.splits = x.splits;
-    a.chunk = x.chunk;
-    a.min_rows = p->tile_from;
-    e = qlk::launch_attn_tile(a, s.head_dim, e4m3, x.units, hs);
-    if (e == hipSuccess && x.splits > 1) e = qlk::launch_attn_join(a, s.head_dim, x.rows, hs);
-  }
-  return e == hipSuccess ? QL_OK : hip_fail(e, "attention launch");
+  if (p && p->tree) return fail(QL_E_INVALID, "the plan is for trees");
+  return run_plan(p, q, cache, page_table, table_stride, seq_lens, cu_q, nullptr, 0, out, lse, workspace, stream);
+}
+
+ql_status qlinear_tree_attention(ql_attention_plan p, const ql_rows* q, const ql_kv_cache* cache,
+                                 const int32_t* page_table, int64_t table_stride, const int32_t* seq_lens,
+                                 const int32_t* cu_q, const uint64_t* sees, int64_t sees_words, const ql_rows* out,
+                                 float* lse, void* workspace, void* stream) {
+  if (p && !p->tree) return fail(QL_E_INVALID, "the plan is not for trees");
+  return run_plan(p, q, cache, page_table, table_stride, seq_lens, cu_q, sees, sees_words, out, lse, workspace, stream);
 }
 
 // Slices of a vocabulary row: enough workgroups for the card with few
@@ -467,6 +499,69 @@ ql_status qlinear_verify_draft(int64_t batch, int64_t n_drafts, int64_t max_draf
   a.slices = verify_slices(batch, vocab);
   hipError_t e = qlk::launch_verify(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? QL_OK : hip_fail(e, "draft verification launch");
+}
+
+ql_status qlinear_tree_commit(int64_t batch, int64_t tokens, int64_t max_depth, int64_t max_kv, const ql_kv_cache* caches,
+                              int32_t n_caches, const int32_t* page_table, int64_t table_stride, const int32_t* seq_lens,
+                              const int32_t* cu_q, const int32_t* node_tokens, const int32_t* parents,
+                              const int32_t* sampled, int32_t* out_tokens, int32_t* accepted, int32_t* new_lens,
+                              void* stream) {
+  if (batch < 0 || tokens < 0 || max_depth < 0 || max_kv < 0 || n_caches < 0) return fail(QL_E_INVALID, "negative size");
+  if (batch > 65536 || tokens > kMaxTokens || max_kv > (int64_t(1) << 30) || n_caches > 4096)
+    return fail(QL_E_UNSUPPORTED, "more than 2^16 sequences, 2^24 nodes, 2^30 cached tokens or 2^12 caches");
+  if (max_depth > qlk::kCommitDepth) return fail(QL_E_UNSUPPORTED, "max_depth exceeds %d", qlk::kCommitDepth);
+  if (n_caches > 0 && !caches) return fail(QL_E_INVALID, "caches is NULL");
+  qlk::CommitArgs a{};
+  a.page_size = 16;
+  a.num_pages = int64_t(1) << 31;
+  ql_status st;
+  for (int i = 0; i < n_caches; ++i) {
+    qlk::Pages k, v;
+    if ((st = check_cache(caches + i, &k, &v)) != QL_OK) return st;
+    if (!norm_dim(caches[i].head_dim)) return fail(QL_E_UNSUPPORTED, "head_dim %d must be 64, 128 or 256", caches[i].head_dim);
+    if (caches[i].page_size != caches[0].page_size) return fail(QL_E_INVALID, "the caches have pages of different sizes");
+    a.page_size = caches[i].page_size;
+    a.num_pages = std::min(a.num_pages, caches[i].num_pages);
+  }
+  if (batch == 0) return QL_OK;
+  if (!seq_lens || !cu_q || !out_tokens || !accepted) return fail(QL_E_INVALID, "NULL pointer");
+  if (tokens > 0 && (!node_tokens || !parents || !sampled)) return fail(QL_E_INVALID, "node_tokens, parents or sampled is NULL");
+  if (n_caches > 0 && max_kv > 0 && !page_table) return fail(QL_E_INVALID, "page_table is NULL");
+  if (n_caches > 0 && batch > 1 && table_stride < (max_kv + a.page_size - 1) / a.page_size)
+    return fail(QL_E_INVALID, "page_table rows hold fewer than ceil(max_kv / page_size) entries");
+  if (new_lens == seq_lens) return fail(QL_E_INVALID, "new_lens must not be seq_lens");
+  for (const void* p : {(const void*)page_table, (const void*)seq_lens, (const void*)cu_q, (const void*)node_tokens,
+                        (const void*)parents, (const void*)sampled, (const void*)out_tokens, (const void*)accepted,
+                        (const void*)new_lens})
+    if (!aligned(p, 4)) return fail(QL_E_ALIGN, "pointers must be 4-byte aligned");
+  a.table = page_table;
+  a.table_row = table_stride;
+  a.seq_lens = seq_lens;
+  a.cu_q = cu_q;
+  a.node_tokens = node_tokens;
+  a.parents = parents;
+  a.sampled = sampled;
+  a.out_tokens = out_tokens;
+  a.accepted = accepted;
+  a.new_lens = new_lens;
+  a.batch = (int)batch;
+  a.tokens = (int)tokens;
+  a.max_depth = (int)max_depth;
+  a.max_kv = (int)max_kv;
+  hipError_t e = hipSuccess;
+  for (int i = 0; e == hipSuccess && (i == 0 || i < n_caches); i += qlk::kCommitLayers) {
+    a.layers = std::min(n_caches - i, qlk::kCommitLayers);
+    for (int j = 0; j < a.layers; ++j) {
+      const ql_kv_cache& c = caches[i + j];
+      qlk::CommitLayer& l = a.layer[j];
+      check_cache(&c, &l.k, &l.v);
+      l.kv_heads = c.kv_heads;
+      l.head_bytes = c.head_dim * (c.type == QL_KV_E4M3 ? 1 : 2);
+    }
+    e = qlk::launch_tree_commit(a, static_cast<hipStream_t>(stream));
+    a.out_tokens = nullptr;
+  }
+  return e == hipSuccess ? QL_OK : hip_fail(e, "tree commit launch");
 }
 
 }  // extern "C"

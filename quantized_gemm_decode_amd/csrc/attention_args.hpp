@@ -49,8 +49,10 @@ struct AttnArgs {
                          // the tile kernel, [slots, 2, kv_heads, R] rows of the stream kernel
   float* part_ml;        // their rows' maxima (base 2) and sums
   uint64_t page_magic;
+  const uint64_t* sees;  // trees of drafts: [tokens, words] new tokens of its sequence that a token sees, one a bit
   float scale_log2;      // softmax scale * log2(e)
   int batch, tokens, q_heads, kv_heads, group, page_size, num_pages, max_kv, causal, window;
+  int words;             // of a row of `sees`
   // tile kernel
   int row_blocks;        // most blocks of R (token, head of the group) rows of a sequence and KV head
   int by_rows;           // numbering of the units (see unit_at)
@@ -76,6 +78,30 @@ struct VerifyArgs {
   int batch, vocab, max_drafts, slices;
 };
 
+constexpr int kCommitLayers = 32;     // caches of one launch
+constexpr int kCommitDepth = 1024;    // most accepted tokens of a sequence
+
+struct CommitLayer {
+  Pages k, v;
+  int kv_heads, head_bytes;
+};
+
+struct CommitArgs {
+  const int32_t* table;        // page of each (sequence, page column)
+  int64_t table_row;
+  const int32_t* seq_lens;
+  const int32_t* cu_q;
+  const int32_t* node_tokens;  // [tokens]
+  const int32_t* parents;
+  const int32_t* sampled;
+  int32_t* out_tokens;         // [batch, max_depth + 1]; null: not this launch's to write
+  int32_t* accepted;           // [batch]
+  int32_t* new_lens;           // [batch] or null
+  int64_t num_pages;           // of the smallest cache
+  int batch, tokens, max_depth, max_kv, page_size, layers;
+  CommitLayer layer[kCommitLayers];
+};
+
 constexpr int kPageMagicShift = 36;
 
 // The page column of the 16-key group `sub` (page_size / 16 groups a page):
@@ -95,10 +121,12 @@ constexpr int kVerifySlice = 4096;
 hipError_t launch_heads(const HeadArgs& a, int head_dim, bool append, bool e4m3, hipStream_t s);
 // Slots of the stream kernel: as many as the card holds waves for each KV head.
 int attn_stream_slots(int head_dim, bool e4m3, int rows, int kv_heads, int heads_wg);
+// (Attention for trees where a.sees is given.)
 hipError_t launch_attn_stream(const AttnArgs& a, int head_dim, bool e4m3, int rows, hipStream_t s);
 hipError_t launch_attn_stream_join(const AttnArgs& a, int head_dim, int rows, int most_rows, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, bool e4m3, int units, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, hipStream_t s);
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
+hipError_t launch_tree_commit(const CommitArgs& a, hipStream_t s);
 
 }  // namespace qlk

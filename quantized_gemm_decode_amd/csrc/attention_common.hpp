@@ -174,6 +174,19 @@ __device__ __forceinline__ void row_range(const AttnArgs& a, const Unit& u, int 
   *lo = a.window ? max(0, p - a.window + 1) : 0;
 }
 
+// Trees of drafted tokens (TREE; a.causal and a.window are 0 then): a row sees
+// the keys before the sequence's new tokens and those of these that its token's
+// bits name.  Which of the 32 keys from the `node`-th new token on (below 0:
+// keys before them) token `tok` sees, one a bit.
+__device__ __forceinline__ uint32_t tree_bits(const AttnArgs& a, int tok, int node) {
+  const uint64_t* bits = a.sees + (int64_t)tok * a.words;
+  if (node < 0) return node <= -32 ? 0xffffffffu : (uint32_t)(bits[0] << -node) | ((1u << -node) - 1);
+  const int w = node >> 6, s = node & 63;
+  uint64_t x = w < a.words ? bits[w] >> s : 0;
+  if (s > 32 && w + 1 < a.words) x |= bits[w + 1] << (64 - s);
+  return (uint32_t)x;
+}
+
 // Where 64 16-key groups of a sequence lie: lane i holds the byte offsets of
 // group `group` of its own in K and V.  One gather of page numbers and one
 // round of address arithmetic serve 64 groups; a wave then picks a group by

@@ -244,7 +244,7 @@ constexpr int stream_workgroups(int D, bool e4m3, int row_tiles) { return e4m3 &
 // 3,000 keys 47.0 and 47.9 us, 8,000 keys 109.7 and 109.6).
 constexpr int stream_depth(int D, bool e4m3, int row_tiles) { return stream_workgroups(D, e4m3, row_tiles) == 1 ? 2 : 1; }
 
-template <int D, bool E4M3, int NR>
+template <int D, bool E4M3, int NR, bool TREE>
 __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, NR)) attn_stream_kernel(AttnArgs a) {
   constexpr int R = 16 * NR, DT = D / 16;
   constexpr int KS = D / 32;  // products over D of one 16-key group
@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
     }
     // keys that every row sees
     const int full_lo = a.window ? max(0, pos0 + (rows - 1) / a.group - a.window + 1) : 0;
-    const int full_hi = a.causal ? min(s.len, max(0, pos0 + 1)) : s.len;
+    const int full_hi = TREE ? min(s.len, max(0, pos0)) : a.causal ? min(s.len, max(0, pos0 + 1)) : s.len;
     auto is_whole = [&](int key) { return key >= full_lo && key + 32 <= full_hi; };
     const int key0 = key;
     bool dropped = false;
@@ -370,10 +370,12 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
         if (!whole) {
           int first = key + 4 * g;
           pin(first);
+          uint32_t bits = 0xffffffffu;
+          if (TREE) bits = tree_bits(a, s.first + min(16 * n + r, rows - 1) / a.group, key - pos0) >> 4 * g;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             const int k = first + 16 * (j / 4) + j % 4;
-            x[n][j] = k >= lo[n] && k < hi[n] ? x[n][j] : kNegInf;
+            x[n][j] = k >= lo[n] && k < hi[n] && (!TREE || bits >> (16 * (j / 4) + j % 4) & 1) ? x[n][j] : kNegInf;
           }
         }
         float top = x[n][0];
@@ -431,12 +433,14 @@ __global__ void __launch_bounds__(kStreamWaves * 64, stream_workgroups(D, E4M3, 
           int d0 = 4 * g * DT;
           pin(d0);
 #pragma unroll
-          for (int n = 0; n < NR; ++n)
+          for (int n = 0; n < NR; ++n) {
+            const bool named = !TREE || (tree_bits(a, s.first + min(16 * n + r, rows - 1) / a.group, k - pos0) & 1);
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
               for (int j = 0; j < 4; ++j)
-                if (k >= lo[n] && k < hi[n] && bad_at<D>(bad, d0 + j * DT + dt)) o[n][dt][j] = __uint_as_float(0x7fc00000u);
+                if (named && k >= lo[n] && k < hi[n] && bad_at<D>(bad, d0 + j * DT + dt)) o[n][dt][j] = __uint_as_float(0x7fc00000u);
+          }
         });
       }
     }
@@ -595,7 +599,10 @@ __global__ void __launch_bounds__(kJoinWaves * 64) attn_join_kernel(AttnArgs a, 
 template <int D, bool E4M3, int NR>
 static hipError_t launch_stream(const AttnArgs& a, hipStream_t s) {
   const unsigned grid = (unsigned)(a.slots / (kStreamWaves / a.heads_wg)) * (unsigned)(a.kv_heads / a.heads_wg);
-  hipLaunchKernelGGL((attn_stream_kernel<D, E4M3, NR>), dim3(grid), dim3(kStreamWaves * 64), 0, s, a);
+  if (a.sees)
+    hipLaunchKernelGGL((attn_stream_kernel<D, E4M3, NR, true>), dim3(grid), dim3(kStreamWaves * 64), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_stream_kernel<D, E4M3, NR, false>), dim3(grid), dim3(kStreamWaves * 64), 0, s, a);
   return hipGetLastError();
 }
 

@@ -295,7 +295,7 @@ __device__ __forceinline__ void inner_step(const uint8_t* kl, int kt, const uint
 // with two; 8 chunks of 512 at 2,000, bf16: 96 and 102 us.)
 constexpr int tile_workgroups(int D) { return D == 64 ? 3 : 2; }
 
-template <int D, bool E4M3>
+template <int D, bool E4M3, bool TREE>
 __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile_kernel(AttnArgs a) {
   constexpr int R = kTileRows, DT = D / 32, KS = D / 16;
   constexpr int kBytes = kTileKeys * D * 2;  // one tensor's tile
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
     int full_lo, full_hi, x;
     row_range(a, u, u.rows - 1, &full_lo, &x);
     row_range(a, u, 0, &x, &full_hi);
-    full_hi = min(full_hi, end);
+    full_hi = min(TREE ? max(0, u.pos0) : full_hi, end);
     const int32_t* table = a.table + u.b * a.table_row;
     const int last_sub = (u.len - 1) >> 4;
     using S = Staged<D, E4M3>;
@@ -356,16 +356,22 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
       row_range(a, u, x, lo, hi);
       *hi = x < u.rows ? min(*hi, end) : 0;
     };
+    // trees: which of the keys [key, key + 32) the lane's row sees
+    auto own_bits = [&](int key) {
+      return tree_bits(a, u.first + (u.row0 + min(own_row(), u.rows - 1)) / a.group, key - u.pos0);
+    };
     // masks the scores of keys [key, key + 32) where some row does not see all of them
     auto mask = [&](f32x16& s, int key) {
       if (key < full_lo || key + 32 > full_hi) {
         int first = key + 4 * g, lo, hi;
         pin(first);
         own_range(&lo, &hi);
+        uint32_t bits = 0xffffffffu;
+        if (TREE) bits = own_bits(key) >> 4 * g;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const int j = first + 8 * (i / 4) + i % 4;
-          s[i] = j >= lo && j < hi ? s[i] : kNegInf;
+          s[i] = j >= lo && j < hi && (!TREE || bits >> (8 * (i / 4) + i % 4) & 1) ? s[i] : kNegInf;
         }
       }
     };
@@ -479,11 +485,12 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
         for_nonfinite<D, E4M3>(a, table, h, key, min(kTileKeys, u.len - key), [&](int k, const uint64_t (&bad)[D / 64]) {
           int g4 = 4 * g;
           pin(g4);
+          const bool named = !TREE || (own_bits(k) & 1);
 #pragma unroll
           for (int dt = 0; dt < DT; ++dt)
 #pragma unroll
             for (int i = 0; i < 16; ++i)
-              if (k >= lo && k < hi && bad_at<D>(bad, 32 * dt + 8 * (i / 4) + g4 + i % 4))
+              if (named && k >= lo && k < hi && bad_at<D>(bad, 32 * dt + 8 * (i / 4) + g4 + i % 4))
                 o[dt][i] = __uint_as_float(0x7fc00000u);
         });
       }
@@ -529,8 +536,11 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
 
 template <int D, bool E4M3>
 static hipError_t launch_tile(const AttnArgs& a, int units, hipStream_t s) {
-  hipLaunchKernelGGL((attn_tile_kernel<D, E4M3>), dim3((unsigned)units * (unsigned)a.splits), dim3(kTileWaves * 64), 0, s,
-                     a);
+  const dim3 grid((unsigned)units * (unsigned)a.splits), threads(kTileWaves * 64);
+  if (a.sees)
+    hipLaunchKernelGGL((attn_tile_kernel<D, E4M3, true>), grid, threads, 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_tile_kernel<D, E4M3, false>), grid, threads, 0, s, a);
   return hipGetLastError();
 }
 

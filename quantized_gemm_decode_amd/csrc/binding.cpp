@@ -12,6 +12,8 @@
 #include <c10/hip/HIPGuard.h>
 #include <c10/hip/HIPStream.h>
 
+#include <vector>
+
 #include "../../include/qlinear.h"
 
 namespace {
@@ -29,6 +31,12 @@ int64_t number(PyObject* o) {
   if (v == -1 && PyErr_Occurred()) throw Refused();
   return v;
 }
+
+// A reference that the scope owns.
+struct Owned {
+  PyObject* o;
+  ~Owned() { Py_XDECREF(o); }
+};
 
 // One call's tensors: all on the GPU that the first one names.
 struct Call {
@@ -197,22 +205,28 @@ int64_t qkv_append(PyObject* const* a) {
                             c.stream(a[13]));
 }
 
-// plan, batch, tokens, q_heads, head_dim, columns, workspace bytes, q, cache, cache device, page_table, seq_lens, cu_q,
-// out, lse, workspace, stream
-int64_t attention(PyObject* const* a) {
-  Call c;
-  const int64_t batch = number(a[1]), columns = number(a[5]), need = number(a[6]);
-  int64_t tokens = number(a[2]), q_heads = number(a[3]), dim = number(a[4]);
-  const ql_rows q = c.rows(a[7], "q", tokens, q_heads, dim), out = c.rows(a[13], "out", tokens, q_heads, dim);
-  const ql_kv_cache* cache = c.cache(a[8], a[9]);
-  // rows may lie apart (the columns of a larger table), a row's entries not
-  const at::Tensor& t = c.tensor(a[10], "page_table", at::kInt, "torch.int32");
+// Page numbers of every sequence: rows may lie apart (the columns of a larger
+// table), a row's entries not.
+const at::Tensor& page_table(Call& c, PyObject* o, int64_t batch, int64_t columns) {
+  const at::Tensor& t = c.tensor(o, "page_table", at::kInt, "torch.int32");
   if (t.dim() != 2 || t.size(0) < batch || t.size(1) < columns) {
     PyErr_Format(PyExc_ValueError, "page_table must be a [batch, columns] tensor of at least (%lld, %lld)",
                  (long long)batch, (long long)columns);
     throw Refused();
   }
   if (t.size(1) > 1 && t.stride(1) != 1) refuse("page_table", "must have contiguous rows");
+  return t;
+}
+
+// plan, batch, tokens, q_heads, head_dim, columns, workspace bytes, q, cache, cache device, page_table, seq_lens, cu_q,
+// out, lse, workspace, stream; trees: sees, words of a row that it needs
+int64_t attend(PyObject* const* a, bool tree) {
+  Call c;
+  const int64_t batch = number(a[1]), columns = number(a[5]), need = number(a[6]);
+  int64_t tokens = number(a[2]), q_heads = number(a[3]), dim = number(a[4]);
+  const ql_rows q = c.rows(a[7], "q", tokens, q_heads, dim), out = c.rows(a[13], "out", tokens, q_heads, dim);
+  const ql_kv_cache* cache = c.cache(a[8], a[9]);
+  const at::Tensor& t = page_table(c, a[10], batch, columns);
   const int32_t* table = static_cast<const int32_t*>(t.data_ptr());
   const int32_t* lens = c.i32(a[11], "seq_lens", batch);
   const int32_t* cu = c.i32(a[12], "cu_q", batch + 1);
@@ -222,9 +236,60 @@ int64_t attention(PyObject* const* a) {
     workspace = c.bytes(a[15], "workspace", need);
   else if (need > 0)
     refuse("workspace", "is required by this plan");
+  const ql_attention_plan plan = static_cast<ql_attention_plan>(Call::number_ptr(a[0]));
+  if (!tree) {
+    const OnDevice on(c);
+    return qlinear_attention(plan, &q, cache, table, t.stride(0), lens, cu, &out, lse, workspace, c.stream(a[16]));
+  }
+  const int64_t words = number(a[18]);
+  const int64_t* sees = c.i64(a[17], "sees", 0);
+  const at::Tensor& m = THPVariable_Unpack(a[17]);
+  if (m.dim() != 2 || m.size(0) != tokens || m.size(1) < words) {
+    PyErr_Format(PyExc_ValueError, "sees must be a [tokens, words] tensor of (%lld, at least %lld)", (long long)tokens,
+                 (long long)words);
+    throw Refused();
+  }
   const OnDevice on(c);
-  return qlinear_attention(static_cast<ql_attention_plan>(Call::number_ptr(a[0])), &q, cache, table, t.stride(0), lens, cu,
-                           &out, lse, workspace, c.stream(a[16]));
+  return qlinear_tree_attention(plan, &q, cache, table, t.stride(0), lens, cu, reinterpret_cast<const uint64_t*>(sees),
+                                m.size(1), &out, lse, workspace, c.stream(a[16]));
+}
+
+int64_t attention(PyObject* const* a) { return attend(a, false); }
+int64_t tree_attention(PyObject* const* a) { return attend(a, true); }
+
+// caches (a list or tuple of PagedCache), page_table, max_kv, seq_lens, cu_q, node_tokens, parents, sampled, out_tokens,
+// accepted, new_lens, stream
+int64_t tree_commit(PyObject* const* a) {
+  Call c;
+  const int32_t* tokens = c.i32(a[5], "node_tokens", 0);
+  const int64_t n = THPVariable_Unpack(a[5]).numel();
+  int32_t* out = c.i32(a[8], "out_tokens", 0);
+  const at::Tensor& o = THPVariable_Unpack(a[8]);
+  if (o.dim() != 2 || o.size(1) < 1) refuse("out_tokens", "must be a [batch, max_depth + 1] tensor");
+  const int64_t batch = o.size(0);
+  if (!PyList_Check(a[0]) && !PyTuple_Check(a[0])) refuse("caches", "must be a list or tuple of PagedCache");
+  const Py_ssize_t layers = PySequence_Fast_GET_SIZE(a[0]);
+  std::vector<ql_kv_cache> caches(static_cast<size_t>(layers));
+  for (Py_ssize_t i = 0; i < layers; ++i) {
+    PyObject* cache = PySequence_Fast_GET_ITEM(a[0], i);
+    const Owned address{PyObject_GetAttrString(cache, "address")}, index{PyObject_GetAttrString(cache, "device_index")};
+    if (!address.o || !index.o) throw Refused();
+    caches[static_cast<size_t>(i)] = *c.cache(address.o, index.o);
+  }
+  const at::Tensor& t = page_table(c, a[1], batch, 0);
+  const int64_t most = layers ? t.size(1) * caches[0].page_size : int64_t(1) << 30;
+  const int64_t max_kv = a[2] == Py_None ? most : number(a[2]);
+  if (layers && max_kv > most) refuse("page_table", "has fewer columns than max_kv takes");
+  const int32_t* lens = c.i32(a[3], "seq_lens", batch);
+  const int32_t* cu = c.i32(a[4], "cu_q", batch + 1);
+  const int32_t* parents = c.i32(a[6], "parents", n);
+  const int32_t* sampled = c.i32(a[7], "sampled", n);
+  int32_t* accepted = c.i32(a[9], "accepted", batch);
+  int32_t* new_lens = a[10] == Py_None ? nullptr : c.i32(a[10], "new_lens", batch);
+  const OnDevice on(c);
+  return qlinear_tree_commit(batch, n, o.size(1) - 1, max_kv, caches.data(), static_cast<int32_t>(layers),
+                             static_cast<const int32_t*>(t.data_ptr()), t.stride(0), lens, cu, tokens, parents, sampled, out,
+                             accepted, new_lens, c.stream(a[11]));
 }
 
 // target_probs, draft_probs, draft_tokens, cu_drafts, uniforms, noise, out_tokens, accepted, workspace, stream
@@ -313,6 +378,7 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef kMethods[] = {method<qk_norm_rope, 11>("qk_norm_rope"), method<qkv_append, 14>("qkv_append"),
                           method<attention, 17>("attention"), method<verify_draft, 10>("verify_draft"),
+                          method<tree_attention, 19>("tree_attention"), method<tree_commit, 12>("tree_commit"),
                           method<lora, 9>("lora"), method<sample, 11>("sample"),
                           {nullptr, nullptr, 0, nullptr}};
 

@@ -1,7 +1,8 @@
 """The serving operators around the linears (C ABI section "Serving operators"
 of ``include/qlinear.h``): norm and rotation of the query and key heads, append
-to a paged cache, attention over it, verification of drafted tokens, low-rank
-adapters beside a projection, sampling.
+to a paged cache, attention over it (for trees of drafted tokens too),
+verification of drafted tokens and commit of a tree's branch, low-rank adapters
+beside a projection, sampling.
 
 Tensors keep torch's shapes and strides: heads are ``[tokens, heads,
 head_dim]`` views (the query columns of a QKV projection's output as they
@@ -116,10 +117,12 @@ def qlinear_qkv_append(q, k, v, positions, slots, cos_sin, q_out, cache, q_weigh
 class AttentionPlan:
     """Owner of a ql_attention_plan handle (host object)."""
 
+    _make = "qlinear_attention_plan"
+
     def __init__(self, shape):
         self.shape = shape
         h = ctypes.c_void_p()
-        _lib_check(_lib.load().qlinear_attention_plan(ctypes.byref(shape), ctypes.byref(h)), "qlinear_attention_plan")
+        _lib_check(getattr(_lib.load(), self._make)(ctypes.byref(shape), ctypes.byref(h)), self._make)
         self.handle = h
         self.workspace_bytes = int(_lib.load().qlinear_attention_workspace_bytes(h))
         # what a call is checked against, in the binding's order
@@ -163,6 +166,48 @@ def qlinear_attention(plan, q, cache, page_table, seq_lens, cu_q, out, lse=None,
                                            lse, workspace, _stream(stream))
     if st:
         _lib_check(st, "qlinear_attention")
+
+
+class TreeAttentionPlan(AttentionPlan):
+    """The same for trees of drafted tokens."""
+
+    _make = "qlinear_tree_attention_plan"
+
+    def __init__(self, shape):
+        super().__init__(shape)
+        self._words = -(-min(shape.max_q, shape.tokens) // 64)
+
+
+def qlinear_tree_attention_plan(cache, q_heads, batch, tokens, max_q, max_kv, scale=None):
+    """Plan for trees of drafted tokens: `tokens` nodes of `batch` sequences, at
+    most max_q of one, over contexts of at most max_kv tokens (the nodes included)."""
+    return TreeAttentionPlan(QLAttentionShape(batch, tokens, max_q, max_kv, q_heads, cache.kv_heads, cache.head_dim,
+                                              cache.page_size, cache.kv_type, True, 0, scale or 0.0))
+
+
+def qlinear_tree_attention(plan, q, cache, page_table, seq_lens, cu_q, sees, out, lse=None, workspace=None, stream=None):
+    """qlinear_attention for the nodes of trees: sees int64 [tokens, words], the
+    new tokens of its sequence that each node sees, one a bit (see qlinear.h)."""
+    if not isinstance(plan, TreeAttentionPlan):
+        raise ValueError("the plan is not for trees")
+    if not cache.on_gpu:
+        raise ValueError("the cache must be on the GPU")
+    st = (_module or _binding()).tree_attention(*plan._args, q, cache.address, cache.device_index, page_table, seq_lens, cu_q,
+                                                out, lse, workspace, _stream(stream), sees, plan._words)
+    if st:
+        _lib_check(st, "qlinear_tree_attention")
+
+
+def qlinear_tree_commit(caches, page_table, seq_lens, cu_q, node_tokens, parents, sampled, out_tokens, accepted,
+                        new_lens=None, max_kv=None, stream=None):
+    """Follow the drawn tokens down each sequence's tree, give them out and move
+    the accepted nodes' keys and values behind the context in every cache of the
+    list (see qlinear.h); out_tokens int32 [batch, max_depth + 1].  max_kv: bound
+    of the cached lengths, None: what the page table's columns hold."""
+    st = (_module or _binding()).tree_commit(caches, page_table, max_kv, seq_lens, cu_q, node_tokens, parents, sampled,
+                                             out_tokens, accepted, new_lens, _stream(stream))
+    if st:
+        _lib_check(st, "qlinear_tree_commit")
 
 
 def qlinear_verify_workspace_bytes(batch, vocab):
