@@ -36,18 +36,17 @@ __device__ __forceinline__ int lane_adapter(const LoraArgs& a, int block, uint64
   return i >= 0 && i < a.adapters ? i : -1;
 }
 
-// Calls f(adapter, mask of its tokens) for adapters number slot, slot + slots,
-// ... among the lanes of `left`.
+// Calls f(adapter, mask of its tokens, first of its tile) for the tiles number
+// slot, slot + slots, ... of the lanes of `left`: up to 16 tokens of one adapter.
 template <class F>
-__device__ __forceinline__ void for_adapters(int mine, uint64_t left, int slot, int slots, F f) {
-  for (int n = 0; left; ++n) {
+__device__ __forceinline__ void for_tiles(int mine, uint64_t left, int slot, int slots, F f) {
+  for (int n = 0; left;) {
     const int i = lane_i32(mine, __ffsll((unsigned long long)left) - 1);
     const uint64_t same = __ballot(mine == i) & left;
     left &= ~same;
-    if (n == slot) {
-      f(i, same);
-      slot += slots;
-    }
+    const int end = n + (__popcll(same) + 15) / 16;
+    for (; slot < end; slot += slots) f(i, same, (slot - n) * 16);
+    n = end;
   }
 }
 
@@ -59,87 +58,87 @@ __device__ __forceinline__ int nth_lane(uint64_t mask) {
   return __builtin_amdgcn_ds_permute(at * 4, lane);
 }
 
-// h of one adapter's tokens, one chunk of K, TW tiles of 16 ranks.
-template <int NT, int TW>
+// h of tiles of tokens, one chunk of K, TW tiles of 16 ranks: four waves a
+// quarter of the chunk each.
+template <int TW>
 __global__ void __launch_bounds__(kLoraWaves * 64) lora_down_kernel(LoraArgs a) {
+  __shared__ f32x4 sums[kLoraWaves][TW][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  const int rows = a.slices * a.rank;
-  const int groups = (rows + 16 * TW - 1) / (16 * TW);
-  int id = (int)blockIdx.x * kLoraWaves + wave;
+  const int rows = a.slices * a.rank, groups = (rows + 63) / 64;
+  int id = blockIdx.x;
   const int chunk = id % a.chunks;
   id /= a.chunks;
-  const int row0 = id % groups * 16 * TW;
+  const int row0 = id % groups * 64;
   id /= groups;
-  const int slot = id % a.down_slots, block = id / a.down_slots;
-  if (block * kLoraBlock >= a.tokens) return;
+  const int slot = id % a.slots, block = id / a.slots;
   uint64_t there;
   const int mine = lane_adapter(a, block, &there);
-  const int k0 = chunk * a.chunk, k1 = min(a.k, k0 + a.chunk);
-  for_adapters(mine, __ballot(mine >= 0), slot, a.down_slots, [&](int i, uint64_t mask) {
-    const int n = __popcll(mask), order = nth_lane(mask);
+  const int k0 = chunk * a.chunk + wave * (a.chunk / kLoraWaves), k1 = min(a.k, k0 + a.chunk / kLoraWaves);
+  for_tiles(mine, there, slot, a.slots, [&](int i, uint64_t mask, int c0) {
+    if (i < 0) return;
+    const int n = __popcll(mask), tok = block * kLoraBlock + __shfl(nth_lane(mask), min(c0 + r, n - 1), 64);
     const uint8_t* wp[TW];
 #pragma unroll
     for (int v = 0; v < TW; ++v)
       wp[v] = a.a + i * a.a_step + (int64_t)min(row0 + 16 * v + r, rows - 1) * a.k * 2 + g * 32;
-    for (int c0 = 0; c0 < n; c0 += 16 * NT) {
-      const uint8_t* xp[NT];
-      int tok[NT];
+    const uint8_t* xp = a.x + tok * a.x_row + g * 32;
+    f32x4 h[TW];
 #pragma unroll
-      for (int u = 0; u < NT; ++u) {
-        tok[u] = block * kLoraBlock + __shfl(order, min(c0 + 16 * u + r, n - 1), 64);
-        xp[u] = a.x + tok[u] * a.x_row + g * 32;
-      }
-      f32x4 h[NT][TW];
+    for (int v = 0; v < TW; ++v) h[v] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    // 64 values of K a step, 16 a lane: whole 128-byte lines of a row
+    auto step = [&](int k, bool tail) {
 #pragma unroll
-      for (int u = 0; u < NT; ++u)
+      for (int half = 0; half < 2; ++half) {
+        const bool in = !tail || k + 16 * g + 8 * half < k1;
+        const u32x4 zero = {0u, 0u, 0u, 0u};
+        const u32x4 x = in ? *reinterpret_cast<const u32x4*>(xp + (int64_t)k * 2 + half * 16) : zero;
 #pragma unroll
-        for (int v = 0; v < TW; ++v) h[u][v] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-      // 64 values of K a step, 16 a lane: whole 128-byte lines of a row
-      auto step = [&](int k, bool tail) {
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          const bool in = !tail || k + 16 * g + 8 * half < k1;
-          const u32x4 zero = {0u, 0u, 0u, 0u};
-          u32x4 w[TW];
-#pragma unroll
-          for (int v = 0; v < TW; ++v)
-            w[v] = in ? *reinterpret_cast<const u32x4*>(wp[v] + (int64_t)k * 2 + half * 16) : zero;
-#pragma unroll
-          for (int u = 0; u < NT; ++u) {
-            const u32x4 x = in ? *reinterpret_cast<const u32x4*>(xp[u] + (int64_t)k * 2 + half * 16) : zero;
-#pragma unroll
-            for (int v = 0; v < TW; ++v) h[u][v] = mma_bf16(w[v], x, h[u][v]);
-          }
+        for (int v = 0; v < TW; ++v) {
+          const u32x4 w = in ? *reinterpret_cast<const u32x4*>(wp[v] + (int64_t)k * 2 + half * 16) : zero;
+          h[v] = mma_bf16(w, x, h[v]);
         }
-      };
-      int k = k0;
+      }
+    };
+    int k = k0;
 #pragma unroll 4
-      for (; k + 64 <= k1; k += 64) step(k, false);
-      if (k < k1) step(k, true);
+    for (; k + 64 <= k1; k += 64) step(k, false);
+    if (k < k1) step(k, true);
 #pragma unroll
-      for (int u = 0; u < NT; ++u)
+    for (int v = 0; v < TW; ++v) sums[wave][v][lane] = h[v];
+    __syncthreads();
+    // one wave's place of the product for each tile of ranks
+    if (wave < TW) {
+      f32x4 x = sums[0][wave][lane];
 #pragma unroll
-        for (int v = 0; v < TW; ++v)
-          if (c0 + 16 * u + r < n && row0 + 16 * v + 4 * g < rows)
-            *reinterpret_cast<f32x4*>(a.part + ((int64_t)chunk * a.tokens + tok[u]) * rows + row0 + 16 * v + 4 * g) = h[u][v];
+      for (int w = 1; w < kLoraWaves; ++w) x += sums[w][wave][lane];
+      if (c0 + r < n && row0 + 16 * wave + 4 * g < rows)
+        *reinterpret_cast<f32x4*>(a.part + ((int64_t)chunk * a.tokens + tok) * rows + row0 + 16 * wave + 4 * g) = x;
     }
+    __syncthreads();
   });
 }
 
-// out = y + s B h for one adapter's tokens and a range of column tiles of one
-// slice.  STEPS: products over the ranks, 2 R / 32 rounded up.
-template <int NT, int STEPS>
+// The column of a 64-wide tile that row m of product j stands for: a lane ends
+// with 8 columns of its token from 8 g on and 8 from 32 + 8 g on, so a load or
+// store of 16 bytes a lane covers 64 in a row.
+__device__ __forceinline__ int tile_column(int j, int m) { return j / 2 * 32 + m / 4 * 8 + j % 2 * 4 + m % 4; }
+
+// out = y + s B h for tiles of tokens and a range of column tiles of one slice.
+// BS products of 32 ranks for h rounded and as many for what that left out; ranks
+// of up to 16 have both in one (PACKED).
+template <int BS, bool PACKED>
 __global__ void __launch_bounds__(kLoraWaves * 64) lora_up_kernel(LoraArgs a) {
+  constexpr int HS = PACKED ? 1 : 2 * BS;
+  __shared__ u32x4 h_lds[HS][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
-  int id = (int)blockIdx.x * kLoraWaves + wave;
+  int id = blockIdx.x;
   int range = id % a.ranges, slice = 0, first = 0;
   id /= a.ranges;
-  const int slot = id % a.up_slots, block = id / a.up_slots;
-  if (block * kLoraBlock >= a.tokens) return;
+  const int slot = id % a.slots, block = id / a.slots;
   // the slice, and its first column
-  const int wide = a.tiles_wave * 64;
+  const int wide = a.tiles_wg * 64;
   for (;; ++slice) {
     const int here = (a.width[slice] + wide - 1) / wide;
     if (range < here) break;
@@ -147,113 +146,141 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_up_kernel(LoraArgs a) {
     first += a.width[slice];
   }
   const int width = a.width[slice], rows = a.slices * a.rank, octets = a.rank / 8;
-  const int n0 = range * wide, n1 = min(width, n0 + wide);
+  const int n0 = range * wide + wave * 64, n1 = min(width, range * wide + wide);
   uint64_t there;
   const int mine = lane_adapter(a, block, &there);
-  for_adapters(mine, there, slot, a.up_slots, [&](int i, uint64_t mask) {
+  for_tiles(mine, there, slot, a.slots, [&](int i, uint64_t mask, int c0) {
     if (i < 0 && a.out == a.y) return;
     const int n = __popcll(mask), order = nth_lane(mask);
-    const float scale = i >= 0 && a.scales ? a.scales[i] : 1.0f;
+    const int tok = block * kLoraBlock + __shfl(order, min(c0 + r, n - 1), 64);
+    const bool live = c0 + r < n;
     const uint8_t* b = a.b + (i >= 0 ? i * a.b_step : 0) + (int64_t)first * a.rank * 2;
-    for (int c0 = 0; c0 < n; c0 += 16 * NT) {
-      int tok[NT];
-      u32x4 h[NT][STEPS];
+    const uint8_t* y = a.y + tok * a.y_row + (int64_t)first * 2;
+    uint8_t* out = a.out + tok * a.out_row + (int64_t)first * 2;
+    u32x4 w[4][BS], v[2];
+    auto load = [&](int t) {
 #pragma unroll
-      for (int u = 0; u < NT; ++u) {
-        tok[u] = block * kLoraBlock + __shfl(order, min(c0 + 16 * u + r, n - 1), 64);
+      for (int half = 0; half < 2; ++half)
+        if (live && t + 32 * half + 8 * g < n1) v[half] = *reinterpret_cast<const u32x4*>(y + (t + 32 * half + 8 * g) * 2);
+      if (i >= 0) {
 #pragma unroll
-        for (int s = 0; s < STEPS; ++s) {
-          // places 0 .. octets - 1: h rounded, then what that left out
-          const int place = 4 * s + g, octet = place < octets ? place : place - octets;
-          h[u][s] = u32x4{0u, 0u, 0u, 0u};
-          if (i >= 0 && octet < octets) {
-            f32x4 x[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
-            const float* p = a.part + (int64_t)tok[u] * rows + slice * a.rank + octet * 8;
-            for (int c = 0; c < a.chunks; ++c, p += (int64_t)a.tokens * rows) {
-              x[0] += *reinterpret_cast<const f32x4*>(p);
-              x[1] += *reinterpret_cast<const f32x4*>(p + 4);
+        for (int j = 0; j < 4; ++j) {
+          const uint8_t* p = b + (int64_t)min(t + tile_column(j, r), width - 1) * a.rank * 2;
+#pragma unroll
+          for (int s = 0; s < BS; ++s) {
+            const int octet = PACKED ? (g < octets ? g : g - octets) : 4 * s + g;
+            w[j][s] = octet < octets ? *reinterpret_cast<const u32x4*>(p + octet * 16) : u32x4{0u, 0u, 0u, 0u};
+          }
+        }
+      }
+    };
+    if (n0 < n1) load(n0);
+    if (i >= 0) {
+      // h of the tile's tokens, in the order of the products' operands
+      const float scale = a.scales ? a.scales[i] : 1.0f;
+      for (int s = wave; s < (PACKED ? 1 : BS); s += kLoraWaves) {
+        const int place = 4 * s + g, octet = PACKED && place >= octets ? place - octets : place;
+        u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
+        if (octet < octets) {
+          f32x4 x[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+          const float* p = a.part + (int64_t)tok * rows + slice * a.rank + octet * 8;
+          const int64_t step = (int64_t)a.tokens * rows;
+          int c = 0;
+          for (; c + 4 <= a.chunks; c += 4, p += 4 * step) {
+            f32x4 e[4], f[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              e[k] = *reinterpret_cast<const f32x4*>(p + k * step);
+              f[k] = *reinterpret_cast<const f32x4*>(p + k * step + 4);
             }
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-              const float e = x[k / 2][k % 2 * 2] * scale, f = x[k / 2][k % 2 * 2 + 1] * scale;
-              const uint32_t w = bf16_pair(e, f);
-              h[u][s][k] = place < octets ? w : bf16_pair(e - __uint_as_float(w << 16), f - __uint_as_float(w & 0xffff0000u));
+              x[0] += e[k];
+              x[1] += f[k];
             }
           }
+          for (; c < a.chunks; ++c, p += step) {
+            x[0] += *reinterpret_cast<const f32x4*>(p);
+            x[1] += *reinterpret_cast<const f32x4*>(p + 4);
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float e = x[k / 2][k % 2 * 2] * scale, f = x[k / 2][k % 2 * 2 + 1] * scale;
+            hi[k] = bf16_pair(e, f);
+            lo[k] = bf16_pair(e - __uint_as_float(hi[k] << 16), f - __uint_as_float(hi[k] & 0xffff0000u));
+          }
+        }
+        if (PACKED) {
+          h_lds[0][lane] = place < octets ? hi : lo;
+        } else {
+          h_lds[s][lane] = hi;
+          h_lds[BS + s][lane] = lo;
         }
       }
-      for (int t = n0; t < n1; t += 64) {
-        // product j's row m is column (m / 4) 16 + 4 j + m % 4 of the tile: a lane ends with 16 columns of its token
-        f32x4 o[NT][4];
+      lds_barrier();
+    }
+    u32x4 h[HS];
+    if (i >= 0) {
 #pragma unroll
-        for (int u = 0; u < NT; ++u)
+      for (int s = 0; s < HS; ++s) h[s] = h_lds[s][lane];
+    }
+    for (int t = n0; t < n1; t += 64 * kLoraWaves) {
+      f32x4 o[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[u][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int j = 0; j < 4; ++j) o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if (i >= 0) {
+#pragma unroll
+        for (int s = 0; s < HS; ++s)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[j] = mma_bf16(w[j][s % BS], h[s], o[j]);
+      }
+      const u32x4 now[2] = {v[0], v[1]};
+      if (t + 64 * kLoraWaves < n1) load(t + 64 * kLoraWaves);
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if (!live || t + 32 * half + 8 * g >= n1) continue;
+        u32x4 x = now[half];
         if (i >= 0) {
 #pragma unroll
-          for (int s = 0; s < STEPS; ++s) {
-            const int place = 4 * s + g, octet = place < octets ? place : place - octets;
-            if (4 * s >= 2 * octets) break;
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const int col = min(t + r / 4 * 16 + 4 * j + r % 4, width - 1);
-              const u32x4 w = octet < octets ? *reinterpret_cast<const u32x4*>(b + (int64_t)col * a.rank * 2 + octet * 16)
-                                             : u32x4{0u, 0u, 0u, 0u};
-#pragma unroll
-              for (int u = 0; u < NT; ++u) o[u][j] = mma_bf16(w, h[u][s], o[u][j]);
-            }
+          for (int k = 0; k < 4; ++k) {
+            const f32x4& d = o[2 * half + k / 2];
+            x[k] = bf16_pair(__uint_as_float(x[k] << 16) + d[k % 2 * 2],
+                             __uint_as_float(x[k] & 0xffff0000u) + d[k % 2 * 2 + 1]);
           }
         }
-#pragma unroll
-        for (int u = 0; u < NT; ++u) {
-          if (c0 + 16 * u + r >= n) continue;
-          const int64_t at = (int64_t)(first + t + 16 * g) * 2;
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            if (t + 16 * g + 8 * half >= n1) continue;
-            u32x4 v = *reinterpret_cast<const u32x4*>(a.y + tok[u] * a.y_row + at + half * 16);
-            if (i >= 0) {
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const f32x4& d = o[u][2 * half + k / 2];
-                v[k] = bf16_pair(__uint_as_float(v[k] << 16) + d[k % 2 * 2], __uint_as_float(v[k] & 0xffff0000u) + d[k % 2 * 2 + 1]);
-              }
-            }
-            *reinterpret_cast<u32x4*>(a.out + tok[u] * a.out_row + at + half * 16) = v;
-          }
-        }
+        *reinterpret_cast<u32x4*>(out + (t + 32 * half + 8 * g) * 2) = x;
       }
     }
+    lds_barrier();
   });
 }
 
-template <int NT>
-static hipError_t launch_up(const LoraArgs& a, int blocks, hipStream_t s) {
-  const unsigned grid = (unsigned)((blocks * a.up_slots * a.ranges + kLoraWaves - 1) / kLoraWaves);
-  const dim3 threads(kLoraWaves * 64);
-  if (a.rank <= 16)
-    hipLaunchKernelGGL((lora_up_kernel<NT, 1>), dim3(grid), threads, 0, s, a);
-  else if (a.rank <= 32)
-    hipLaunchKernelGGL((lora_up_kernel<NT, 2>), dim3(grid), threads, 0, s, a);
-  else if (a.rank <= 64)
-    hipLaunchKernelGGL((lora_up_kernel<NT, 4>), dim3(grid), threads, 0, s, a);
-  else
-    hipLaunchKernelGGL((lora_up_kernel<(NT > 2 ? 2 : NT), 8>), dim3(grid), threads, 0, s, a);
-  return hipGetLastError();
-}
-
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
-  const int blocks = (a.tokens + kLoraBlock - 1) / kLoraBlock, rows = a.slices * a.rank;
-  const bool wide = a.tokens > kLoraBlock;
-  const int groups = wide ? (rows + 63) / 64 : (rows + 15) / 16;
-  const unsigned grid = (unsigned)((blocks * a.down_slots * groups * a.chunks + kLoraWaves - 1) / kLoraWaves);
-  if (wide)
-    hipLaunchKernelGGL((lora_down_kernel<4, 4>), dim3(grid), dim3(kLoraWaves * 64), 0, s, a);
+  const int blocks = (a.tokens + kLoraBlock - 1) / kLoraBlock, rows = a.slices * a.rank, groups = (rows + 63) / 64;
+  const dim3 down((unsigned)(blocks * a.slots * groups * a.chunks)), up((unsigned)(blocks * a.slots * a.ranges));
+  const dim3 threads(kLoraWaves * 64);
+  const int tiles = rows >= 64 ? 4 : (rows + 15) / 16;
+  if (tiles == 1)
+    hipLaunchKernelGGL((lora_down_kernel<1>), down, threads, 0, s, a);
+  else if (tiles == 2)
+    hipLaunchKernelGGL((lora_down_kernel<2>), down, threads, 0, s, a);
+  else if (tiles == 3)
+    hipLaunchKernelGGL((lora_down_kernel<3>), down, threads, 0, s, a);
   else
-    hipLaunchKernelGGL((lora_down_kernel<1, 1>), dim3(grid), dim3(kLoraWaves * 64), 0, s, a);
+    hipLaunchKernelGGL((lora_down_kernel<4>), down, threads, 0, s, a);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  return wide ? launch_up<4>(a, blocks, s) : launch_up<1>(a, blocks, s);
+  if (a.rank <= 16)
+    hipLaunchKernelGGL((lora_up_kernel<1, true>), up, threads, 0, s, a);
+  else if (a.rank <= 32)
+    hipLaunchKernelGGL((lora_up_kernel<1, false>), up, threads, 0, s, a);
+  else if (a.rank <= 64)
+    hipLaunchKernelGGL((lora_up_kernel<2, false>), up, threads, 0, s, a);
+  else if (a.rank <= 96)
+    hipLaunchKernelGGL((lora_up_kernel<3, false>), up, threads, 0, s, a);
+  else
+    hipLaunchKernelGGL((lora_up_kernel<4, false>), up, threads, 0, s, a);
+  return hipGetLastError();
 }
 
 }  // namespace qlk

@@ -52,25 +52,21 @@ ql_status lora_shape(const ql_lora* l, int64_t tokens, qlk::LoraArgs* a) {
   a->a_step = l->a_adapter_stride * 2;
   a->b_step = l->b_adapter_stride * 2;
   const int64_t blocks = (tokens + qlk::kLoraBlock - 1) / qlk::kLoraBlock;
-  const bool few = blocks <= 1;
-  // waves for the adapters that a block can hold: as many in a decode batch, in
-  // prompt chunks a block is one request's as a rule
-  const int64_t slots = few ? std::max<int64_t>(1, std::min<int64_t>(tokens, l->adapters)) : 1;
-  a->down_slots = (int)slots;
-  a->up_slots = few ? (int)std::min<int64_t>(tokens, l->adapters + 1) : 1;
-  const int64_t groups = few ? (rows + 15) / 16 : (rows + 63) / 64;
-  const int64_t units = std::max<int64_t>(1, blocks * slots * groups);
-  int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((l->in_features + 255) / 256, (2048 + units - 1) / units));
-  const int64_t chunk = ((l->in_features + chunks - 1) / chunks + 63) / 64 * 64;
+  // a decode batch can hold as many tiles as adapters (and tokens without one),
+  // and one more for every 16 tokens; a prompt's block of 64 tokens has four
+  const int64_t slots = blocks > 1 ? 4 : std::max<int64_t>(1, std::min<int64_t>(tokens, l->adapters + 1 + tokens / 16));
+  a->slots = (int)slots;
+  const int64_t groups = (rows + 63) / 64, units = std::max<int64_t>(1, blocks * slots);
+  int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((l->in_features + 511) / 512, 512 / (units * groups)));
+  const int64_t chunk = ((l->in_features + chunks - 1) / chunks + 255) / 256 * 256;
   chunks = (l->in_features + chunk - 1) / chunk;
   a->chunk = (int)chunk;
   a->chunks = (int)chunks;
-  const int64_t all = std::max<int64_t>(1, blocks * a->up_slots) * tiles;
-  a->tiles_wave = (int)std::max<int64_t>(1, std::min<int64_t>(16, all / 2048));
+  a->tiles_wg = (int)std::max<int64_t>(4, std::min<int64_t>(32, units * tiles / 1024 / 4 * 4));
   int64_t ranges = 0;
-  for (int i = 0; i < l->slices; ++i) ranges += ((l->widths[i] + 63) / 64 + a->tiles_wave - 1) / a->tiles_wave;
+  for (int i = 0; i < l->slices; ++i) ranges += ((l->widths[i] + 63) / 64 + a->tiles_wg - 1) / a->tiles_wg;
   a->ranges = (int)ranges;
-  if (blocks * a->down_slots * groups * chunks >= kMaxWorkgroups || blocks * a->up_slots * ranges >= kMaxWorkgroups)
+  if (units * groups * chunks >= kMaxWorkgroups || units * ranges >= kMaxWorkgroups)
     return fail(QL_E_UNSUPPORTED, "2^24 workgroups or more");
   return QL_OK;
 }

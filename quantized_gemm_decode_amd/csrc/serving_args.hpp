@@ -23,10 +23,9 @@ struct LoraArgs {
   int64_t x_row, y_row, out_row, a_step, b_step;
   int tokens, adapters, rank, k, slices;
   int width[kLoraSlices];
-  int chunk, chunks;       // K of a partial sum (a multiple of 64), their number
-  int down_slots;          // waves that share a block's adapters, first product
-  int up_slots;            // the same, second product
-  int tiles_wave;          // 64-wide column tiles of a wave of the second product
+  int chunk, chunks;       // K of a partial sum (a multiple of 256: 64 a step of each wave), their number
+  int slots;               // workgroups that share a block's tiles of tokens
+  int tiles_wg;            // 64-wide column tiles of a workgroup of the second product
   int ranges;              // of all slices together
 };
 
