@@ -801,13 +801,14 @@ ql_status qlinear_lora(const ql_lora* lora, int64_t tokens, const void* x, int64
  *           others (what qlinear_verify_draft takes)
  * The rules are device arrays of one value a row, each NULL where no row has it
  * (rules NULL: none): temperature binary32 (0 or below, NaN: greedy, the first
- * entry of the order), top_k int32 (0 or below: off), top_p binary32 (1 or above,
+ * entry of the order; below 1e-6: 1e-6), top_k int32 (0 or below: off), top_p binary32 (1 or above,
  * NaN: off), min_p binary32 (0 or below, NaN: off).  A logit of -inf or NaN is no
  * entry; without any the token is -1, its logarithm -inf and the probabilities 0.
  * Logits of +inf share the probability.
  *
  * What is kept does not depend on rounding in binary32: weights are computed in
- * binary64 and summed as integers in steps of 2^-36 of the largest.  Results do
+ * binary64 and summed as integers, to about 10^-11 of a weight (entries of less
+ * than 2^-90 of the largest weigh nothing in the sums).  Results do
  * not depend on timing.  The workspace (qlinear_sample_workspace_bytes, 16-byte
  * aligned; about 8 bytes an entry) needs no initialisation; concurrent calls need
  * distinct ones.  Up to 65535 rows and 2^24 entries a row.  Enqueue-only.

@@ -48,6 +48,7 @@ def sample(logits, noise, temperature=None, top_k=None, top_p=None, min_p=None):
     if not t > 0:
         order, t = order[:1], 1.0
         top_k = top_p = min_p = None
+    t = max(t, float(np.float32(1e-6)))
     top = l[order[0]]
     with np.errstate(invalid="ignore", over="ignore", under="ignore"):
         w = np.exp((l[order] - top) / t) if np.isfinite(top) else (l[order] == top).astype(np.float64)

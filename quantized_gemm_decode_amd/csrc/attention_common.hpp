@@ -68,6 +68,18 @@ __device__ __forceinline__ float row4_sum(float v) {
   return v + __shfl_xor(v, 32, 64);
 }
 
+// Sum over lanes 0 .. l, by lane shifts inside 16 lanes, then the rows' last
+// lanes to the rows behind them.
+__device__ __forceinline__ int inclusive_sum(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr 1
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);   // row_shr 2
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);   // row_shr 4
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);   // row_shr 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15 into rows 1 and 3
+  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast 31 into rows 2 and 3
+  return v;
+}
+
 // A row's lse from its maximum (base 2, -inf: no score above -inf) and sum.  Where
 // all scores are NaN the maximum has not moved either, but the sum is NaN.
 __device__ __forceinline__ float lse_of(float m, float sum) {

@@ -125,18 +125,6 @@ __device__ __forceinline__ Seq seq_of(const AttnArgs& a, int b) {
   return s;
 }
 
-// Sum over lanes 0 .. l, by lane shifts inside 16 lanes, then the rows' last
-// lanes to the rows behind them.
-__device__ __forceinline__ int inclusive_sum(int v) {
-  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, true);   // row_shr 1
-  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, true);   // row_shr 2
-  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, true);   // row_shr 4
-  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, true);   // row_shr 8
-  v += __builtin_amdgcn_update_dpp(0, v, 0x142, 0xa, 0xf, false);  // row_bcast 15 into rows 1 and 3
-  v += __builtin_amdgcn_update_dpp(0, v, 0x143, 0xc, 0xf, false);  // row_bcast 31 into rows 2 and 3
-  return v;
-}
-
 // All sequences' tiles, and how they are cut: `slots` slots of `each` tiles,
 // the first `more` of them one longer.  A sequence takes room for a multiple of
 // 2^pad tiles.

@@ -9,35 +9,41 @@
 // Nothing is sorted.  What is kept is a head of the order, so only its border
 // has to be found: logits are put into buckets of an eighth of T on one grid
 // for the whole row, and a bucket's number and mass of entries say which one
-// the border lies in.  Four launches:
+// the border lies in.  Two launches, a third for probabilities:
 //   scan     a slice's entries in registers: its largest, and its histogram in
 //            LDS relative to that one (one atomic an entry: number and mass in
 //            one word);
 //   collect  adds a row's histograms, finds the border's bucket, draws among
-//            the entries before it and lists those in it (the candidates);
-//   finish   one workgroup a row: the border among the candidates, the token;
+//            the entries before it and lists those in it (the candidates); the
+//            row's last workgroup finds the border among them and the token;
 //   write    probabilities, where they are asked for.
 //
-// Mass is a sum of integers, w in steps of 2^-36 of a slice's largest: sums do
-// not depend on the order of the atomics.  w itself is computed in binary64
-// (10^-11): whether an entry is kept depends on a sum over the whole row, and
-// binary32 exponentials would let one of some thousand rows keep one entry
-// more or less.  The vector unit does binary64 products at binary32's pace.
+// Whether an entry is kept depends on a sum over the whole row, and binary32
+// exponentials would let one of some thousand rows keep one entry more or
+// less.  So masses are computed in binary64, whose products the vector unit
+// does at binary32's pace, and summed as integers, which do not depend on the
+// order of the atomics: in a bucket l grid = q + f, w is exp((f - 1/2) / 8), a
+// short series, times a factor of the bucket.
 #include "attention_common.hpp"
 #include "serving_args.hpp"
 
 namespace qlk {
 
-constexpr int kSampleThreads = 256;
-constexpr int kMassBits = 50;
+constexpr int kSampleThreads = 512;
+constexpr int kSampleWaves = kSampleThreads / 64;
+constexpr int kSampleCopies = 4;         // of a histogram: lanes of equal buckets add one after the other
+constexpr int kMassBits = 49;            // 16384 entries of up to e^(1/16) 2^34
 constexpr uint64_t kMassMask = (uint64_t(1) << kMassBits) - 1;
-constexpr int kMassScale = 36;   // w in steps of 2^-36
+constexpr double kMassOne = 17179869184.0;   // 2^34
+constexpr double kLog2E = 1.44269504088896340736;
 
-// 2^y for y <= 0 as m 2^e with m in [0.7, 1.42): the exponential's own series.
+// 2^y as m 2^e with m in [0.7, 1.42): the exponential's own series (6 10^-15).
 __device__ __forceinline__ double exp2_parts(double y, int* e) {
-  y = fmax(y, -1000.0);
+  y = fmin(fmax(y, -1000.0), 1000.0);
   const double n = rint(y), f = (y - n) * 0.69314718055994530942;
-  double p = 1.0 / 362880.0;
+  double p = 1.0 / 39916800.0;
+  p = fma(p, f, 1.0 / 3628800.0);
+  p = fma(p, f, 1.0 / 362880.0);
   p = fma(p, f, 1.0 / 40320.0);
   p = fma(p, f, 1.0 / 5040.0);
   p = fma(p, f, 1.0 / 720.0);
@@ -51,50 +57,52 @@ __device__ __forceinline__ double exp2_parts(double y, int* e) {
   return p;
 }
 
-// An entry's weight relative to `top`: 1 for top itself (also where that is
-// infinite), 0 for what is infinitely far from it.
-__device__ __forceinline__ double weight_of(float l, float top, double rate) {
+__device__ __forceinline__ double exp2_of(double y) {
   int e;
-  const double m = exp2_parts(((double)l - (double)top) * rate, &e);
-  return l == top ? 1.0 : ldexp(m, e);
-}
-
-// The same in steps of 2^-36, rounded to nearest (the low bits of 2^52 + w).
-__device__ __forceinline__ uint64_t mass_of(float l, float top, double rate) {
-  const double w = ldexp(weight_of(l, top, rate), kMassScale) + 4503599627370496.0;
-  return (uint64_t)__double_as_longlong(w) & ((uint64_t(1) << 52) - 1);
+  const double m = exp2_parts(y, &e);
+  return ldexp(m, e);
 }
 
 // One row's rules.
 struct Rules {
   double rate;       // log2(e) / T
-  float grid;        // buckets per unit of the logits
-  float span;        // buckets an e-fold of w takes
+  double grid;       // buckets per unit of the logits: 8 / T
   int k;             // 0: off
   float p, m;        // 1, 0: off
-  bool greedy;
 };
 
 __device__ __forceinline__ Rules rules_of(const SampleArgs& a, int row) {
   Rules r;
   const float t = a.temperature ? a.temperature[row] : 1.0f;
-  r.greedy = !(t > 0.0f);
-  const double inv = r.greedy ? 1.0 : 1.0 / (double)t;
-  r.rate = inv * 1.44269504088896340736;
-  // an eighth of T; wider where logits of up to 10^4 would leave 2^23 buckets
-  r.grid = (float)fmin(8.0 * inv, 800.0);
-  r.span = r.greedy ? r.grid : r.grid * t;
-  r.k = r.greedy ? 1 : a.top_k ? a.top_k[row] : 0;
-  r.p = r.greedy || !a.top_p ? 1.0f : a.top_p[row];
-  r.m = r.greedy || !a.min_p ? 0.0f : a.min_p[row];
-  r.k = max(r.k, 0);
-  r.p = r.p < 1.0f ? r.p : 1.0f;               // NaN: off
+  const bool greedy = !(t > 0.0f);
+  const double inv = greedy ? 1.0 : 1.0 / (double)fmaxf(t, 1e-6f);
+  r.rate = inv * kLog2E;
+  r.grid = 8.0 * inv;
+  r.k = greedy ? 1 : a.top_k ? max(a.top_k[row], 0) : 0;
+  r.p = greedy || !a.top_p ? 1.0f : a.top_p[row];
+  r.m = greedy || !a.min_p ? 0.0f : a.min_p[row];
+  r.p = r.p < 1.0f ? fmaxf(r.p, 0.0f) : 1.0f;  // NaN: off
   r.m = r.m > 0.0f ? fminf(r.m, 1.0f) : 0.0f;
   return r;
 }
 
-__device__ __forceinline__ int bucket_of(float l, float grid) {
-  return (int)fminf(fmaxf(floorf(__fmul_rn(l, grid)), -8388608.0f), 8388608.0f);
+// The grid's line below a logit.  (Beyond 2^53 lines neighbouring binary32
+// logits are more than 2^29 of them apart: a bucket then holds equal ones.)
+__device__ __forceinline__ double line_of(float l, double grid) { return floor((double)l * grid); }
+
+// An entry's mass in its bucket, in steps of 2^-34: exp((f - 1/2) / 8) for the
+// part f of l grid above the line, by the polynomial that meets it at the six
+// Chebyshev nodes of [0, 1] (off by 3 10^-12 at most).  The low bits of 2^52 + x
+// are x rounded.
+__device__ __forceinline__ uint64_t mass_word(float l, double grid) {
+  const double f = __builtin_amdgcn_fract((double)l * grid);
+  double p = kMassOne * 2.54348632162432e-07;
+  p = fma(p, f, kMassOne * 9.53864143867337e-06);
+  p = fma(p, f, kMassOne * 0.0003058076755491678);
+  p = fma(p, f, kMassOne * 0.007339162402444752);
+  p = fma(p, f, kMassOne * 0.11742663303627268);
+  p = fma(p, f, kMassOne * 0.9394130628109114 + 4503599627370496.0);
+  return (uint64_t)__double_as_longlong(p) - (uint64_t(0x433) << 52);
 }
 
 // Values that order as binary32 logits do, and their inverse.
@@ -102,20 +110,21 @@ __device__ __forceinline__ uint32_t order_of(float l) {
   const uint32_t u = __float_as_uint(l);
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
-__device__ __forceinline__ float logit_of(uint32_t o) {
+__device__ __forceinline__ float logit_of(uint64_t key) {
+  const uint32_t o = (uint32_t)(key >> 32);
   return __uint_as_float(o & 0x80000000u ? o & 0x7fffffffu : ~o);
 }
 // The place of an entry in the order: larger is earlier.
 __device__ __forceinline__ uint64_t key_of(float l, int v) { return (uint64_t)order_of(l) << 32 | (0xffffffffu - (uint32_t)v); }
+__device__ __forceinline__ int index_of(uint64_t key) { return (int)(0xffffffffu - (uint32_t)key); }
 
 typedef unsigned u32x4b __attribute__((ext_vector_type(4), aligned(2)));
 
-// N entries from v on (as many as there are; the others -inf).  NaN is no entry,
+// 8 entries from v on (as many as there are; the others -inf).  NaN is no entry,
 // and zeros are alike.
-template <bool BF16, int N>
-__device__ __forceinline__ void load_logits(const SampleArgs& a, int row, int v, float (&x)[N]) {
-  static_assert(N == 8, "two or one 16-byte loads");
-  if (v + N <= a.vocab) {
+template <bool BF16>
+__device__ __forceinline__ void load_logits(const SampleArgs& a, int row, int v, float (&x)[8]) {
+  if (v + 8 <= a.vocab) {
     if constexpr (BF16) {
       const u32x4 t = *reinterpret_cast<const u32x4b*>(static_cast<const uint16_t*>(a.logits) + row * a.row + v);
 #pragma unroll
@@ -134,7 +143,7 @@ __device__ __forceinline__ void load_logits(const SampleArgs& a, int row, int v,
     }
   } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
+    for (int i = 0; i < 8; ++i) {
       x[i] = kNegInf;
       if (v + i < a.vocab)
         x[i] = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[row * a.row + v + i])
@@ -142,8 +151,11 @@ __device__ __forceinline__ void load_logits(const SampleArgs& a, int row, int v,
     }
   }
 #pragma unroll
-  for (int i = 0; i < N; ++i) x[i] = x[i] == x[i] ? x[i] + 0.0f : kNegInf;
+  for (int i = 0; i < 8; ++i) x[i] = x[i] == x[i] ? x[i] + 0.0f : kNegInf;
 }
+
+// Where a row has +inf, that is its only value: as 0 here.
+__device__ __forceinline__ float beside_inf(float l) { return l == -kNegInf ? 0.0f : kNegInf; }
 
 __device__ __forceinline__ float wave_max(float v) {
 #pragma unroll
@@ -164,6 +176,16 @@ __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
   return v;
 }
 
+// A value that is the same in all lanes, as such (a scalar register).
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
+__device__ __forceinline__ float uniform(float v) { return __uint_as_float(uniform((int)__float_as_uint(v))); }
+__device__ __forceinline__ double uniform(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)(uint32_t)uniform((int)(u >> 32)) << 32 | (uint32_t)uniform((int)u)));
+}
+
+__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+
 // A score and its index as one word: the larger score, between equals the
 // lower index.
 __device__ __forceinline__ uint64_t score_of(double w, float noise, int v) {
@@ -174,49 +196,128 @@ __device__ __forceinline__ uint64_t score_of(double w, float noise, int v) {
 // Slice blockIdx.x of row blockIdx.y; PIECES pieces of 8 entries a thread.
 template <bool BF16, int PIECES>
 __global__ void __launch_bounds__(kSampleThreads) sample_scan_kernel(SampleArgs a) {
-  const int row = blockIdx.y, slice = blockIdx.x, first = slice * PIECES * 8 * kSampleThreads;
-  __shared__ unsigned long long hist[kSampleBuckets];
-  __shared__ float tops[kSampleThreads / 64];
-  __shared__ unsigned long long all;
+  const int row = blockIdx.y, slice = blockIdx.x, first = slice * PIECES * 8 * kSampleThreads, t = threadIdx.x;
+  __shared__ unsigned long long hist[kSampleBuckets * kSampleCopies];
+  __shared__ float tops[kSampleWaves];
   float x[PIECES][8], top = kNegInf;
 #pragma unroll
-  for (int i = 0; i < PIECES; ++i) load_logits<BF16>(a, row, first + (i * kSampleThreads + (int)threadIdx.x) * 8, x[i]);
+  for (int i = 0; i < PIECES; ++i) load_logits<BF16>(a, row, first + (i * kSampleThreads + t) * 8, x[i]);
   const Rules r = rules_of(a, row);
-  hist[threadIdx.x] = 0;
-  if (threadIdx.x == 0) all = 0;
+#pragma unroll
+  for (int i = 0; i < kSampleCopies; ++i) hist[i * kSampleThreads + t] = 0;
 #pragma unroll
   for (int i = 0; i < PIECES; ++i)
 #pragma unroll
     for (int j = 0; j < 8; ++j) top = fmaxf(top, x[i][j]);
   top = wave_max(top);
-  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = top;
+  if ((t & 63) == 0) tops[t >> 6] = top;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kSampleThreads / 64; ++i) top = fmaxf(top, tops[i]);
-  const int most = bucket_of(top, r.grid);
+  for (int i = 0; i < kSampleWaves; ++i) top = fmaxf(top, tops[i]);
+  if (t == 0) {
+    a.top[(int64_t)row * a.slices + slice] = top;
+    if (slice == 0) {
+      a.count[2 * row] = a.count[2 * row + 1] = 0;
+      a.best[row] = 0;
+    }
+  }
+  if (top == -kNegInf) {
+    top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] = beside_inf(x[i][j]);
+  }
+  const double line = line_of(top, r.grid);
 #pragma unroll
   for (int i = 0; i < PIECES; ++i)
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (x[i][j] > kNegInf)
-        atomicAdd(&hist[min(most - bucket_of(x[i][j], r.grid), kSampleBuckets - 1)],
-                  (unsigned long long)(uint64_t(1) << kMassBits | mass_of(x[i][j], top, r.rate)));
+    for (int j = 0; j < 8; ++j) {
+      if (!(x[i][j] > kNegInf)) continue;
+      const int bucket = (int)fmin(line - line_of(x[i][j], r.grid), kSampleBuckets - 1.0);
+      // (the last bucket and what is beyond weigh less than 2^-90 of the largest: no mass)
+      const uint64_t mass = bucket < kSampleBuckets - 1 ? mass_word(x[i][j], r.grid) : 0;
+      atomicAdd(&hist[bucket * kSampleCopies + (t & (kSampleCopies - 1))], (unsigned long long)(mass + (uint64_t(1) << kMassBits)));
+    }
   __syncthreads();
-  const uint64_t mine = hist[threadIdx.x], sum = wave_sum_u64(mine);
-  const int64_t at = (int64_t)row * a.slices + slice;
-  a.hist[at * kSampleBuckets + threadIdx.x] = mine;
-  if ((threadIdx.x & 63) == 0) atomicAdd(&all, (unsigned long long)sum);
-  __syncthreads();
-  if (threadIdx.x == 0) a.slice[at] = SampleSlice{top, most, all};
+  uint64_t sum = 0;
+#pragma unroll
+  for (int i = 0; i < kSampleCopies; ++i) sum += hist[t * kSampleCopies + i];
+  a.hist[((int64_t)row * a.slices + slice) * kSampleBuckets + t] = sum;
 }
+
+// What a row's histograms say; the same in every thread of its workgroups.
+struct Settled {
+  float top;         // largest logit (0 where that is +inf); -inf: no entry
+  bool inf;
+  double line;       // the grid's line below it
+  int lo, hi;        // buckets before lo are kept whole, those after hi are not; between them the candidates
+  int count;         // entries of the buckets before lo
+  double mass;       // their mass, of the largest's
+  double unit;       // log2 of the weight that candidates' masses refer to: the middle of bucket lo
+  double all;        // mass of all entries
+  int k;             // top-k, 0: off or without effect
+};
 
 // Sums over the threads before this one, in their order.
 struct Before {
   int count;
   double mass;
 };
-__device__ __forceinline__ Before sum_before(int count, double mass, Before* waves) {
-  const int lane = threadIdx.x & 63;
+
+__device__ __forceinline__ Settled settle_row(const SampleArgs& a, int row, const Rules& r) {
+  static_assert(kSampleThreads == kSampleBuckets, "a thread a bucket");
+  constexpr int W = kSampleWaves, U = 10;
+  __shared__ int shift[kSampleThreads];
+  __shared__ float tops[W];
+  __shared__ Before waves[W];
+  __shared__ int k_bucket, p_lo, p_hi, lo_count;
+  __shared__ double k_mass[2], lo_mass;
+  const int b = threadIdx.x, lane = b & 63, wave = b >> 6;
+  const float* part = a.top + (int64_t)row * a.slices;
+  Settled s;
+  float mine = b < a.slices ? part[b] : kNegInf, top = mine;
+  for (int i = b + kSampleThreads; i < a.slices; i += kSampleThreads) top = fmaxf(top, part[i]);
+  top = wave_max(top);
+  if (lane == 0) tops[wave] = top;
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < W; ++i) top = fmaxf(top, tops[i]);
+  top = uniform(top);
+  s.inf = top == -kNegInf;
+  s.top = s.inf ? 0.0f : top;
+  s.line = uniform(line_of(s.top, r.grid));
+  // a thread adds one bucket over the slices
+  int count = 0;
+  uint64_t sum = 0;
+  for (int i0 = 0; i0 < a.slices; i0 += kSampleThreads) {
+    if (i0) {
+      __syncthreads();
+      mine = i0 + b < a.slices ? part[i0 + b] : kNegInf;
+    }
+    // slices without an entry, or without +inf beside one that has it: none
+    const bool there = s.inf ? mine == -kNegInf : mine > kNegInf;
+    shift[b] = there ? (int)fmin(s.line - line_of(s.inf ? 0.0f : mine, r.grid), (double)kSampleBuckets) : 2 * kSampleBuckets;
+    __syncthreads();
+    const int n = min(kSampleThreads, a.slices - i0);
+    const uint64_t* h = a.hist + ((int64_t)row * a.slices + i0) * kSampleBuckets;
+    for (int i = 0; i < n; i += U) {
+      uint64_t x[U];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int at = b - shift[min(i + k, n - 1)];
+        x[k] = i + k < n && at >= 0 && at < kSampleBuckets - 1 ? h[(int64_t)(i + k) * kSampleBuckets + at] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        count += (int)(x[k] >> kMassBits);
+        sum += x[k] & kMassMask;
+      }
+    }
+  }
+  // w of the middle of bucket b is exp((1/2 - f - b) / 8), f of the largest
+  const double middle = (0.5 - __builtin_amdgcn_fract((double)s.top * r.grid) - b) * (0.125 * kLog2E);
+  double mass = sum ? (double)sum / kMassOne * exp2_of(middle) : 0.0;
   int c = count;
   double m = mass;
 #pragma unroll
@@ -228,436 +329,505 @@ __device__ __forceinline__ Before sum_before(int count, double mass, Before* wav
       m += m2;
     }
   }
-  if (lane == 63) waves[threadIdx.x >> 6] = Before{c, m};
-  __syncthreads();
-  Before b = {c - count, m - mass};
-  for (int w = 0; w < (int)(threadIdx.x >> 6); ++w) {
-    b.count += waves[w].count;
-    b.mass += waves[w].mass;
-  }
-  return b;
-}
-
-// What the row's histograms say; the same in every thread of every workgroup.
-__device__ __forceinline__ SampleRow settle_row(const SampleArgs& a, int row, const Rules& r) {
-  static_assert(kSampleThreads == kSampleBuckets, "a thread a bucket");
-  __shared__ double scale[kSampleThreads];
-  __shared__ int shift[kSampleThreads];
-  __shared__ float tops[kSampleThreads / 64];
-  __shared__ Before waves[kSampleThreads / 64];
-  __shared__ int all_count, k_bucket, p_lo, p_hi, lo_count;
-  __shared__ double all_mass, k_mass[2], lo_mass;
-  const int b = threadIdx.x;
-  const SampleSlice* part = a.slice + (int64_t)row * a.slices;
-  SampleRow s;
-  float top = kNegInf;
-  for (int i = b; i < a.slices; i += kSampleThreads) top = fmaxf(top, part[i].top);
-  top = wave_max(top);
-  if ((b & 63) == 0) tops[b >> 6] = top;
-  __syncthreads();
-  for (int i = 0; i < kSampleThreads / 64; ++i) top = fmaxf(top, tops[i]);
-  s.top = top;
-  s.bucket = bucket_of(top, r.grid);
-  // a thread adds one bucket over the slices; the last one, what is left of all
-  int count = 0, all_c = 0;
-  double mass = 0.0, all_m = 0.0;
-  for (int i0 = 0; i0 < a.slices; i0 += kSampleThreads) {
-    __syncthreads();
-    if (i0 + b < a.slices) {
-      const SampleSlice p = part[i0 + b];
-      scale[b] = p.top > kNegInf ? ldexp(weight_of(p.top, top, r.rate), -kMassScale) : 0.0;
-      shift[b] = p.top > kNegInf ? s.bucket - p.bucket : kSampleBuckets;
-    }
-    __syncthreads();
-    const int n = min(kSampleThreads, a.slices - i0);
-    const uint64_t* h = a.hist + ((int64_t)row * a.slices + i0) * kSampleBuckets;
-    for (int i = 0; i < n; ++i) {
-      const int at = b - shift[i];
-      uint64_t x = 0;
-      if (b == kSampleBuckets - 1)
-        x = part[i0 + i].all;
-      else if (at >= 0)
-        x = h[(int64_t)i * kSampleBuckets + at];
-      count += (int)(x >> kMassBits);
-      mass += (double)(x & kMassMask) * scale[i];
-    }
-  }
-  if (b == kSampleBuckets - 1) {
-    all_c = count;
-    all_m = mass;
-    count = 0;
-    mass = 0.0;
-  }
-  Before before = sum_before(count, mass, waves);
-  if (b == kSampleBuckets - 1) {
-    count = all_c - before.count;
-    mass = fmax(all_m - before.mass, 0.0);
-    all_count = all_c;
-    all_mass = before.mass + mass;
+  if (lane == 63) waves[wave] = Before{c, m};
+  if (b == 0) {
     k_bucket = p_lo = p_hi = kSampleBuckets - 1;
-    lo_count = 0;
-    lo_mass = 0.0;
+    k_mass[0] = k_mass[1] = -1.0;
   }
   __syncthreads();
-  const bool k_on = r.k > 0 && r.k < all_count, p_on = r.p < 1.0f, m_on = r.m > 0.0f;
-  if (k_on && before.count < r.k && before.count + count >= r.k) {
+  Before before = {0, 0.0}, all = {0, 0.0};
+#pragma unroll
+  for (int w = 0; w < W; ++w) {
+    if (w == wave) before = all;
+    all.count += waves[w].count;
+    all.mass += waves[w].mass;
+  }
+  const double end = before.mass + m;
+  before.count += c - count;
+  before.mass = fmax(end - mass, 0.0);
+  // the last bucket holds what all others do not: no mass, and any number of entries
+  const bool p_on = r.p < 1.0f, m_on = r.m > 0.0f;
+  s.all = all.mass;
+  if (r.k > 0 && before.count < r.k && before.count + count >= r.k) {
     k_bucket = b;
     k_mass[0] = before.mass;
-    k_mass[1] = before.mass + mass;
+    k_mass[1] = end;
   }
   __syncthreads();
   // the border lies where the mass reaches p of the first k's, which is known up to the k-th's bucket: the first
   // bucket that reaches it (rounding of these sums allowed for)
+  const bool k_found = k_mass[1] >= 0.0;
   if (p_on) {
-    const double p = fmax((double)r.p, 0.0), least = p * (k_on ? k_mass[0] : all_mass) * (1.0 - 1e-9),
-                 most = p * (k_on ? k_mass[1] : all_mass) * (1.0 + 1e-9);
-    const double end = before.mass + mass;
+    const double least = (double)r.p * (k_found ? k_mass[0] : all.mass) * (1.0 - 1e-10),
+                 most = (double)r.p * (k_found ? k_mass[1] : all.mass) * (1.0 + 1e-10);
     if (end >= least && (b == 0 || before.mass < least)) atomicMin(&p_lo, b);
     if (end >= most && (b == 0 || before.mass < most)) atomicMin(&p_hi, b);
   }
   __syncthreads();
+  // a k beyond the entries that have mass cuts nothing that top-p has not
+  s.k = p_on && !k_found ? 0 : r.k;
   s.lo = kSampleBuckets;
   s.hi = kSampleBuckets - 1;
-  if (k_on) {
-    s.lo = min(s.lo, k_bucket);
-    s.hi = min(s.hi, k_bucket);
-  }
+  if (s.k) s.lo = s.hi = k_bucket;
   if (p_on) {
     s.lo = min(s.lo, p_lo);
-    if (!k_on) s.hi = min(s.hi, p_hi);
+    if (!s.k) s.hi = min(s.hi, p_hi);
   }
   if (m_on) {
-    // (logits beyond the grid's ends share a bucket: nothing is sure then)
-    const float at = abs(s.bucket) < 8388608 - 1024 ? floorf(-logf(r.m) * r.span) : __uint_as_float(0x7fc00000u);
-    s.lo = min(s.lo, (int)fminf(fmaxf(at - 2.0f, 0.0f), kSampleBuckets - 1.0f));
-    if (!(k_on && p_on)) s.hi = min(s.hi, (int)fminf(at + 3.0f, kSampleBuckets - 1.0f));
+    const float at = floorf(-8.0f * logf(r.m));
+    s.lo = min(s.lo, (int)fminf(fmaxf(at - 1.0f, 0.0f), kSampleBuckets - 1.0f));
+    if (!(s.k && p_on)) s.hi = min(s.hi, (int)fminf(at + 2.0f, kSampleBuckets - 1.0f));
   }
   if (b == s.lo) {
     lo_count = before.count;
     lo_mass = before.mass;
   }
   if (s.lo == kSampleBuckets && b == 0) {
-    lo_count = all_count;
-    lo_mass = all_mass;
+    lo_count = all.count;
+    lo_mass = all.mass;
   }
   __syncthreads();
-  s.count = lo_count;
-  s.mass = (uint64_t)rint(ldexp(lo_mass, kMassScale));
-  s.greedy = r.greedy;
-  s.rate = r.rate;
-  s.limit = fmax((double)r.p, 0.0) * ldexp(all_mass, kMassScale);
-  s.top_k = k_on ? r.k : 0;
-  s.top_p = r.p;
-  s.min_p = r.m;
-  s.least = 0;
-  s.total = 0;
+  s.lo = uniform(s.lo);
+  s.hi = uniform(s.hi);
+  s.k = uniform(s.k);
+  s.all = uniform(s.all);
+  s.count = uniform(lo_count);
+  s.mass = uniform(lo_mass);
+  s.unit = (0.5 - __builtin_amdgcn_fract((double)s.top * r.grid) - s.lo) * (0.125 * kLog2E);
   return s;
 }
 
-template <bool BF16, int PIECES>
-__global__ void __launch_bounds__(kSampleThreads) sample_collect_kernel(SampleArgs a) {
-  const int row = blockIdx.y, slice = blockIdx.x, first = slice * PIECES * 8 * kSampleThreads;
-  __shared__ uint64_t tops[kSampleThreads / 64];
-  __shared__ int found;
-  const Rules r = rules_of(a, row);
-  if (threadIdx.x == 0) found = 0;
-  const SampleRow s = settle_row(a, row, r);
-  const int64_t at = (int64_t)row * a.slices + slice;
-  uint64_t best = 0, *list = a.cand + at * a.entries;
-  for (int i = 0; i < PIECES; ++i) {
-    const int v = first + (i * kSampleThreads + (int)threadIdx.x) * 8;
-    float x[8];
-    load_logits<BF16>(a, row, v, x);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (!(x[j] > kNegInf)) continue;
-      const int bucket = min(s.bucket - bucket_of(x[j], r.grid), kSampleBuckets - 1);
-      if (bucket < s.lo) {
-        const uint64_t score = score_of(weight_of(x[j], s.top, s.rate), a.noise[(int64_t)row * a.vocab + v + j], v + j);
-        best = score > best ? score : best;
-      } else if (bucket <= s.hi) {
-        list[atomicAdd(&found, 1)] = key_of(x[j], v + j);
-      }
-    }
-  }
-  best = wave_max_key(best);
-  if ((threadIdx.x & 63) == 0) tops[threadIdx.x >> 6] = best;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    for (int i = 1; i < kSampleThreads / 64; ++i) best = tops[i] > best ? tops[i] : best;
-    a.best[at] = best;
-    a.found[at] = found;
-    if (slice == 0) a.state[row] = s;
-  }
+// An entry's weight, relative to the largest's.
+__device__ __forceinline__ double weight_of(float l, float top, double rate) {
+  return exp2_of(((double)l - (double)top) * rate);
+}
+// A candidate's mass, in steps of 2^-34 of the middle of the first candidates'
+// bucket: in that one the number that the histogram has.
+__device__ __forceinline__ uint64_t cand_mass(float l, const Settled& s, double grid) {
+  const double below = s.line - line_of(l, grid) - s.lo;
+  const uint64_t m = mass_word(l, grid);
+  return below == 0.0 ? m : (uint64_t)rint((double)m * exp2_of(-below * (0.125 * kLog2E)));
 }
 
-constexpr int kFinishThreads = 512;
-constexpr int kFinishHeld = 2048;   // candidates that a workgroup keeps in LDS
-constexpr int kFinishLast = 64;     // candidates that one wave orders by itself
-
-// A row's candidates.
-struct Candidates {
-  const SampleArgs& a;
-  int row, n;
-  uint64_t* held;
-  template <class F>
-  __device__ __forceinline__ void each(F f) const {
-    if (n <= kFinishHeld) {
-      for (int i = threadIdx.x; i < n; i += kFinishThreads) f(held[i]);
-    } else {
-      for (int s = threadIdx.x >> 6; s < a.slices; s += kFinishThreads / 64) {
-        const int64_t at = (int64_t)row * a.slices + s;
-        for (int i = threadIdx.x & 63; i < a.found[at]; i += 64) f(a.cand[at * a.entries + i]);
-      }
+// The best score among many entries, a wave together: few can be the best one,
+// so binary32's exponential and reciprocal pick out those that come within 10^-4
+// of the best so far (what these can be off by while w is a binary32 number).
+struct BestScore {
+  uint64_t best = 0;   // this lane's
+  float bound = 0.0f;  // of the wave's
+  __device__ __forceinline__ void add(const bool (&in)[4], const uint64_t (&key)[4], const float (&noise)[4], float top, double rate) {
+    float about[4], most = 0.0f;
+    bool near = false;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      about[u] = __builtin_amdgcn_exp2f((logit_of(key[u]) - top) * (float)rate) * __builtin_amdgcn_rcpf(noise[u]);
+      near |= in[u] && !(about[u] < bound);
+      most = in[u] ? fmaxf(most, about[u]) : most;
     }
+    if (!__any(near)) return;
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if (in[u] && !(about[u] < bound)) {
+        const uint64_t score = score_of(weight_of(logit_of(key[u]), top, rate), noise[u], index_of(key[u]));
+        best = score > best ? score : best;
+      }
+    most = wave_max(most) * (1.0f - 1e-4f);
+    bound = most > 1e-30f && most < 1e30f ? fmaxf(bound, most) : bound;
   }
 };
 
-// The last candidate in the order that is kept: by rank (fewer than `most`
-// entries before it) or, most < 0, by mass (less than `limit` before it).
-// -> its key (all ones: none is kept) and the mass up to and with it.  Candidates
-// are counted into 256 parts of their range, again within the part that the
-// border lies in, until one wave orders what is left.
-__device__ __forceinline__ uint64_t border(const Candidates& c, const SampleRow& s, int most, double limit, uint64_t* upto) {
-  __shared__ unsigned long long mass[256], low, high, keys[kFinishLast];
-  __shared__ unsigned count[256];
-  __shared__ uint64_t b_mass, out_key, out_mass;
-  __shared__ int b_count, part, listed;
-  const int t = threadIdx.x;
-  uint64_t lo = 0, hi = ~uint64_t(0);   // range of keys that the border is among
-  int before = s.count;                 // entries before that range, and their mass
-  uint64_t before_mass = s.mass;
-  int inside = c.n;
-  while (inside > kFinishLast) {
-    // the range that is in use
-    if (t == 0) {
-      low = ~0ull;
-      high = 0;
-      part = -1;
-    }
-    if (t < 256) {
-      mass[t] = 0;
-      count[t] = 0;
-    }
-    __syncthreads();
-    uint64_t a = ~uint64_t(0), b = 0;
-    c.each([&](uint64_t k) {
-      if (k >= lo && k <= hi) {
-        a = k < a ? k : a;
-        b = k > b ? k : b;
-      }
-    });
-    b = wave_max_key(b);
-    a = ~wave_max_key(~a);
-    if ((t & 63) == 0) {
-      atomicMin(&low, (unsigned long long)a);
-      atomicMax(&high, (unsigned long long)b);
-    }
-    __syncthreads();
-    lo = low;
-    hi = high;
-    const int shift = max(0, 56 - __clzll((long long)(hi - lo)));
-    c.each([&](uint64_t k) {
-      if (k >= lo && k <= hi) {
-        const int i = (int)((hi - k) >> shift);
-        atomicAdd(&count[i], 1u);
-        atomicAdd(&mass[i], (unsigned long long)mass_of(logit_of((uint32_t)(k >> 32)), s.top, s.rate));
-      }
-    });
-    __syncthreads();
-    // wave 0: the part of the border, four a lane
-    if (t < 64) {
-      int n[4], sum = 0;
-      uint64_t m[4], msum = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        n[i] = (int)count[4 * t + i];
-        m[i] = mass[4 * t + i];
-        sum += n[i];
-        msum += m[i];
-      }
-      int at = sum;
-      uint64_t mat = msum;
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const int x = __shfl_up(at, o, 64);
-        const uint64_t y = (uint64_t)__shfl_up((unsigned long long)mat, o, 64);
-        if (t >= o) {
-          at += x;
-          mat += y;
-        }
-      }
-      at += before - sum;
-      mat += before_mass - msum;
-      int mine = -1, mine_at = 0;
-      uint64_t mine_mass = 0;
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        // the last part whose first entry is kept
-        if (n[i] > 0 && (most >= 0 ? at < most : (double)mat < limit)) {
-          mine = 4 * t + i;
-          mine_at = at;
-          mine_mass = mat;
-        }
-        at += n[i];
-        mat += m[i];
-      }
-      const uint64_t any = __ballot(mine >= 0);
-      if (any && t == 63 - __clzll((long long)any)) {
-        part = mine;
-        b_count = mine_at;
-        b_mass = mine_mass;
-      }
-    }
-    __syncthreads();
-    const int p = part;
-    if (p < 0) {   // not even the first one
-      *upto = before_mass;
-      __syncthreads();
-      return ~uint64_t(0);
-    }
-    before = b_count;
-    before_mass = b_mass;
-    inside = (int)count[p];
-    const uint64_t top = hi - ((uint64_t)p << shift);
-    const uint64_t wide = (uint64_t(1) << shift) - 1;
-    lo = top - lo > wide ? top - wide : lo;
-    hi = top;
-    __syncthreads();
-  }
-  if (t == 0) listed = 0;
-  __syncthreads();
-  c.each([&](uint64_t k) {
-    if (k >= lo && k <= hi) keys[atomicAdd(&listed, 1)] = k;
-  });
-  __syncthreads();
-  if (t < 64) {
-    const bool in = t < listed;
-    const uint64_t key = in ? keys[t] : 0;
-    const uint64_t own = in ? mass_of(logit_of((uint32_t)(key >> 32)), s.top, s.rate) : 0;
-    int at = before;
-    uint64_t mat = before_mass;
-    for (int j = 0; j < listed; ++j) {
-      const uint64_t k = (uint64_t)__shfl((unsigned long long)key, j, 64), m = (uint64_t)__shfl((unsigned long long)own, j, 64);
-      if (k > key) {
-        ++at;
-        mat += m;
-      }
-    }
-    const bool kept = in && (most >= 0 ? at < most : (double)mat < limit);
-    const uint64_t last = ~wave_max_key(kept ? ~key : 0);   // the smallest kept key; none: all ones
-    const uint64_t sum = wave_max_key(kept ? mat + own : before_mass);
-    if (t == 0) {
-      out_key = last;
-      out_mass = sum;
-    }
-  }
-  __syncthreads();
-  const uint64_t key = out_key;
-  *upto = out_mass;
-  __syncthreads();
-  return key;
+// What a row's workgroups leave for its last one is stored and read at the
+// point that is coherent for all XCDs, so no write-back of an L2 is needed (a
+// fence by each of 1,216 workgroups took 190 us).
+template <class T>
+__device__ __forceinline__ void store_shared(T* p, T v) {
+  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+template <class T>
+__device__ __forceinline__ T load_shared(const T* p) {
+  return __hip_atomic_load(const_cast<T*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
+constexpr int kFinishLast = 64;     // candidates that one wave orders by itself
+constexpr int kFinishParts = 256;   // parts that a range of candidates is counted into
+constexpr int kFinishCopies = 2;    // of the counts: lanes of equal parts add one after the other
+constexpr int kWaveList = 1024;     // entries that a wave notes before it works on them: a piece's 512 and as many more
+constexpr int kHeld = kSampleWaves * kWaveList;
+
+// LDS of a workgroup of the second launch.
+struct CollectSpace {
+  uint64_t held[kHeld];   // waves' lists: surely kept entries from the front, candidates from the back; then the row's candidates
+  unsigned long long mass[kFinishCopies][kFinishParts];
+  unsigned count[kFinishCopies][kFinishParts];
+  unsigned long long keys[kFinishLast], own[kFinishLast];
+  uint64_t tops[kSampleWaves], sums[kSampleWaves];
+  uint64_t b_mass;
+  int b_count, part, listed, last;
+};
+
+// f(keys, which are there) for the candidates of a row, four a lane at a time
+// with all lanes of a wave together: from LDS, where they are loaded to in turns
+// if they are very many.
+constexpr int kEach = 4;
+template <class F>
+__device__ __forceinline__ void each(const uint64_t* list, int n, uint64_t* held, bool loaded, F f) {
+#pragma unroll 1
+  for (int c0 = 0; c0 < n; c0 += kHeld) {
+    const int m = min(n - c0, kHeld);
+    if (!loaded) {
+      __syncthreads();
+#pragma unroll 8
+      for (int i = threadIdx.x; i < m; i += kSampleThreads) held[i] = load_shared(list + c0 + i);
+      __syncthreads();
+    }
+#pragma unroll 1
+    for (int i0 = 0; i0 < m; i0 += kEach * kSampleThreads) {
+      uint64_t key[kEach];
+      bool in[kEach];
+#pragma unroll
+      for (int u = 0; u < kEach; ++u) {
+        const int i = i0 + u * kSampleThreads + (int)threadIdx.x;
+        in[u] = i < m;
+        key[u] = held[min(i, m - 1)];
+      }
+      f(key, in);
+    }
+  }
+}
+
+// The token, by the row's last workgroup: everything that the others wrote is
+// there.  The border among the candidates is looked for by rank (top-k), then by
+// mass (top-p): the last one that is kept has fewer than `most` of them before
+// it, or less than `limit` of their mass.  They are counted into parts of their
+// range, again within the part that the border lies in, until one wave orders
+// what is left.  (The code is run once a row, from a cold instruction cache: it
+// is kept short.  Unrolled to five times its length it took 2 to 3 times as long.)
 template <bool BF16>
-__global__ void __launch_bounds__(kFinishThreads) sample_finish_kernel(SampleArgs a) {
-  __shared__ uint64_t held[kFinishHeld], tops[kFinishThreads / 64], sums[kFinishThreads / 64];
-  __shared__ int n, listed;
-  const int row = blockIdx.x, t = threadIdx.x;
-  SampleRow s = a.state[row];
-  if (s.top == kNegInf) {   // no entry at all
-    if (t == 0) {
-      a.tokens[row] = -1;
-      if (a.logprobs) a.logprobs[row] = kNegInf;
-    }
-    return;
-  }
-  if (t == 0) n = listed = 0;
-  __syncthreads();
-  uint64_t best = 0;
-  for (int i = t; i < a.slices; i += kFinishThreads) {
-    const int64_t at = (int64_t)row * a.slices + i;
-    const uint64_t b = a.best[at];
-    best = b > best ? b : best;
-    atomicAdd(&n, a.found[at]);
-  }
-  __syncthreads();
-  const Candidates c = {a, row, n, held};
-  if (n <= kFinishHeld) {
-    for (int i = t >> 6; i < a.slices; i += kFinishThreads / 64) {
-      const int64_t at = (int64_t)row * a.slices + i;
-      for (int j = t & 63; j < a.found[at]; j += 64) held[atomicAdd(&listed, 1)] = a.cand[at * a.entries + j];
-    }
+__device__ __forceinline__ void finish_row(const SampleArgs& a, int row, const Rules& r, const Settled& s, CollectSpace& sp) {
+  const int t = threadIdx.x, copy = t % kFinishCopies;
+  const uint64_t* list = a.cand + (int64_t)row * a.vocab;
+  const int n = load_shared(a.count + 2 * row);
+  uint64_t best = load_shared(a.best + row);
+  const bool held = n <= kHeld;
+  if (held) {
+#pragma unroll 8
+    for (int i = t; i < n; i += kSampleThreads) sp.held[i] = load_shared(list + i);
     __syncthreads();
   }
-  uint64_t least = 0, upto;
-  if (c.n > 0) {
-    if (s.top_k) {
-      least = border(c, s, s.top_k, 0.0, &upto);
-      s.limit = (double)s.top_p * (double)upto;
+  const double step = exp2_of(s.unit) / kMassOne;   // of candidates' masses
+  // a mass that reaches the limit but for these products' rounding does; the first entry is kept whatever it is
+  double limit = (double)r.p * s.all;
+  uint64_t least = 0, upto = 0;   // smallest kept candidate, and the mass up to it
+#pragma unroll 1
+  for (int by_mass = 0; by_mass < 2; ++by_mass) {
+    if (n == 0 || !(by_mass ? r.p < 1.0f : s.k > 0)) continue;
+    const int most = s.k - s.count;
+    if (by_mass) {
+      limit = (limit * (1.0 - 1e-13) - s.mass) / step;
+      if (s.count == 0) limit = fmax(limit, 0.5);
     }
-    if (s.top_p < 1.0f) {
-      // the first entry is kept whatever the limit
-      const uint64_t k = border(c, s, -1, fmax(s.limit, 0.5), &upto);
-      least = k > least ? k : least;
+    // the range of keys that the border is among: at first the candidates' buckets and a line more to each side
+    // (rounding to binary32 passes no logit)
+    uint64_t hi = key_of((float)((s.line - s.lo + 2.0) / r.grid), 0), lo = 0;
+    if (s.hi < kSampleBuckets - 1) lo = key_of((float)((s.line - s.hi - 1.0) / r.grid), 0) & ~uint64_t(0xffffffff);
+    int before = 0, inside = n;   // candidates before that range, and in it
+    uint64_t before_mass = 0;
+#pragma unroll 1
+    while (inside > kFinishLast) {
+      if (t == 0) sp.part = -1;
+      if (t < kFinishCopies * kFinishParts) (&sp.mass[0][0])[t] = (&sp.count[0][0])[t] = 0;
+      __syncthreads();
+      const int shift = max(0, 56 - __clzll((long long)(hi - lo)));
+      each(list, n, sp.held, held, [&](uint64_t (&key)[kEach], bool (&there)[kEach]) {
+        uint64_t mass[kEach];
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) mass[u] = cand_mass(logit_of(key[u]), s, r.grid);
+#pragma unroll
+        for (int u = 0; u < kEach; ++u) {
+          const uint64_t k = key[u];
+          const bool in = there[u] && k >= lo && k <= hi;
+          const int i = (int)((hi - k) >> shift);
+          if (in) {
+            atomicAdd(&sp.count[copy][i], 1u);
+            atomicAdd(&sp.mass[copy][i], (unsigned long long)mass[u]);
+          }
+        }
+      });
+      __syncthreads();
+      // wave 0: the last part whose first entry is kept, four of them a lane
+      if (t < 64) {
+        constexpr int L = kFinishParts / 64;
+        int c[L], sum = 0;
+        uint64_t m[L], msum = 0;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          c[i] = (int)(sp.count[0][L * t + i] + sp.count[1][L * t + i]);
+          m[i] = sp.mass[0][L * t + i] + sp.mass[1][L * t + i];
+          sum += c[i];
+          msum += m[i];
+        }
+        int at = sum;
+        uint64_t mat = msum;
+#pragma unroll 1
+        for (int o = 1; o < 64; o <<= 1) {
+          const int x = __shfl_up(at, o, 64);
+          const uint64_t y = (uint64_t)__shfl_up((unsigned long long)mat, o, 64);
+          if (t >= o) {
+            at += x;
+            mat += y;
+          }
+        }
+        at += before - sum;
+        mat += before_mass - msum;
+        int mine = -1, mine_at = 0;
+        uint64_t mine_mass = 0;
+#pragma unroll
+        for (int i = 0; i < L; ++i) {
+          if (c[i] > 0 && (by_mass ? (double)mat < limit : at < most)) {
+            mine = L * t + i;
+            mine_at = at;
+            mine_mass = mat;
+          }
+          at += c[i];
+          mat += m[i];
+        }
+        const uint64_t any = __ballot(mine >= 0);
+        if (any && t == 63 - __clzll((long long)any)) {
+          sp.part = mine;
+          sp.b_count = mine_at;
+          sp.b_mass = mine_mass;
+        }
+      }
+      __syncthreads();
+      const int p = sp.part;
+      if (p < 0) {   // not even the first one is kept
+        inside = 0;
+      } else {
+        before = sp.b_count;
+        before_mass = sp.b_mass;
+        inside = (int)(sp.count[0][p] + sp.count[1][p]);
+        const uint64_t top = hi - ((uint64_t)p << shift), wide = (uint64_t(1) << shift) - 1;
+        lo = top - lo > wide ? top - wide : lo;
+        hi = top;
+        // the ends of the range come to the next keys that there can be: bf16 logits have but a few values (their
+        // orders end in 16 zeros, below 0 ones), equal logits the vocabulary's indices
+        uint32_t l = (uint32_t)(lo >> 32), h = (uint32_t)(hi >> 32);
+        if (BF16) {
+          l = l & 0x80000000u ? (l + 0xffffu) & 0xffff0000u : l | 0xffffu;
+          h = h & 0x80000000u ? h & 0xffff0000u : ((h + 1u) & 0xffff0000u) - 1u;
+        }
+        lo = max_u64(lo, (uint64_t)l << 32 | (0xffffffffu - (uint32_t)(a.vocab - 1)));
+        hi = ~max_u64(~hi, ~((uint64_t)h << 32 | 0xffffffffu));
+      }
+      __syncthreads();
     }
+    if (t == 0) sp.listed = 0;
+    __syncthreads();
+    if (inside > 0)
+      each(list, n, sp.held, held, [&](uint64_t (&key)[kEach], bool (&there)[kEach]) {
+#pragma unroll
+        for (int u = 0; u < kEach; ++u)
+          if (there[u] && key[u] >= lo && key[u] <= hi) sp.keys[atomicAdd(&sp.listed, 1)] = key[u];
+      });
+    __syncthreads();
+    // every wave the same: an entry a lane
+    const int m = uniform(sp.listed), lane = t & 63;
+    const uint64_t key = lane < m ? sp.keys[lane] : 0, mass = lane < m ? cand_mass(logit_of(key), s, r.grid) : 0;
+    if (t < 64) sp.own[lane] = mass;
+    __syncthreads();
+    int at = before;
+    uint64_t mat = before_mass;
+#pragma unroll 8
+    for (int j = 0; j < m; ++j) {
+      const bool ahead = sp.keys[j] > key;
+      at += ahead;
+      mat += ahead ? sp.own[j] : 0;
+    }
+    const bool kept = lane < m && (by_mass ? (double)mat < limit : at < most);
+    const uint64_t last = ~wave_max_key(kept ? ~key : 0);   // the smallest kept key; none: all ones
+    upto = wave_max_key(kept ? mat + mass : before_mass);
+    if (!by_mass) limit = (double)r.p * (s.mass + (double)upto * step);
+    least = last > least ? last : least;
+    __syncthreads();
   }
+  // the kept candidates' scores; their mass anew where min-p drops some
   uint64_t sum = 0;
-  if (c.n > 0)
-    c.each([&](uint64_t k) {
-      if (k < least) return;
-      const float l = logit_of((uint32_t)(k >> 32));
-      const double w = weight_of(l, s.top, s.rate);
-      if (w < (double)s.min_p) return;
-      const int v = (int)(0xffffffffu - (uint32_t)k);
-      sum += mass_of(l, s.top, s.rate);
-      const uint64_t score = score_of(w, a.noise[(int64_t)row * a.vocab + v], v);
-      best = score > best ? score : best;
-    });
+  BestScore score;
+  const float* noise = a.noise + (int64_t)row * a.vocab;
+  each(list, n, sp.held, held, [&](uint64_t (&key)[kEach], bool (&there)[kEach]) {
+    float e[kEach];
+#pragma unroll
+    for (int u = 0; u < kEach; ++u) {
+      there[u] = there[u] && key[u] >= least;
+      e[u] = there[u] ? noise[index_of(key[u])] : 1.0f;
+    }
+    if (r.m > 0.0f) {
+#pragma unroll
+      for (int u = 0; u < kEach; ++u) {
+        there[u] = there[u] && weight_of(logit_of(key[u]), s.top, r.rate) >= (double)r.m;
+        if (there[u]) sum += cand_mass(logit_of(key[u]), s, r.grid);
+      }
+    }
+    score.add(there, key, e, s.top, r.rate);
+  });
+  best = score.best > best ? score.best : best;
   best = wave_max_key(best);
   sum = wave_sum_u64(sum);
   if ((t & 63) == 0) {
-    tops[t >> 6] = best;
-    sums[t >> 6] = sum;
+    sp.tops[t >> 6] = best;
+    sp.sums[t >> 6] = sum;
   }
   __syncthreads();
   if (t == 0) {
-    sum += s.mass;
-    for (int i = 1; i < kFinishThreads / 64; ++i) {
-      best = tops[i] > best ? tops[i] : best;
-      sum += sums[i];
+    for (int i = 1; i < kSampleWaves; ++i) {
+      best = sp.tops[i] > best ? sp.tops[i] : best;
+      sum += sp.sums[i];
     }
-    s.least = least;
-    s.total = sum;
-    a.state[row] = s;
-    const int v = (int)(0xffffffffu - (uint32_t)best);
+    const double total = s.mass + (double)(r.m > 0.0f ? sum : upto) * step;
+    const int v = index_of(best);
     a.tokens[row] = v;
     if (a.logprobs) {
       const int64_t at = row * a.row + v;
       const float l = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
-      a.logprobs[row] = (float)log(ldexp(weight_of(l + 0.0f, s.top, s.rate), kMassScale) / (double)sum);
+      a.logprobs[row] = (float)log(weight_of(s.inf ? 0.0f : l, s.top, r.rate) / total);
     }
+    if (a.probs) a.state[row] = SampleRow{total, least, s.inf ? -kNegInf : s.top, s.lo, s.hi};
   }
 }
 
+template <bool BF16, int PIECES>
+__global__ void __launch_bounds__(kSampleThreads, 4) sample_collect_kernel(SampleArgs a) {
+  constexpr int E = PIECES * 8 * kSampleThreads;
+  const int row = blockIdx.y, slice = blockIdx.x, first = slice * E, t = threadIdx.x, lane = t & 63;
+  __shared__ CollectSpace sp;
+  float x[8];
+  load_logits<BF16>(a, row, first + t * 8, x);
+  const Rules r = rules_of(a, row);
+  const Settled s = settle_row(a, row, r);
+  if (s.top == kNegInf) {   // no entry at all
+    if (slice == 0 && t == 0) {
+      a.tokens[row] = -1;
+      if (a.logprobs) a.logprobs[row] = kNegInf;
+      if (a.probs) a.state[row].top = kNegInf;
+    }
+    return;
+  }
+  // (no buckets after the last one: the comparisons are with lines as they lie)
+  const double sure = s.lo == kSampleBuckets ? __builtin_huge_val() : s.lo;
+  const double maybe = s.hi == kSampleBuckets - 1 ? __builtin_huge_val() : s.hi;
+  uint64_t* list = sp.held + (t >> 6) * kWaveList;
+  int found[2] = {0, 0};   // entries of the wave's list
+  BestScore score;
+#pragma unroll 1
+  for (int i = 0; i < PIECES; ++i) {
+    const int v = first + (i * kSampleThreads + t) * 8;
+    unsigned bits[2] = {0, 0};
+    float now[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      now[j] = s.inf ? beside_inf(x[j]) : x[j];
+      const double below = s.line - line_of(now[j], r.grid);
+      const bool there = now[j] > kNegInf;
+      bits[0] |= (unsigned)(there && below < sure) << j;
+      bits[1] |= (unsigned)(there && below >= sure && below <= maybe) << j;
+    }
+    if (i + 1 < PIECES) load_logits<BF16>(a, row, v + 8 * kSampleThreads, x);
+    const float* noise = a.noise + (int64_t)row * a.vocab;
+    // all of the wave's are kept: without the list
+    if (__all(bits[0] == 0xffu)) {
+      const f32x4u* p = reinterpret_cast<const f32x4u*>(noise + v);
+      const f32x4u e[2] = {p[0], p[1]};
+      const bool in[4] = {true, true, true, true};
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint64_t key[4];
+        float y[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          key[u] = key_of(now[4 * h + u], v + 4 * h + u);
+          y[u] = e[h][u];
+        }
+        score.add(in, key, y, s.top, r.rate);
+      }
+      bits[0] = 0;
+    }
+    // places in the list: sums over the lanes
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      if (!__any(bits[kind] != 0)) continue;
+      const int n = __popc(bits[kind]), upto = inclusive_sum(n);
+      int at = found[kind] + upto - n;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (bits[kind] >> j & 1) {
+          list[kind ? kWaveList - 1 - at : at] = key_of(now[j], v + j);
+          ++at;
+        }
+      found[kind] += lane_i32(upto, 63);
+    }
+    const bool end = i + 1 == PIECES;
+    if (!end && found[0] + found[1] <= kWaveList - 512) continue;
+    // the candidates' place in the row's list; as a rule all of the wave's at the end
+    const bool flush = found[1] > 0 && (end || found[1] > 128);
+    int base = 0;
+    if (flush && lane == 0) base = atomicAdd(&a.count[2 * row], found[1]);
+#pragma unroll 1
+    for (int k = 0; k < found[0]; k += 256) {
+      uint64_t key[4];
+      float e[4];
+      bool in[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        in[u] = k + 64 * u + lane < found[0];
+        key[u] = list[min(k + 64 * u + lane, found[0] - 1)];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) e[u] = noise[index_of(key[u])];
+      score.add(in, key, e, s.top, r.rate);
+    }
+    found[0] = 0;
+    if (flush) {
+      base = lane_i32(base, 0);
+#pragma unroll 1
+      for (int k = lane; k < found[1]; k += 64) store_shared(a.cand + (int64_t)row * a.vocab + base + k, list[kWaveList - 1 - k]);
+      found[1] = 0;
+    }
+  }
+  const uint64_t best = wave_max_key(score.best);
+  if (lane == 0 && best) atomicMax(reinterpret_cast<unsigned long long*>(a.best + row), (unsigned long long)best);
+  // the last of the row's workgroups goes on
+  __builtin_amdgcn_s_waitcnt(0);
+  __syncthreads();
+  if (t == 0) sp.last = atomicAdd(&a.count[2 * row + 1], 1) == a.slices - 1;
+  __syncthreads();
+  if (!sp.last) return;
+  finish_row<BF16>(a, row, r, s, sp);
+}
+
+constexpr int kWriteThreads = 256;
+
 // Probabilities: w over the mass of the kept entries.
 template <bool BF16>
-__global__ void __launch_bounds__(kSampleThreads) sample_write_kernel(SampleArgs a) {
-  const int row = blockIdx.y, v = ((int)blockIdx.x * kSampleThreads + (int)threadIdx.x) * 8;
+__global__ void __launch_bounds__(kWriteThreads) sample_write_kernel(SampleArgs a) {
+  const int row = blockIdx.y, v = ((int)blockIdx.x * kWriteThreads + (int)threadIdx.x) * 8;
   if (v >= a.vocab) return;
   const SampleRow s = a.state[row];
   const Rules r = rules_of(a, row);
-  const double per = s.top > kNegInf ? ldexp(1.0, kMassScale) / (double)s.total : 0.0;
+  const bool inf = s.top == -kNegInf;
+  const float top = inf ? 0.0f : s.top;
+  const double line = line_of(top, r.grid), per = 1.0 / s.total;
   float x[8], p[8];
   load_logits<BF16>(a, row, v, x);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     p[j] = 0.0f;
+    if (inf) x[j] = beside_inf(x[j]);
     if (!(x[j] > kNegInf)) continue;
-    const int bucket = min(s.bucket - bucket_of(x[j], r.grid), kSampleBuckets - 1);
-    if (bucket < s.lo || (bucket <= s.hi && key_of(x[j], v + j) >= s.least)) {
-      const double w = weight_of(x[j], s.top, s.rate);
-      if (bucket < s.lo || w >= (double)s.min_p) p[j] = (float)(w * per);
+    const double below = line - line_of(x[j], r.grid);
+    const bool in = below < s.lo || s.lo == kSampleBuckets;
+    if (in || ((below <= s.hi || s.hi == kSampleBuckets - 1) && key_of(x[j], v + j) >= s.least)) {
+      const double w = weight_of(x[j], top, r.rate);
+      if (in || w >= (double)r.m) p[j] = (float)(w * per);
     }
   }
   float* out = a.probs + (int64_t)row * a.vocab + v;
@@ -677,19 +847,17 @@ static hipError_t launch_rows(const SampleArgs& a, hipStream_t s) {
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((sample_collect_kernel<BF16, PIECES>), grid, dim3(kSampleThreads), 0, s, a);
   e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((sample_finish_kernel<BF16>), dim3((unsigned)a.rows), dim3(kFinishThreads), 0, s, a);
-  e = hipGetLastError();
   if (e != hipSuccess || !a.probs) return e;
-  const int per = 8 * kSampleThreads;
+  const int per = 8 * kWriteThreads;
   hipLaunchKernelGGL((sample_write_kernel<BF16>), dim3((unsigned)((a.vocab + per - 1) / per), (unsigned)a.rows),
-                     dim3(kSampleThreads), 0, s, a);
+                     dim3(kWriteThreads), 0, s, a);
   return hipGetLastError();
 }
 
 hipError_t launch_sample(const SampleArgs& a, bool bf16, hipStream_t s) {
   constexpr int WIDE = kSampleWide / (8 * kSampleThreads), NARROW = kSampleNarrow / (8 * kSampleThreads);
   if (a.entries == kSampleWide) return bf16 ? launch_rows<true, WIDE>(a, s) : launch_rows<false, WIDE>(a, s);
+  if (a.entries == kSampleWide / 2) return bf16 ? launch_rows<true, WIDE / 2>(a, s) : launch_rows<false, WIDE / 2>(a, s);
   return bf16 ? launch_rows<true, NARROW>(a, s) : launch_rows<false, NARROW>(a, s);
 }
 

@@ -83,11 +83,13 @@ ql_status check_matrix(const void* p, int64_t stride, int64_t width, int64_t tok
 // Entries of a vocabulary row that a workgroup takes: long slices, which leave
 // fewer histograms to add, where they still fill the card.
 int sample_entries(int64_t rows, int64_t vocab) {
-  return rows * ((vocab + qlk::kSampleWide - 1) / qlk::kSampleWide) >= 512 ? qlk::kSampleWide : qlk::kSampleNarrow;
+  int entries = qlk::kSampleWide;
+  while (entries > qlk::kSampleNarrow && rows * ((vocab + entries - 1) / entries) < 256) entries /= 2;
+  return entries;
 }
 
 struct SampleSpace {
-  int64_t slices, entries, hist, slice, state, best, found, cand, end;
+  int64_t slices, entries, hist, cand, best, state, top, count, end;
 };
 
 SampleSpace sample_space(int64_t rows, int64_t vocab) {
@@ -97,11 +99,11 @@ SampleSpace sample_space(int64_t rows, int64_t vocab) {
   const int64_t all = rows * s.slices;
   s.hist = 0;
   s.cand = s.hist + all * qlk::kSampleBuckets * 8;
-  s.best = s.cand + all * s.entries * 8;
-  s.slice = s.best + all * 8;
-  s.state = s.slice + all * (int64_t)sizeof(qlk::SampleSlice);
-  s.found = s.state + rows * (int64_t)sizeof(qlk::SampleRow);
-  s.end = (s.found + all * 4 + 15) / 16 * 16;
+  s.best = s.cand + rows * vocab * 8;
+  s.state = s.best + rows * 8;
+  s.top = s.state + rows * (int64_t)sizeof(qlk::SampleRow);
+  s.count = s.top + all * 4;
+  s.end = (s.count + rows * 8 + 15) / 16 * 16;
   return s;
 }
 
@@ -192,10 +194,10 @@ ql_status qlinear_sample(const ql_sampling* rules, int64_t rows, int64_t vocab, 
   a.logprobs = logprobs;
   a.probs = probs;
   a.hist = reinterpret_cast<uint64_t*>(base + w.hist);
-  a.slice = reinterpret_cast<qlk::SampleSlice*>(base + w.slice);
+  a.top = reinterpret_cast<float*>(base + w.top);
   a.state = reinterpret_cast<qlk::SampleRow*>(base + w.state);
   a.best = reinterpret_cast<uint64_t*>(base + w.best);
-  a.found = reinterpret_cast<int32_t*>(base + w.found);
+  a.count = reinterpret_cast<int32_t*>(base + w.count);
   a.cand = reinterpret_cast<uint64_t*>(base + w.cand);
   a.rows = (int)rows;
   a.vocab = (int)vocab;

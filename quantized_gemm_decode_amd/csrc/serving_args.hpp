@@ -29,29 +29,15 @@ struct LoraArgs {
   int ranges;              // of all slices together
 };
 
-// What a slice of a vocabulary row leaves for the others: its largest logit,
-// that one's bucket, and its entries' number and mass.
-struct SampleSlice {
-  float top;
-  int bucket;
-  uint64_t all;
-};
+constexpr int kSampleBuckets = 512;
+constexpr int kSampleWide = 16384, kSampleNarrow = 4096;   // entries of a slice
 
-// What is settled of a row before its candidates are looked at.
+// What the probabilities of a row need.
 struct SampleRow {
-  float top;               // largest logit; -inf: no entry
-  int bucket;              // its bucket
-  int lo, hi;              // buckets before lo are kept whole, those after hi are not; between them the candidates
-  int count;               // entries of the buckets before lo
-  int greedy;
-  uint64_t mass;           // and their mass
-  double rate;             // log2(e) / temperature
-  double limit;            // top-p: mass that ends the kept entries; of all, or with top-k of its entries' share
-  int top_k;               // 0: off
-  float top_p, min_p;      // 1, 0: off
-  // known at the end
+  double total;            // mass of the kept entries
   uint64_t least;          // smallest kept candidate
-  uint64_t total;          // mass of the kept entries
+  float top;               // largest logit; -inf: no entry
+  int lo, hi;              // buckets before lo are kept whole, those after hi are not
 };
 
 struct SampleArgs {
@@ -66,16 +52,13 @@ struct SampleArgs {
   float* logprobs;         // [rows] or null
   float* probs;            // [rows, vocab] or null
   uint64_t* hist;          // [rows, slices, kSampleBuckets]: entries (high bits) and their mass
-  SampleSlice* slice;      // [rows, slices]
+  float* top;              // [rows, slices]: a slice's largest logit
+  uint64_t* best;          // [rows]: best score among the surely kept entries
+  uint64_t* cand;          // [rows, vocab]: candidates
+  int32_t* count;          // [rows, 2]: candidates, and workgroups that are done
   SampleRow* state;        // [rows]
-  uint64_t* best;          // [rows, slices]: best score among a slice's surely kept entries
-  int32_t* found;          // [rows, slices]: candidates of a slice
-  uint64_t* cand;          // [rows, slices, entries]: they themselves
   int rows, vocab, slices, entries;
 };
-
-constexpr int kSampleBuckets = 256;
-constexpr int kSampleWide = 8192, kSampleNarrow = 2048;   // entries of a slice
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
 hipError_t launch_sample(const SampleArgs& a, bool bf16, hipStream_t s);
