@@ -9,13 +9,13 @@
 // Nothing is sorted.  What is kept is a head of the order, so only its border
 // has to be found: logits are put into buckets of an eighth of T on one grid
 // for the whole row, and a bucket's number and mass of entries say which one
-// the border lies in.  Two launches, a third for probabilities:
+// the border lies in.  Three launches, a fourth for probabilities:
 //   scan     a slice's entries in registers: its largest, and its histogram in
 //            LDS relative to that one (one atomic an entry: number and mass in
 //            one word);
 //   collect  adds a row's histograms, finds the border's bucket, draws among
-//            the entries before it and lists those in it (the candidates); the
-//            row's last workgroup finds the border among them and the token;
+//            the entries before it and lists those in it (the candidates);
+//   finish   one workgroup a row: the border among the candidates, the token;
 //   write    probabilities, where they are asked for.
 //
 // Whether an entry is kept depends on a sum over the whole row, and binary32
@@ -26,6 +26,8 @@
 // short series, times a factor of the bucket.
 #include "attention_common.hpp"
 #include "serving_args.hpp"
+
+#include <type_traits>
 
 namespace qlk {
 
@@ -157,23 +159,42 @@ __device__ __forceinline__ void load_logits(const SampleArgs& a, int row, int v,
 // Where a row has +inf, that is its only value: as 0 here.
 __device__ __forceinline__ float beside_inf(float l) { return l == -kNegInf ? 0.0f : kNegInf; }
 
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o, 64));
-  return v;
-}
-__device__ __forceinline__ uint64_t wave_max_key(uint64_t v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const uint64_t w = (uint64_t)__shfl_xor((unsigned long long)v, o, 64);
-    v = v > w ? v : w;
+// Reductions over a wave by lane shifts (v_mov_dpp: no trip to LDS), returned in
+// every lane; `none` is what lanes without a neighbour add.
+template <class T, class F>
+__device__ __forceinline__ T wave_reduce(T v, T none, F add) {
+  auto shifted = [&](auto ctrl, auto rows) {
+    constexpr int C = decltype(ctrl)::value, R = decltype(rows)::value;
+    if constexpr (sizeof(T) == 8) {
+      const uint64_t x = __builtin_bit_cast(uint64_t, v), o = __builtin_bit_cast(uint64_t, none);
+      const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp((int)(uint32_t)o, (int)(uint32_t)x, C, R, 0xf, false);
+      const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp((int)(o >> 32), (int)(x >> 32), C, R, 0xf, false);
+      v = add(v, __builtin_bit_cast(T, (uint64_t)hi << 32 | lo));
+    } else {
+      v = add(v, __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, v), C, R, 0xf, false)));
+    }
+  };
+  shifted(std::integral_constant<int, 0x111>(), std::integral_constant<int, 0xf>());   // row_shr 1, 2, 4, 8
+  shifted(std::integral_constant<int, 0x112>(), std::integral_constant<int, 0xf>());
+  shifted(std::integral_constant<int, 0x114>(), std::integral_constant<int, 0xf>());
+  shifted(std::integral_constant<int, 0x118>(), std::integral_constant<int, 0xf>());
+  shifted(std::integral_constant<int, 0x142>(), std::integral_constant<int, 0xa>());   // row_bcast 15 into rows 1 and 3
+  shifted(std::integral_constant<int, 0x143>(), std::integral_constant<int, 0xc>());   // row_bcast 31 into rows 2 and 3
+  if constexpr (sizeof(T) == 8) {
+    const uint64_t x = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(T, (uint64_t)(uint32_t)lane_i32((int)(x >> 32), 63) << 32 | (uint32_t)lane_i32((int)x, 63));
+  } else {
+    return __builtin_bit_cast(T, lane_i32(__builtin_bit_cast(int, v), 63));
   }
-  return v;
 }
+
+__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
+__device__ __forceinline__ float wave_max(float v) {
+  return wave_reduce(v, kNegInf, [](float a, float b) { return fmaxf(a, b); });
+}
+__device__ __forceinline__ uint64_t wave_max_key(uint64_t v) { return wave_reduce(v, uint64_t(0), max_u64); }
 __device__ __forceinline__ uint64_t wave_sum_u64(uint64_t v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += (uint64_t)__shfl_xor((unsigned long long)v, o, 64);
-  return v;
+  return wave_reduce(v, uint64_t(0), [](uint64_t a, uint64_t b) { return a + b; });
 }
 
 // A value that is the same in all lanes, as such (a scalar register).
@@ -183,8 +204,6 @@ __device__ __forceinline__ double uniform(double v) {
   const uint64_t u = (uint64_t)__double_as_longlong(v);
   return __longlong_as_double((long long)((uint64_t)(uint32_t)uniform((int)(u >> 32)) << 32 | (uint32_t)uniform((int)u)));
 }
-
-__device__ __forceinline__ uint64_t max_u64(uint64_t a, uint64_t b) { return a > b ? a : b; }
 
 // A score and its index as one word: the larger score, between equals the
 // lower index.
@@ -217,7 +236,7 @@ __global__ void __launch_bounds__(kSampleThreads) sample_scan_kernel(SampleArgs 
   if (t == 0) {
     a.top[(int64_t)row * a.slices + slice] = top;
     if (slice == 0) {
-      a.count[2 * row] = a.count[2 * row + 1] = 0;
+      a.count[row] = 0;
       a.best[row] = 0;
     }
   }
@@ -246,26 +265,14 @@ __global__ void __launch_bounds__(kSampleThreads) sample_scan_kernel(SampleArgs 
   a.hist[((int64_t)row * a.slices + slice) * kSampleBuckets + t] = sum;
 }
 
-// What a row's histograms say; the same in every thread of its workgroups.
-struct Settled {
-  float top;         // largest logit (0 where that is +inf); -inf: no entry
-  bool inf;
-  double line;       // the grid's line below it
-  int lo, hi;        // buckets before lo are kept whole, those after hi are not; between them the candidates
-  int count;         // entries of the buckets before lo
-  double mass;       // their mass, of the largest's
-  double unit;       // log2 of the weight that candidates' masses refer to: the middle of bucket lo
-  double all;        // mass of all entries
-  int k;             // top-k, 0: off or without effect
-};
-
 // Sums over the threads before this one, in their order.
 struct Before {
   int count;
   double mass;
 };
 
-__device__ __forceinline__ Settled settle_row(const SampleArgs& a, int row, const Rules& r) {
+// What a row's histograms say; the same in every thread of its workgroups.
+__device__ __forceinline__ SampleRow settle_row(const SampleArgs& a, int row, const Rules& r) {
   static_assert(kSampleThreads == kSampleBuckets, "a thread a bucket");
   constexpr int W = kSampleWaves, U = 10;
   __shared__ int shift[kSampleThreads];
@@ -275,7 +282,7 @@ __device__ __forceinline__ Settled settle_row(const SampleArgs& a, int row, cons
   __shared__ double k_mass[2], lo_mass;
   const int b = threadIdx.x, lane = b & 63, wave = b >> 6;
   const float* part = a.top + (int64_t)row * a.slices;
-  Settled s;
+  SampleRow s;
   float mine = b < a.slices ? part[b] : kNegInf, top = mine;
   for (int i = b + kSampleThreads; i < a.slices; i += kSampleThreads) top = fmaxf(top, part[i]);
   top = wave_max(top);
@@ -403,7 +410,7 @@ __device__ __forceinline__ double weight_of(float l, float top, double rate) {
 }
 // A candidate's mass, in steps of 2^-34 of the middle of the first candidates'
 // bucket: in that one the number that the histogram has.
-__device__ __forceinline__ uint64_t cand_mass(float l, const Settled& s, double grid) {
+__device__ __forceinline__ uint64_t cand_mass(float l, const SampleRow& s, double grid) {
   const double below = s.line - line_of(l, grid) - s.lo;
   const uint64_t m = mass_word(l, grid);
   return below == 0.0 ? m : (uint64_t)rint((double)m * exp2_of(-below * (0.125 * kLog2E)));
@@ -436,33 +443,102 @@ struct BestScore {
   }
 };
 
-// What a row's workgroups leave for its last one is stored and read at the
-// point that is coherent for all XCDs, so no write-back of an L2 is needed (a
-// fence by each of 1,216 workgroups took 190 us).
-template <class T>
-__device__ __forceinline__ void store_shared(T* p, T v) {
-  __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-template <class T>
-__device__ __forceinline__ T load_shared(const T* p) {
-  return __hip_atomic_load(const_cast<T*>(p), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+constexpr int kWaveList = 640;   // entries that a wave notes before it works on them: a piece's 512 and some more
+
+template <bool BF16, int PIECES>
+__global__ void __launch_bounds__(kSampleThreads, 6) sample_collect_kernel(SampleArgs a) {
+  constexpr int E = PIECES * 8 * kSampleThreads;
+  const int row = blockIdx.y, slice = blockIdx.x, first = slice * E, t = threadIdx.x, lane = t & 63;
+  // a wave's surely kept entries from the front, its candidates from the back
+  __shared__ uint64_t lists[kSampleWaves][kWaveList];
+  float x[8];
+  load_logits<BF16>(a, row, first + t * 8, x);
+  const Rules r = rules_of(a, row);
+  const SampleRow s = settle_row(a, row, r);
+  if (slice == 0 && t == 0) a.state[row] = s;
+  if (s.top == kNegInf) return;   // no entry at all
+  // (no buckets after the last one: the comparisons are with lines as they lie)
+  const double sure = s.lo == kSampleBuckets ? __builtin_huge_val() : s.lo;
+  const double maybe = s.hi == kSampleBuckets - 1 ? __builtin_huge_val() : s.hi;
+  uint64_t* list = lists[t >> 6];
+  int found[2] = {0, 0};   // entries of the wave's list
+  BestScore score;
+#pragma unroll 1
+  for (int i = 0; i < PIECES; ++i) {
+    const int v = first + (i * kSampleThreads + t) * 8;
+    unsigned bits[2] = {0, 0};
+    if (i) load_logits<BF16>(a, row, v, x);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      if (s.inf) x[j] = beside_inf(x[j]);
+      const double below = s.line - line_of(x[j], r.grid);
+      const bool there = x[j] > kNegInf;
+      bits[0] |= (unsigned)(there && below < sure) << j;
+      bits[1] |= (unsigned)(there && below >= sure && below <= maybe) << j;
+    }
+    const float* noise = a.noise + (int64_t)row * a.vocab;
+    // places in the list: sums over the lanes
+#pragma unroll
+    for (int kind = 0; kind < 2; ++kind) {
+      if (!__any(bits[kind] != 0)) continue;
+      const int n = __popc(bits[kind]), upto = inclusive_sum(n);
+      int at = found[kind] + upto - n;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        if (bits[kind] >> j & 1) {
+          list[kind ? kWaveList - 1 - at : at] = key_of(x[j], v + j);
+          ++at;
+        }
+      found[kind] += lane_i32(upto, 63);
+    }
+    const bool end = i + 1 == PIECES;
+    if (!end && found[0] + found[1] <= kWaveList - 512) continue;
+    // the candidates' place in the row's list; as a rule all of the wave's at the end
+    const bool flush = found[1] > 0 && (end || found[1] > 128);
+    int base = 0;
+    if (flush && lane == 0) base = atomicAdd(&a.count[row], found[1]);
+#pragma unroll 1
+    for (int k = 0; k < found[0]; k += 256) {
+      uint64_t key[4];
+      float e[4];
+      bool in[4];
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        in[u] = k + 64 * u + lane < found[0];
+        key[u] = list[min(k + 64 * u + lane, found[0] - 1)];
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) e[u] = noise[index_of(key[u])];
+      score.add(in, key, e, s.top, r.rate);
+    }
+    found[0] = 0;
+    if (flush) {
+      base = lane_i32(base, 0);
+#pragma unroll 1
+      for (int k = lane; k < found[1]; k += 64) a.cand[(int64_t)row * a.vocab + base + k] = list[kWaveList - 1 - k];
+      found[1] = 0;
+    }
+  }
+  const uint64_t best = wave_max_key(score.best);
+  if (lane == 0 && best) atomicMax(reinterpret_cast<unsigned long long*>(a.best + row), (unsigned long long)best);
 }
 
 constexpr int kFinishLast = 64;     // candidates that one wave orders by itself
 constexpr int kFinishParts = 256;   // parts that a range of candidates is counted into
 constexpr int kFinishCopies = 2;    // of the counts: lanes of equal parts add one after the other
-constexpr int kWaveList = 1024;     // entries that a wave notes before it works on them: a piece's 512 and as many more
-constexpr int kHeld = kSampleWaves * kWaveList;
+constexpr int kFinishThreads = 512;
+constexpr int kFinishWaves = kFinishThreads / 64;
+constexpr int kHeld = 16384;        // candidates that LDS holds
 
-// LDS of a workgroup of the second launch.
-struct CollectSpace {
-  uint64_t held[kHeld];   // waves' lists: surely kept entries from the front, candidates from the back; then the row's candidates
+struct FinishSpace {
+  uint64_t held[kHeld];
   unsigned long long mass[kFinishCopies][kFinishParts];
   unsigned count[kFinishCopies][kFinishParts];
-  unsigned long long keys[kFinishLast], own[kFinishLast];
-  uint64_t tops[kSampleWaves], sums[kSampleWaves];
+  unsigned long long keys[kFinishLast], own[kFinishLast], mat[kFinishLast];   // what is left: masses, and those before
+  int at[kFinishLast];
+  uint64_t tops[kFinishWaves], sums[kFinishWaves];
   uint64_t b_mass;
-  int b_count, part, listed, last;
+  int b_count, part, listed;
 };
 
 // f(keys, which are there) for the candidates of a row, four a lane at a time
@@ -476,17 +552,17 @@ __device__ __forceinline__ void each(const uint64_t* list, int n, uint64_t* held
     const int m = min(n - c0, kHeld);
     if (!loaded) {
       __syncthreads();
-#pragma unroll 8
-      for (int i = threadIdx.x; i < m; i += kSampleThreads) held[i] = load_shared(list + c0 + i);
+#pragma unroll 4
+      for (int i = threadIdx.x; i < m; i += kFinishThreads) held[i] = list[c0 + i];
       __syncthreads();
     }
 #pragma unroll 1
-    for (int i0 = 0; i0 < m; i0 += kEach * kSampleThreads) {
+    for (int i0 = 0; i0 < m; i0 += kEach * kFinishThreads) {
       uint64_t key[kEach];
       bool in[kEach];
 #pragma unroll
       for (int u = 0; u < kEach; ++u) {
-        const int i = i0 + u * kSampleThreads + (int)threadIdx.x;
+        const int i = i0 + u * kFinishThreads + (int)threadIdx.x;
         in[u] = i < m;
         key[u] = held[min(i, m - 1)];
       }
@@ -495,23 +571,32 @@ __device__ __forceinline__ void each(const uint64_t* list, int n, uint64_t* held
   }
 }
 
-// The token, by the row's last workgroup: everything that the others wrote is
-// there.  The border among the candidates is looked for by rank (top-k), then by
+// The token of row blockIdx.x.  The border among the candidates is looked for by rank (top-k), then by
 // mass (top-p): the last one that is kept has fewer than `most` of them before
 // it, or less than `limit` of their mass.  They are counted into parts of their
 // range, again within the part that the border lies in, until one wave orders
 // what is left.  (The code is run once a row, from a cold instruction cache: it
 // is kept short.  Unrolled to five times its length it took 2 to 3 times as long.)
 template <bool BF16>
-__device__ __forceinline__ void finish_row(const SampleArgs& a, int row, const Rules& r, const Settled& s, CollectSpace& sp) {
-  const int t = threadIdx.x, copy = t % kFinishCopies;
+__global__ void __launch_bounds__(kFinishThreads) sample_finish_kernel(SampleArgs a) {
+  __shared__ FinishSpace sp;
+  const int row = blockIdx.x, t = threadIdx.x, copy = t % kFinishCopies;
+  const SampleRow s = a.state[row];
+  if (s.top == kNegInf) {   // no entry at all
+    if (t == 0) {
+      a.tokens[row] = -1;
+      if (a.logprobs) a.logprobs[row] = kNegInf;
+    }
+    return;
+  }
+  const Rules r = rules_of(a, row);
   const uint64_t* list = a.cand + (int64_t)row * a.vocab;
-  const int n = load_shared(a.count + 2 * row);
-  uint64_t best = load_shared(a.best + row);
+  const int n = a.count[row];
+  uint64_t best = a.best[row];
   const bool held = n <= kHeld;
   if (held) {
-#pragma unroll 8
-    for (int i = t; i < n; i += kSampleThreads) sp.held[i] = load_shared(list + i);
+#pragma unroll 4
+    for (int i = t; i < n; i += kFinishThreads) sp.held[i] = list[i];
     __syncthreads();
   }
   const double step = exp2_of(s.unit) / kMassOne;   // of candidates' masses
@@ -630,19 +715,30 @@ __device__ __forceinline__ void finish_row(const SampleArgs& a, int row, const R
           if (there[u] && key[u] >= lo && key[u] <= hi) sp.keys[atomicAdd(&sp.listed, 1)] = key[u];
       });
     __syncthreads();
-    // every wave the same: an entry a lane
+    // an entry a lane in every wave, which compares with its share of the entries
     const int m = uniform(sp.listed), lane = t & 63;
     const uint64_t key = lane < m ? sp.keys[lane] : 0, mass = lane < m ? cand_mass(logit_of(key), s, r.grid) : 0;
-    if (t < 64) sp.own[lane] = mass;
-    __syncthreads();
-    int at = before;
-    uint64_t mat = before_mass;
-#pragma unroll 8
-    for (int j = 0; j < m; ++j) {
-      const bool ahead = sp.keys[j] > key;
-      at += ahead;
-      mat += ahead ? sp.own[j] : 0;
+    if (t < 64) {
+      sp.own[lane] = mass;
+      sp.mat[lane] = before_mass;
+      sp.at[lane] = before;
     }
+    __syncthreads();
+    int ahead = 0;
+    uint64_t ahead_mass = 0;
+#pragma unroll 2
+    for (int j = t >> 6; j < m; j += kFinishWaves) {
+      const bool first = sp.keys[j] > key;
+      ahead += first;
+      ahead_mass += first ? sp.own[j] : 0;
+    }
+    if (ahead) {
+      atomicAdd(&sp.at[lane], ahead);
+      atomicAdd(&sp.mat[lane], (unsigned long long)ahead_mass);
+    }
+    __syncthreads();
+    const int at = sp.at[lane];
+    const uint64_t mat = sp.mat[lane];
     const bool kept = lane < m && (by_mass ? (double)mat < limit : at < most);
     const uint64_t last = ~wave_max_key(kept ? ~key : 0);   // the smallest kept key; none: all ones
     upto = wave_max_key(kept ? mat + mass : before_mass);
@@ -679,7 +775,7 @@ __device__ __forceinline__ void finish_row(const SampleArgs& a, int row, const R
   }
   __syncthreads();
   if (t == 0) {
-    for (int i = 1; i < kSampleWaves; ++i) {
+    for (int i = 1; i < kFinishWaves; ++i) {
       best = sp.tops[i] > best ? sp.tops[i] : best;
       sum += sp.sums[i];
     }
@@ -691,117 +787,9 @@ __device__ __forceinline__ void finish_row(const SampleArgs& a, int row, const R
       const float l = BF16 ? bf16_to_f32(static_cast<const uint16_t*>(a.logits)[at]) : static_cast<const float*>(a.logits)[at];
       a.logprobs[row] = (float)log(weight_of(s.inf ? 0.0f : l, s.top, r.rate) / total);
     }
-    if (a.probs) a.state[row] = SampleRow{total, least, s.inf ? -kNegInf : s.top, s.lo, s.hi};
+    a.state[row].total = total;
+    a.state[row].least = least;
   }
-}
-
-template <bool BF16, int PIECES>
-__global__ void __launch_bounds__(kSampleThreads, 4) sample_collect_kernel(SampleArgs a) {
-  constexpr int E = PIECES * 8 * kSampleThreads;
-  const int row = blockIdx.y, slice = blockIdx.x, first = slice * E, t = threadIdx.x, lane = t & 63;
-  __shared__ CollectSpace sp;
-  float x[8];
-  load_logits<BF16>(a, row, first + t * 8, x);
-  const Rules r = rules_of(a, row);
-  const Settled s = settle_row(a, row, r);
-  if (s.top == kNegInf) {   // no entry at all
-    if (slice == 0 && t == 0) {
-      a.tokens[row] = -1;
-      if (a.logprobs) a.logprobs[row] = kNegInf;
-      if (a.probs) a.state[row].top = kNegInf;
-    }
-    return;
-  }
-  // (no buckets after the last one: the comparisons are with lines as they lie)
-  const double sure = s.lo == kSampleBuckets ? __builtin_huge_val() : s.lo;
-  const double maybe = s.hi == kSampleBuckets - 1 ? __builtin_huge_val() : s.hi;
-  uint64_t* list = sp.held + (t >> 6) * kWaveList;
-  int found[2] = {0, 0};   // entries of the wave's list
-  BestScore score;
-#pragma unroll 1
-  for (int i = 0; i < PIECES; ++i) {
-    const int v = first + (i * kSampleThreads + t) * 8;
-    unsigned bits[2] = {0, 0};
-    float now[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      now[j] = s.inf ? beside_inf(x[j]) : x[j];
-      const double below = s.line - line_of(now[j], r.grid);
-      const bool there = now[j] > kNegInf;
-      bits[0] |= (unsigned)(there && below < sure) << j;
-      bits[1] |= (unsigned)(there && below >= sure && below <= maybe) << j;
-    }
-    if (i + 1 < PIECES) load_logits<BF16>(a, row, v + 8 * kSampleThreads, x);
-    const float* noise = a.noise + (int64_t)row * a.vocab;
-    // all of the wave's are kept: without the list
-    if (__all(bits[0] == 0xffu)) {
-      const f32x4u* p = reinterpret_cast<const f32x4u*>(noise + v);
-      const f32x4u e[2] = {p[0], p[1]};
-      const bool in[4] = {true, true, true, true};
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint64_t key[4];
-        float y[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          key[u] = key_of(now[4 * h + u], v + 4 * h + u);
-          y[u] = e[h][u];
-        }
-        score.add(in, key, y, s.top, r.rate);
-      }
-      bits[0] = 0;
-    }
-    // places in the list: sums over the lanes
-#pragma unroll
-    for (int kind = 0; kind < 2; ++kind) {
-      if (!__any(bits[kind] != 0)) continue;
-      const int n = __popc(bits[kind]), upto = inclusive_sum(n);
-      int at = found[kind] + upto - n;
-#pragma unroll
-      for (int j = 0; j < 8; ++j)
-        if (bits[kind] >> j & 1) {
-          list[kind ? kWaveList - 1 - at : at] = key_of(now[j], v + j);
-          ++at;
-        }
-      found[kind] += lane_i32(upto, 63);
-    }
-    const bool end = i + 1 == PIECES;
-    if (!end && found[0] + found[1] <= kWaveList - 512) continue;
-    // the candidates' place in the row's list; as a rule all of the wave's at the end
-    const bool flush = found[1] > 0 && (end || found[1] > 128);
-    int base = 0;
-    if (flush && lane == 0) base = atomicAdd(&a.count[2 * row], found[1]);
-#pragma unroll 1
-    for (int k = 0; k < found[0]; k += 256) {
-      uint64_t key[4];
-      float e[4];
-      bool in[4];
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        in[u] = k + 64 * u + lane < found[0];
-        key[u] = list[min(k + 64 * u + lane, found[0] - 1)];
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) e[u] = noise[index_of(key[u])];
-      score.add(in, key, e, s.top, r.rate);
-    }
-    found[0] = 0;
-    if (flush) {
-      base = lane_i32(base, 0);
-#pragma unroll 1
-      for (int k = lane; k < found[1]; k += 64) store_shared(a.cand + (int64_t)row * a.vocab + base + k, list[kWaveList - 1 - k]);
-      found[1] = 0;
-    }
-  }
-  const uint64_t best = wave_max_key(score.best);
-  if (lane == 0 && best) atomicMax(reinterpret_cast<unsigned long long*>(a.best + row), (unsigned long long)best);
-  // the last of the row's workgroups goes on
-  __builtin_amdgcn_s_waitcnt(0);
-  __syncthreads();
-  if (t == 0) sp.last = atomicAdd(&a.count[2 * row + 1], 1) == a.slices - 1;
-  __syncthreads();
-  if (!sp.last) return;
-  finish_row<BF16>(a, row, r, s, sp);
 }
 
 constexpr int kWriteThreads = 256;
@@ -813,20 +801,18 @@ __global__ void __launch_bounds__(kWriteThreads) sample_write_kernel(SampleArgs 
   if (v >= a.vocab) return;
   const SampleRow s = a.state[row];
   const Rules r = rules_of(a, row);
-  const bool inf = s.top == -kNegInf;
-  const float top = inf ? 0.0f : s.top;
-  const double line = line_of(top, r.grid), per = 1.0 / s.total;
+  const double per = 1.0 / s.total;
   float x[8], p[8];
   load_logits<BF16>(a, row, v, x);
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     p[j] = 0.0f;
-    if (inf) x[j] = beside_inf(x[j]);
+    if (s.inf) x[j] = beside_inf(x[j]);
     if (!(x[j] > kNegInf)) continue;
-    const double below = line - line_of(x[j], r.grid);
+    const double below = s.line - line_of(x[j], r.grid);
     const bool in = below < s.lo || s.lo == kSampleBuckets;
     if (in || ((below <= s.hi || s.hi == kSampleBuckets - 1) && key_of(x[j], v + j) >= s.least)) {
-      const double w = weight_of(x[j], top, r.rate);
+      const double w = weight_of(x[j], s.top, r.rate);
       if (in || w >= (double)r.m) p[j] = (float)(w * per);
     }
   }
@@ -846,6 +832,9 @@ static hipError_t launch_rows(const SampleArgs& a, hipStream_t s) {
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL((sample_collect_kernel<BF16, PIECES>), grid, dim3(kSampleThreads), 0, s, a);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL((sample_finish_kernel<BF16>), dim3((unsigned)a.rows), dim3(kFinishThreads), 0, s, a);
   e = hipGetLastError();
   if (e != hipSuccess || !a.probs) return e;
   const int per = 8 * kWriteThreads;

@@ -103,7 +103,7 @@ SampleSpace sample_space(int64_t rows, int64_t vocab) {
   s.state = s.best + rows * 8;
   s.top = s.state + rows * (int64_t)sizeof(qlk::SampleRow);
   s.count = s.top + all * 4;
-  s.end = (s.count + rows * 8 + 15) / 16 * 16;
+  s.end = (s.count + rows * 4 + 15) / 16 * 16;
   return s;
 }
 

@@ -32,12 +32,19 @@ struct LoraArgs {
 constexpr int kSampleBuckets = 512;
 constexpr int kSampleWide = 16384, kSampleNarrow = 4096;   // entries of a slice
 
-// What the probabilities of a row need.
+// What a row's histograms say of it, and what is kept at last.
 struct SampleRow {
-  double total;            // mass of the kept entries
-  uint64_t least;          // smallest kept candidate
-  float top;               // largest logit; -inf: no entry
-  int lo, hi;              // buckets before lo are kept whole, those after hi are not
+  double line;       // the grid's line below the largest logit
+  double mass;       // of the buckets before lo, of the largest's weight
+  double unit;       // log2 of the weight that candidates' masses refer to: the middle of bucket lo
+  double all;        // mass of all entries
+  double total;      // of the kept ones
+  uint64_t least;    // smallest kept candidate
+  float top;         // largest logit (0 where that is +inf); -inf: no entry
+  int inf;
+  int lo, hi;        // buckets before lo are kept whole, those after hi are not; between them the candidates
+  int count;         // entries of the buckets before lo
+  int k;             // top-k, 0: off or without effect
 };
 
 struct SampleArgs {
@@ -55,7 +62,7 @@ struct SampleArgs {
   float* top;              // [rows, slices]: a slice's largest logit
   uint64_t* best;          // [rows]: best score among the surely kept entries
   uint64_t* cand;          // [rows, vocab]: candidates
-  int32_t* count;          // [rows, 2]: candidates, and workgroups that are done
+  int32_t* count;          // [rows]: candidates
   SampleRow* state;        // [rows]
   int rows, vocab, slices, entries;
 };
