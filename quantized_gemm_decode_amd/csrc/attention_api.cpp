@@ -25,7 +25,9 @@ struct Part {
   int row_blocks, splits, chunk, units;  // tile kernel
   bool by_rows;
   int slots, heads_wg, most;             // stream kernel; most rows of its sequences
+  int shares;                            // trees: workgroups that their keys are cut for at most
   int64_t o_at, ml_at, end;              // partial outputs, their maxima and sums, in the workspace (bytes)
+  int64_t cut_at;                        // trees: how the keys were cut
 };
 
 }  // namespace
@@ -226,6 +228,35 @@ ql_status plan_tile(const ql_attention_shape& s, int64_t rows, int64_t at, Part*
   return QL_OK;
 }
 
+// The tile kernel for trees: its workgroups cut the keys by the lengths they
+// find (see tree_cut), as the stream kernel's do; the plan fixes how many there
+// can be.  With more than 512 sequences, or contexts of at most two tiles, a unit
+// is never cut.
+ql_status plan_tree(const ql_attention_shape& s, int64_t rows, Part* p) {
+  const int64_t group = s.q_heads / s.kv_heads, R = kTileRows;
+  const int64_t blocks = (rows + R - 1) / R;
+  const int64_t units = std::min(s.batch * blocks, s.tokens * group / R + s.batch) * s.kv_heads;
+  const int64_t slots = qlk::attn_tile_slots(s.head_dim);
+  const bool cut = s.batch <= 512 && s.max_kv > 128;
+  const int64_t shares = cut ? (4 * units + 5 * slots - 1) / (4 * slots) * slots : units;
+  if (s.tokens * s.q_heads >= (int64_t(1) << 31)) return fail(QL_E_UNSUPPORTED, "tokens * q_heads exceeds 2^31");
+  if (shares >= kMaxWorkgroups || s.tokens * s.q_heads / 4 + s.kv_heads >= kMaxWorkgroups)
+    return fail(QL_E_UNSUPPORTED, "2^24 workgroups or more");
+  p->used = true;
+  p->rows = (int)R;
+  p->row_blocks = (int)blocks;
+  p->splits = cut ? 2 : 1;
+  p->chunk = 1 << 30;
+  p->units = (int)units;
+  p->by_rows = s.tokens * group / R + s.batch < s.batch * blocks;
+  p->shares = (int)shares;
+  const int64_t parts = cut ? shares * R : 0;
+  p->ml_at = parts * s.head_dim * 4;
+  p->cut_at = p->ml_at + parts * 2 * 4;
+  p->end = p->cut_at + (cut ? (s.batch * 8 + 15) / 16 * 16 : 0);
+  return QL_OK;
+}
+
 // The stream kernel for sequences of at most `rows` rows: the shares of the
 // keys are cut on the device, the plan fixes how many there can be.
 ql_status plan_stream(const ql_attention_shape& s, int64_t rows, Part* p) {
@@ -288,10 +319,11 @@ ql_status new_plan(const ql_attention_shape* s, bool tree, ql_attention_plan* ou
   // (1,024 and 31 x 3,000) 116 and 227; 4 M (512 and 63 x 8,000) 491 and 974.
   const int64_t few = max_q > 0 ? s->batch - (s->tokens + max_q - 1) / max_q : 0;
   // (More query heads a KV head than that launch takes rows: none would go there.)
-  const bool mixed = chunks && group <= kMixedRows && few * s->kv_heads * tile_span(*s) > 160000;
+  // (Trees are of a size as a rule, and their units cut by what is there.)
+  const bool mixed = chunks && !tree && group <= kMixedRows && few * s->kv_heads * tile_span(*s) > 160000;
   p->tile_from = mixed ? kMixedRows + 1 : 0;
   if (!chunks || mixed) st = plan_stream(*s, mixed ? kMixedRows : rows, &p->stream);
-  if (st == QL_OK && chunks) st = plan_tile(*s, rows, p->stream.end, &p->tile);
+  if (st == QL_OK && chunks) st = tree ? plan_tree(*s, rows, &p->tile) : plan_tile(*s, rows, p->stream.end, &p->tile);
   if (st != QL_OK) {
     delete p;
     return st;
@@ -373,6 +405,8 @@ ql_status run_plan(ql_attention_plan p, const ql_rows* q, const ql_kv_cache* cac
     a.splits = x.splits;
     a.chunk = x.chunk;
     a.min_rows = p->tile_from;
+    a.shares = x.shares;
+    a.cut = workspace ? reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + x.cut_at) : nullptr;
     e = qlk::launch_attn_tile(a, s.head_dim, e4m3, x.units, hs);
     if (e == hipSuccess && x.splits > 1) e = qlk::launch_attn_join(a, s.head_dim, x.rows, hs);
   }

@@ -58,6 +58,9 @@ struct AttnArgs {
   int by_rows;           // numbering of the units (see unit_at)
   int splits, chunk;     // most chunks of keys of a unit, and their length
   int min_rows;          // sequences with fewer rows are left to the stream kernel
+  // trees: the keys are cut on the device (see tree_cut)
+  int32_t* cut;          // [batch, 2]: a sequence's first share (of one KV head), shares of a unit
+  int shares;            // workgroups there are at most
   // stream kernel
   int slots;             // shares that all sequences' keys are cut into, for each KV head
   int heads_wg;          // KV heads of a workgroup (1, 2 or 4); its other waves take other slots
@@ -126,6 +129,8 @@ hipError_t launch_attn_stream(const AttnArgs& a, int head_dim, bool e4m3, int ro
 hipError_t launch_attn_stream_join(const AttnArgs& a, int head_dim, int rows, int most_rows, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, bool e4m3, int units, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, hipStream_t s);
+// Workgroups of the tile kernel that the card holds at once.
+int attn_tile_slots(int head_dim);
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);
 hipError_t launch_tree_commit(const CommitArgs& a, hipStream_t s);
 

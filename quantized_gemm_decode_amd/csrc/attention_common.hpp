@@ -173,6 +173,74 @@ __device__ __forceinline__ Unit unit_at(const AttnArgs& a, int n, int R) {
   return unit_of(a, s, blocks - 1 - (n - start(s.b, s.first)), R);
 }
 
+// Trees: the units' keys are cut by the lengths found, into the fewest equal
+// shares that keep every workgroup the card holds busy once (or for more units than
+// that, twice): `chunk` keys or fewer of a unit each.  A host's bound of the
+// lengths would leave the card idle behind the longest ones (16 sequences of 515
+// .. 4,099 keys, 32 nodes of 32 / 8 heads: 54 us so cut, 33 by the lengths).
+struct TreeCut {
+  int chunk;
+};
+
+__device__ __forceinline__ int tree_blocks(const Sequence& s, int group, int R) { return ((s.end - s.first) * group + R - 1) / R; }
+
+// Sequence b as this lane's own; none beyond the batch.
+__device__ __forceinline__ Sequence tree_sequence(const AttnArgs& a, int b) {
+  if (b >= a.batch) return Sequence{-1, 0, 0, 0};
+  const int q0 = min(max(a.cu_q[b], 0), a.tokens), q1 = min(max(a.cu_q[b + 1], q0), a.tokens);
+  return Sequence{b, q0, q1, min(max(a.seq_lens[b], 0), a.max_kv)};
+}
+
+__device__ __forceinline__ int tree_shares(int len, int chunk) { return max(1, (int)(((int64_t)len + chunk - 1) / chunk)); }
+
+__device__ __forceinline__ TreeCut tree_cut(const AttnArgs& a, int R, int slots) {
+  const int lane = threadIdx.x & 63;
+  const Sequence mine = tree_sequence(a, lane);
+  // shares of one KV head with chunks of c keys
+  auto count = [&](int c) {
+    int n = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+      const Sequence s = b0 ? tree_sequence(a, b0 + lane) : mine;
+      n += lane_i32(inclusive_sum(min(tree_blocks(s, a.group, R), a.row_blocks) * tree_shares(s.len, c)), 63);
+    }
+    return n;
+  };
+  const int units = count(INT32_MAX) * a.kv_heads;
+  const int most = (4 * units + 5 * slots - 1) / (4 * slots) * slots / a.kv_heads;   // units / slots + 1/4, rounded up
+  int lo = 2, hi = max(2, (a.max_kv + 63) / 64);   // of 64 keys
+  while (lo < hi) {
+    const int mid = (lo + hi) / 2;
+    if (count(mid * 64) <= most)
+      hi = mid;
+    else
+      lo = mid + 1;
+  }
+  return TreeCut{lo * 64};
+}
+
+// Share n of one KV head: its unit, the share of the unit's keys and their number.
+__device__ __forceinline__ Unit tree_unit(const AttnArgs& a, const TreeCut& cut, int n, int R, int* share, int* shares) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    const Sequence s = tree_sequence(a, b0 + lane);
+    const int each = tree_shares(s.len, cut.chunk);
+    const int upto = before + inclusive_sum(min(tree_blocks(s, a.group, R), a.row_blocks) * each);
+    const uint64_t past = __ballot(upto > n);
+    if (past) {
+      const int i = __ffsll((unsigned long long)past) - 1;
+      const Sequence own = {b0 + i, lane_i32(s.first, i), lane_i32(s.end, i), lane_i32(s.len, i)};
+      *shares = lane_i32(each, i);
+      const int at = n - (i ? lane_i32(upto, i - 1) : before);
+      *share = at % *shares;
+      return unit_of(a, own, at / *shares, R);
+    }
+    before = lane_i32(upto, 63);
+  }
+  Unit none{};
+  return none;
+}
+
 // Where the partial results of one row over chunk `split` lie: rows of all
 // tokens, for each chunk and KV head.
 __device__ __forceinline__ int64_t part_at(const AttnArgs& a, int h, int split, int row) {

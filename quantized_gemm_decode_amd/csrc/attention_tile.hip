@@ -295,6 +295,22 @@ __device__ __forceinline__ void inner_step(const uint8_t* kl, int kt, const uint
 // with two; 8 chunks of 512 at 2,000, bf16: 96 and 102 us.)
 constexpr int tile_workgroups(int D) { return D == 64 ? 3 : 2; }
 
+// How the keys of trees were cut, for the join.
+__device__ __forceinline__ void tell_cut(const AttnArgs& a, const TreeCut& cut) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    const Sequence s = tree_sequence(a, b0 + lane);
+    const int each = tree_shares(s.len, cut.chunk), all = min(tree_blocks(s, a.group, kTileRows), a.row_blocks) * each;
+    const int upto = before + inclusive_sum(all);
+    if (threadIdx.x < 64 && s.b >= 0) {
+      a.cut[2 * s.b] = upto - all;
+      a.cut[2 * s.b + 1] = each;
+    }
+    before = lane_i32(upto, 63);
+  }
+}
+
 template <int D, bool E4M3, bool TREE>
 __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile_kernel(AttnArgs a) {
   constexpr int R = kTileRows, DT = D / 32, KS = D / 16;
@@ -306,12 +322,30 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
   int id = blockIdx.x;
   const int h = id % a.kv_heads;
   id /= a.kv_heads;
-  const int split = id % a.splits;
-  const Unit u = unit_at(a, id / a.splits, R);
-  if (u.rows == 0) return;
-  if (u.chunks == 0 ? split != 0 : split >= u.chunks) return;
-  const int begin = (u.lo & ~63) + split * a.chunk;
-  const int end = min(u.hi, begin + a.chunk);
+  int split, chunk, chunks;
+  Unit u;
+  if constexpr (TREE) {
+    split = 0;
+    chunks = 1;
+    if (a.splits > 1) {
+      const TreeCut cut = tree_cut(a, R, 256 * tile_workgroups(D));
+      if (blockIdx.x == 0) tell_cut(a, cut);
+      u = tree_unit(a, cut, id, R, &split, &chunks);
+    } else {
+      u = unit_at(a, id, R);
+    }
+    if (u.rows == 0) return;
+    chunk = ((u.len + chunks - 1) / chunks + 63) / 64 * 64;   // the shares as equal as whole tiles are
+  } else {
+    split = id % a.splits;
+    u = unit_at(a, id / a.splits, R);
+    if (u.rows == 0) return;
+    if (u.chunks == 0 ? split != 0 : split >= u.chunks) return;
+    chunk = a.chunk;
+    chunks = u.chunks;
+  }
+  const int begin = (u.lo & ~63) + split * chunk;
+  const int end = min(u.hi, begin + chunk);
   const int tiles = end > begin ? (end - begin + kTileKeys - 1) / kTileKeys : 0;
 
   // this lane's row, and what follows from it, is worked out again where it is
@@ -503,7 +537,7 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
   place = u.row0 + row;
   const int tok = u.first + place / a.group, head = h * a.group + place % a.group;
   const float v_scale = E4M3 && a.vc.scale ? a.vc.scale[h] : 1.0f;
-  if (u.chunks <= 1) {
+  if (chunks <= 1) {
     const float inv = sum > 0.0f || sum != sum ? v_scale / sum : 0.0f;  // a row that saw no key is zero
     uint8_t* out = a.out.p + (int64_t)tok * a.out.token + (int64_t)head * a.out.head + g * 8;
 #pragma unroll
@@ -517,7 +551,7 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
     if (a.lse && g == 0)
       a.lse[(int64_t)tok * a.q_heads + head] = lse_of(w.m, sum);
   } else {
-    const int64_t part = part_at(a, h, split, u.first * a.group + place);
+    const int64_t part = TREE ? (int64_t)blockIdx.x * R + row : part_at(a, h, split, u.first * a.group + place);
     float* out = a.part_o + part * D + 4 * g;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
@@ -538,11 +572,13 @@ template <int D, bool E4M3>
 static hipError_t launch_tile(const AttnArgs& a, int units, hipStream_t s) {
   const dim3 grid((unsigned)units * (unsigned)a.splits), threads(kTileWaves * 64);
   if (a.sees)
-    hipLaunchKernelGGL((attn_tile_kernel<D, E4M3, true>), grid, threads, 0, s, a);
+    hipLaunchKernelGGL((attn_tile_kernel<D, E4M3, true>), dim3((unsigned)a.shares), threads, 0, s, a);
   else
     hipLaunchKernelGGL((attn_tile_kernel<D, E4M3, false>), grid, threads, 0, s, a);
   return hipGetLastError();
 }
+
+int attn_tile_slots(int head_dim) { return 256 * tile_workgroups(head_dim); }
 
 hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, bool e4m3, int units, hipStream_t s) {
   if (head_dim == 64) return e4m3 ? launch_tile<64, true>(a, units, s) : launch_tile<64, false>(a, units, s);

@@ -121,7 +121,7 @@ def test_bounds_may_be_loose(max_q, max_kv, words):
 @pytest.mark.parametrize("new", [[8, 3], [40, 33]])
 def test_a_chain_is_causal_attention(new):
     """Nodes in a row, each seeing those before it: the same bits as qlinear_attention's."""
-    p = Tree(11, new, [300, 90], 8, 2, 128, 16, False)
+    p = Tree(11, new, [120, 90], 8, 2, 128, 16, False)      # (short enough that both are cut alike)
     p.dev_sees = torch.cat([torch.tensor([(1 << (i + 1)) - 1 for i in range(n)]) for n in new])[:, None].cuda()
     out, ls = p.run(p.plan())
     want, want_ls = Problem.run(p, Problem.plan(p))
@@ -147,6 +147,30 @@ def test_nonfinite_keys_and_values_stay_with_the_rows_that_see_them(new, kv, D, 
     p.k.view(nan.dtype)[page, place, :, 5] = nan
     got, _ = p.run(p.plan())
     assert torch.equal(got[~sees], want[~sees]) and torch.isnan(got[sees]).all()
+
+
+@pytest.mark.parametrize("batch,nodes,kv,D,hq,hk", [(70, 34, 260, 64, 4, 1), (9, 40, 3000, 128, 8, 2), (3, 200, 900, 64, 4, 4),
+                                                    (40, 36, 700, 128, 16, 4), (520, 33, 140, 64, 2, 2)])
+def test_many_trees(batch, nodes, kv, D, hq, hk):
+    """More sequences than lanes, keys cut into many shares, more units than the card holds, batches that are not cut."""
+    new = [(nodes, 1, nodes // 2, 0, nodes - 1)[i % 5] for i in range(batch)]
+    p = Tree(60 + batch, new, [nodes + (i * 7919) % kv for i in range(batch)], hq, hk, D, 16, False)
+    out, ls = p.run(p.plan())
+    p.check(out, ls)
+
+
+def test_cu_q_that_is_none_stays_inside():
+    """Sequences that overlap or run backwards: some rows are computed, nothing outside out is written."""
+    p = Tree(4, [40] * 8, [900] * 8, 8, 2, 128, 16, False)
+    want, _ = p.run(p.plan())
+    plan = p.plan()
+    wide = torch.full((p.T + 2, 8, 128), 9.0, dtype=BF16, device="cuda")
+    cu = torch.tensor([0, 320, 0, 320, -5, 10 ** 6, 7, 320, 320], dtype=torch.int32, device="cuda")
+    ws = plan.new_workspace()
+    ql.qlinear_tree_attention(plan, p.q, p.cache, p.table.cuda(), p.lens.cuda(), cu, p.dev_sees, wide[1:-1], workspace=ws)
+    torch.cuda.synchronize()
+    assert (wide[0] == 9).all() and (wide[-1] == 9).all()
+    assert torch.equal(p.run(plan)[0], want)
 
 
 def test_tree_attention_replays():
