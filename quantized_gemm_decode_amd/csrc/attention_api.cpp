@@ -250,9 +250,8 @@ ql_status plan_tree(const ql_attention_shape& s, int64_t rows, Part* p) {
   p->units = (int)units;
   p->by_rows = s.tokens * group / R + s.batch < s.batch * blocks;
   p->shares = (int)shares;
-  const int64_t parts = cut ? shares * R : 0;
-  p->ml_at = parts * s.head_dim * 4;
-  p->cut_at = p->ml_at + parts * 2 * 4;
+  // pairs of binary32 values of 256 lanes: half a row's outputs each, its maximum and sum
+  p->cut_at = cut ? shares * 256 * 8 * (s.head_dim / 4 + 1) : 0;
   p->end = p->cut_at + (cut ? (s.batch * 8 + 15) / 16 * 16 : 0);
   return QL_OK;
 }
@@ -408,7 +407,8 @@ ql_status run_plan(ql_attention_plan p, const ql_rows* q, const ql_kv_cache* cac
     a.shares = x.shares;
     a.cut = workspace ? reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + x.cut_at) : nullptr;
     e = qlk::launch_attn_tile(a, s.head_dim, e4m3, x.units, hs);
-    if (e == hipSuccess && x.splits > 1) e = qlk::launch_attn_join(a, s.head_dim, x.rows, hs);
+    if (e == hipSuccess && x.splits > 1)
+      e = p->tree ? qlk::launch_attn_tree_join(a, s.head_dim, x.units, hs) : qlk::launch_attn_join(a, s.head_dim, x.rows, hs);
   }
   return e == hipSuccess ? QL_OK : hip_fail(e, "attention launch");
 }

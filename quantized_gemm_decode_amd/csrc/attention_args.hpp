@@ -46,7 +46,8 @@ struct AttnArgs {
   const int32_t* cu_q;
   float* lse;            // [tokens, q_heads] or null
   float* part_o;         // partial outputs of head_dim values a row: [kv_heads, splits, tokens * group] rows of
-                         // the tile kernel, [slots, 2, kv_heads, R] rows of the stream kernel
+                         // the tile kernel, [slots, 2, kv_heads, R] rows of the stream kernel (trees: [shares, waves,
+                         // registers and one of maxima and sums, lanes] pairs)
   float* part_ml;        // their rows' maxima (base 2) and sums
   uint64_t page_magic;
   const uint64_t* sees;  // trees of drafts: [tokens, words] new tokens of its sequence that a token sees, one a bit
@@ -129,6 +130,7 @@ hipError_t launch_attn_stream(const AttnArgs& a, int head_dim, bool e4m3, int ro
 hipError_t launch_attn_stream_join(const AttnArgs& a, int head_dim, int rows, int most_rows, hipStream_t s);
 hipError_t launch_attn_tile(const AttnArgs& a, int head_dim, bool e4m3, int units, hipStream_t s);
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, hipStream_t s);
+hipError_t launch_attn_tree_join(const AttnArgs& a, int head_dim, int units, hipStream_t s);
 // Workgroups of the tile kernel that the card holds at once.
 int attn_tile_slots(int head_dim);
 hipError_t launch_verify(const VerifyArgs& a, hipStream_t s);

@@ -173,16 +173,18 @@ __device__ __forceinline__ Unit unit_at(const AttnArgs& a, int n, int R) {
   return unit_of(a, s, blocks - 1 - (n - start(s.b, s.first)), R);
 }
 
-// Trees: the units' keys are cut by the lengths found, into the fewest equal
-// shares that keep every workgroup the card holds busy once (or for more units than
-// that, twice): `chunk` keys or fewer of a unit each.  A host's bound of the
-// lengths would leave the card idle behind the longest ones (16 sequences of 515
-// .. 4,099 keys, 32 nodes of 32 / 8 heads: 54 us so cut, 33 by the lengths).
+// Trees: the units' keys are cut by the lengths found, into equal shares of a
+// unit that are as many as the card takes at once (or for more units than that, a
+// multiple).  A host's bound of the lengths would leave the card idle behind the
+// longest ones (16 sequences of 515 .. 4,099 keys, 32 nodes of 32 / 8 heads: 54 us so
+// cut, @).
 struct TreeCut {
-  int chunk;
+  float per_key;   // shares a key
 };
 
-__device__ __forceinline__ int tree_blocks(const Sequence& s, int group, int R) { return ((s.end - s.first) * group + R - 1) / R; }
+__device__ __forceinline__ int tree_blocks(const AttnArgs& a, const Sequence& s, int R) {
+  return min(((s.end - s.first) * a.group + R - 1) / R, a.row_blocks);
+}
 
 // Sequence b as this lane's own; none beyond the batch.
 __device__ __forceinline__ Sequence tree_sequence(const AttnArgs& a, int b) {
@@ -191,51 +193,84 @@ __device__ __forceinline__ Sequence tree_sequence(const AttnArgs& a, int b) {
   return Sequence{b, q0, q1, min(max(a.seq_lens[b], 0), a.max_kv)};
 }
 
-__device__ __forceinline__ int tree_shares(int len, int chunk) { return max(1, (int)(((int64_t)len + chunk - 1) / chunk)); }
+// Shares of a unit.  (Rounding of the product only moves a border between counts.)
+__device__ __forceinline__ int tree_shares(int len, const TreeCut& cut) { return max(1, (int)ceilf((float)len * cut.per_key)); }
 
-__device__ __forceinline__ TreeCut tree_cut(const AttnArgs& a, int R, int slots) {
+__device__ __forceinline__ TreeCut tree_cut(const AttnArgs& a, const Sequence& mine, int R, int slots) {
   const int lane = threadIdx.x & 63;
-  const Sequence mine = tree_sequence(a, lane);
-  // shares of one KV head with chunks of c keys
+  int units = 0;       // of one KV head
+  float keys = 0.0f;   // and theirs
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
+    const Sequence s = b0 ? tree_sequence(a, b0 + lane) : mine;
+    const int blocks = tree_blocks(a, s, R);
+    units += lane_i32(inclusive_sum(blocks), 63);
+    keys += (float)lane_i32(inclusive_sum((int)min((int64_t)blocks * ((s.len + 63) >> 6), (int64_t)1 << 24)), 63) * 64.0f;
+  }
+  const int most = (4 * units * a.kv_heads + 5 * slots - 1) / (4 * slots) * slots / a.kv_heads;   // units / slots + 1/4, rounded up
+  // shares of one KV head with chunks of 64 c keys are between keys / 64 c and that plus the units
   auto count = [&](int c) {
+    const TreeCut cut = {1.0f / (float)(64 * c)};
     int n = 0;
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
       const Sequence s = b0 ? tree_sequence(a, b0 + lane) : mine;
-      n += lane_i32(inclusive_sum(min(tree_blocks(s, a.group, R), a.row_blocks) * tree_shares(s.len, c)), 63);
+      n += lane_i32(inclusive_sum(tree_blocks(a, s, R) * tree_shares(s.len, cut)), 63);
     }
     return n;
   };
-  const int units = count(INT32_MAX) * a.kv_heads;
-  const int most = (4 * units + 5 * slots - 1) / (4 * slots) * slots / a.kv_heads;   // units / slots + 1/4, rounded up
-  int lo = 2, hi = max(2, (a.max_kv + 63) / 64);   // of 64 keys
+  const int longest = (a.max_kv + 63) / 64;
+  int lo = max(2, (int)(keys / (float)(64 * most))), hi = max(lo, longest);
+  if (most > units) hi = min(hi, max(lo, (int)(keys / (float)(64 * (most - units))) + 1));
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
-    if (count(mid * 64) <= most)
+    if (count(mid) <= most)
       hi = mid;
     else
       lo = mid + 1;
   }
-  return TreeCut{lo * 64};
+  return TreeCut{1.0f / (float)(64 * lo)};
+}
+
+// The shares of this lane's sequence, and those before them (of one KV head).  Up
+// to 64 sequences: by falling length of a share, so that the last ones to start
+// are the short ones (32 sequences of 1,021 .. 8,190 keys, 33 .. 64 nodes of 40 / 8
+// heads, E4M3, 1,024 shares: 188 us in the sequences' order).
+struct TreeShares {
+  int each, all, before;   // of a unit, of all its units
+};
+__device__ __forceinline__ TreeShares tree_shares_of(const AttnArgs& a, const TreeCut& cut, const Sequence& s, int R, int before) {
+  TreeShares t;
+  t.each = tree_shares(s.len, cut);
+  t.all = tree_blocks(a, s, R) * t.each;
+  t.before = before + inclusive_sum(t.all) - t.all;
+  if (a.batch <= 64) {
+    const int lane = threadIdx.x & 63, size = s.len / t.each;
+    t.before = 0;
+    for (int j = 0; j < a.batch; ++j) {
+      const int other = lane_i32(size, j), n = lane_i32(t.all, j);
+      t.before += other > size || (other == size && j < lane) ? n : 0;
+    }
+  }
+  return t;
 }
 
 // Share n of one KV head: its unit, the share of the unit's keys and their number.
-__device__ __forceinline__ Unit tree_unit(const AttnArgs& a, const TreeCut& cut, int n, int R, int* share, int* shares) {
+__device__ __forceinline__ Unit tree_unit(const AttnArgs& a, const TreeCut& cut, const Sequence& mine, int n, int R, int* share,
+                                         int* shares) {
   const int lane = threadIdx.x & 63;
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    const Sequence s = tree_sequence(a, b0 + lane);
-    const int each = tree_shares(s.len, cut.chunk);
-    const int upto = before + inclusive_sum(min(tree_blocks(s, a.group, R), a.row_blocks) * each);
-    const uint64_t past = __ballot(upto > n);
-    if (past) {
-      const int i = __ffsll((unsigned long long)past) - 1;
+    const Sequence s = b0 ? tree_sequence(a, b0 + lane) : mine;
+    const TreeShares t = tree_shares_of(a, cut, s, R, before);
+    const uint64_t here = __ballot(n >= t.before && n - t.before < t.all);
+    if (here) {
+      const int i = __ffsll((unsigned long long)here) - 1;
       const Sequence own = {b0 + i, lane_i32(s.first, i), lane_i32(s.end, i), lane_i32(s.len, i)};
-      *shares = lane_i32(each, i);
-      const int at = n - (i ? lane_i32(upto, i - 1) : before);
+      *shares = lane_i32(t.each, i);
+      const int at = n - lane_i32(t.before, i);
       *share = at % *shares;
       return unit_of(a, own, at / *shares, R);
     }
-    before = lane_i32(upto, 63);
+    before = lane_i32(t.before + t.all, 63);
   }
   Unit none{};
   return none;

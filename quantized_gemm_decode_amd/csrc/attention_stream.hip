@@ -571,23 +571,13 @@ __global__ void __launch_bounds__(kJoinWaves * 64) attn_stream_join_kernel(AttnA
 
 // The tile kernel's units that were cut into chunks: one wave a row of a KV
 // head (new token, query head of the group).
-template <int D, bool TREE>
+template <int D>
 __global__ void __launch_bounds__(kJoinWaves * 64) attn_join_kernel(AttnArgs a, int R) {
   const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int h = (int)blockIdx.x % a.kv_heads, at = (int)blockIdx.x / a.kv_heads * kJoinWaves + wave;
   if (at >= a.tokens * a.group) return;
   const Sequence s = sequence_at(a, at, [&](int, int q0) { return q0 * a.group; });
   const int row = at - s.first * a.group;  // of the sequence
-  if constexpr (TREE) {
-    if (s.b < 0 || row >= (s.end - s.first) * a.group || row / R >= a.row_blocks) return;
-    const int shares = uniform_i32(a.cut + 2 * s.b + 1), before = uniform_i32(a.cut + 2 * s.b) + row / R * shares;
-    // (a cu_q that is none may name more shares than there are)
-    if (shares <= 1 || (int64_t)(before + shares) * a.kv_heads > a.shares) return;
-    const int64_t first = ((int64_t)before * a.kv_heads + h) * R + row % R;
-    const int64_t step = (int64_t)a.kv_heads * R;
-    join_row<D, 1>(a, first, first + step, step, shares, at / a.group, h * a.group + at % a.group);
-    return;
-  }
   const Unit u = unit_of(a, s, row / R, R);
   if (row - u.row0 >= u.rows || u.chunks <= 1) return;
   const int64_t first = part_at(a, h, 0, at), step = (int64_t)a.tokens * a.group;
@@ -645,20 +635,12 @@ hipError_t launch_attn_stream_join(const AttnArgs& a, int head_dim, int rows, in
   return hipGetLastError();
 }
 
-template <int D>
-static void launch_join(const AttnArgs& a, int rows, hipStream_t s) {
-  const dim3 grid((unsigned)((a.tokens * a.group + kJoinWaves - 1) / kJoinWaves) * (unsigned)a.kv_heads);
-  if (a.sees)
-    hipLaunchKernelGGL((attn_join_kernel<D, true>), grid, dim3(kJoinWaves * 64), 0, s, a, rows);
-  else
-    hipLaunchKernelGGL((attn_join_kernel<D, false>), grid, dim3(kJoinWaves * 64), 0, s, a, rows);
-}
-
 hipError_t launch_attn_join(const AttnArgs& a, int head_dim, int rows, hipStream_t s) {
+  const unsigned grid = (unsigned)((a.tokens * a.group + kJoinWaves - 1) / kJoinWaves) * (unsigned)a.kv_heads;
   if (head_dim == 64)
-    launch_join<64>(a, rows, s);
+    hipLaunchKernelGGL((attn_join_kernel<64>), dim3(grid), dim3(kJoinWaves * 64), 0, s, a, rows);
   else
-    launch_join<128>(a, rows, s);
+    hipLaunchKernelGGL((attn_join_kernel<128>), dim3(grid), dim3(kJoinWaves * 64), 0, s, a, rows);
   return hipGetLastError();
 }
 

@@ -105,6 +105,37 @@ __device__ __forceinline__ void load_v(const AttnArgs& a, const Groups& at, int 
     t->x[j] = *reinterpret_cast<const u32x4*>(v + j * (Staged<D, E4M3>::RP * (int)a.vc.token) + lane);
 }
 
+// The same rows straight into LDS, without registers (bf16: nothing to
+// convert): 16 bytes a lane from row + off, to `to` and the lanes' places behind
+// it.  Lanes load the pieces that their places hold.  The caller waits for it.
+__device__ __forceinline__ void load_to_lds(const uint8_t* row, uint32_t off, const uint8_t* to) {
+  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)to);
+  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(row) : "memory");
+}
+template <int D>
+__device__ __forceinline__ void fetch_k(const AttnArgs& a, const Groups& at, int i, uint8_t* kl) {
+  using S = Staged<D, false>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const uint8_t* k = a.kc.p + pick(at.k_lo, at.k_hi, i);
+#pragma unroll
+  for (int j = 0; j < S::PASSES; ++j) {
+    const int row = j * S::RP + lane / S::CH;
+    load_to_lds(k, (uint32_t)(row * (int)a.kc.token + k_piece<D>(row, lane % S::CH) * 16), kl + (wave * 16 + j * S::RP) * D * 2);
+  }
+}
+template <int D>
+__device__ __forceinline__ void fetch_v(const AttnArgs& a, const Groups& at, int i, uint8_t* vl) {
+  using S = Staged<D, false>;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const uint8_t* v = a.vc.p + pick(at.v_lo, at.v_hi, i);
+#pragma unroll
+  for (int j = 0; j < S::PASSES; ++j) {
+    const int row = j * S::RP + lane / S::CH, c = lane % S::CH;
+    load_to_lds(v, (uint32_t)(row * (int)a.vc.token + (v_block<D>(row, c / 4) * 4 + c % 4) * 16),
+                vl + (wave * 16 + j * S::RP) * D * 2);
+  }
+}
+
 // 16 E4M3 codes as two pieces of bf16.
 __device__ __forceinline__ void widen(const u32x4& c, u32x4* lo, u32x4* hi) {
   *lo = u32x4{e4m3_to_bf16<false>(c.x), e4m3_to_bf16<true>(c.x), e4m3_to_bf16<false>(c.y), e4m3_to_bf16<true>(c.y)};
@@ -301,13 +332,12 @@ __device__ __forceinline__ void tell_cut(const AttnArgs& a, const TreeCut& cut) 
   int before = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
     const Sequence s = tree_sequence(a, b0 + lane);
-    const int each = tree_shares(s.len, cut.chunk), all = min(tree_blocks(s, a.group, kTileRows), a.row_blocks) * each;
-    const int upto = before + inclusive_sum(all);
+    const TreeShares t = tree_shares_of(a, cut, s, kTileRows, before);
     if (threadIdx.x < 64 && s.b >= 0) {
-      a.cut[2 * s.b] = upto - all;
-      a.cut[2 * s.b + 1] = each;
+      a.cut[2 * s.b] = t.before;
+      a.cut[2 * s.b + 1] = t.each;
     }
-    before = lane_i32(upto, 63);
+    before = lane_i32(t.before + t.all, 63);
   }
 }
 
@@ -328,9 +358,10 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
     split = 0;
     chunks = 1;
     if (a.splits > 1) {
-      const TreeCut cut = tree_cut(a, R, 256 * tile_workgroups(D));
+      const Sequence mine = tree_sequence(a, lane);
+      const TreeCut cut = tree_cut(a, mine, R, 256 * tile_workgroups(D));
       if (blockIdx.x == 0) tell_cut(a, cut);
-      u = tree_unit(a, cut, id, R, &split, &chunks);
+      u = tree_unit(a, cut, mine, id, R, &split, &chunks);
     } else {
       u = unit_at(a, id, R);
     }
@@ -475,24 +506,40 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
     // step T: scores of tile T + 1, weights of keys 32 .. 95 and sums over
     // keys 0 .. 63 of tile T; meanwhile K of tile T + 2 and V of tile T + 1
     // come in, one after the other through the same registers
+    // Trees stream long contexts past few rows: both come in at once, from the
+    // start of the step on, bf16 straight into LDS (16 sequences of 515 .. 4,099
+    // keys, 32 nodes of 32 / 8 heads: 45 us one after the other)
     auto step = [&](int T, auto hidden) {
-      constexpr bool HIDDEN = decltype(hidden)::value;
+      constexpr bool HIDDEN = decltype(hidden)::value, FETCH = TREE && D == 128 && !E4M3 && !HIDDEN;
       const int key = begin + T * kTileKeys;
       const uint8_t* kl = k_lds[(T + 1) & 1];
       const uint8_t* vl = v_lds[T & 1];
-      load_v<D, E4M3>(a, at, (T + 1) & 63, v_lane, &staged);
+      if constexpr (FETCH) {
+        fetch_v<D>(a, at, (T + 1) & 63, v_lds[(T + 1) & 1]);
+        if (T + 2 < tiles) {
+          if (((T + 2) & 63) == 0) at = groups_at(a, table, h, ((key + 2 * kTileKeys) >> 4) + wave + 4 * lane, last_sub);
+          fetch_k<D>(a, at, (T + 2) & 63, k_lds[T & 1]);
+        }
+      } else {
+        load_v<D, E4M3>(a, at, (T + 1) & 63, v_lane, &staged);
+      }
       if (HIDDEN) mask(s1, key + 32);
       refer(s1, vl, 0, p0);
       inner_step<D>(kl, 0, vl, 0, q, s1, &w, p0, o, &s0, p1);
-      store_v<D, E4M3>(staged, key + kTileKeys, u.len, v_lds[(T + 1) & 1], HIDDEN && part(T + 1), &dropped);
-      if (T + 2 < tiles) {
-        if (((T + 2) & 63) == 0) at = groups_at(a, table, h, ((key + 2 * kTileKeys) >> 4) + wave + 4 * lane, last_sub);
-        load_k<D, E4M3>(a, at, (T + 2) & 63, k_lane, &staged);
+      if constexpr (!FETCH) {
+        store_v<D, E4M3>(staged, key + kTileKeys, u.len, v_lds[(T + 1) & 1], HIDDEN && part(T + 1), &dropped);
+        if (T + 2 < tiles) {
+          if (((T + 2) & 63) == 0) at = groups_at(a, table, h, ((key + 2 * kTileKeys) >> 4) + wave + 4 * lane, last_sub);
+          load_k<D, E4M3>(a, at, (T + 2) & 63, k_lane, &staged);
+        }
       }
       if (HIDDEN) mask(s0, key + kTileKeys);
       refer(s0, vl, 1, p1);
       inner_step<D>(kl, 1, vl, 1, q, s0, &w, p1, o, &s1, p0);
-      if (T + 2 < tiles) store_k<D, E4M3>(staged, k_lds[T & 1]);
+      if constexpr (FETCH)
+        __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt 0: this wave's share has arrived
+      else if (T + 2 < tiles)
+        store_k<D, E4M3>(staged, k_lds[T & 1]);
       lds_barrier();
     };
     // tiles [first, last) are seen whole; a loop each, for the hidden ones' work
@@ -551,7 +598,22 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
     if (a.lse && g == 0)
       a.lse[(int64_t)tok * a.q_heads + head] = lse_of(w.m, sum);
   } else {
-    const int64_t part = TREE ? (int64_t)blockIdx.x * R + row : part_at(a, h, split, u.first * a.group + place);
+    if constexpr (TREE) {
+      // as the registers lie, for the join's lanes to read in the same way.  Written through (at the point that is
+      // coherent for all XCDs): left in the L2s, it waits for the kernel's end to be written back, 0.35 us a MB
+      uint64_t* out = reinterpret_cast<uint64_t*>(a.part_o) + ((int64_t)blockIdx.x * kTileWaves + wave) * (DT * 8 + 1) * 64 + lane;
+      auto put = [&](int i, float x, float y) {
+        __hip_atomic_store(out + i * 64, (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x), __ATOMIC_RELAXED,
+                           __HIP_MEMORY_SCOPE_AGENT);
+      };
+      put(0, w.m, sum);
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) put(1 + dt * 8 + i, o[dt][2 * i] * v_scale, o[dt][2 * i + 1] * v_scale);
+      return;
+    }
+    const int64_t part = part_at(a, h, split, u.first * a.group + place);
     float* out = a.part_o + part * D + 4 * g;
 #pragma unroll
     for (int dt = 0; dt < DT; ++dt)
@@ -566,6 +628,69 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
       a.part_ml[part * 2 + 1] = sum;
     }
   }
+}
+
+// Joins the shares of a tree's units.  grid.x: units of all KV heads, as unit_at
+// numbers them; grid.y: 32 of the values.  A lane has the row and the values that
+// it had in the tile kernel, and adds its shares in their order.
+template <int D>
+__global__ void __launch_bounds__(kTileWaves * 64) attn_tree_join_kernel(AttnArgs a) {
+  constexpr int R = kTileRows, DT = D / 32;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), dt = blockIdx.y;
+  const int h = (int)blockIdx.x % a.kv_heads;
+  const Unit u = unit_at(a, (int)blockIdx.x / a.kv_heads, R);
+  if (u.rows == 0) return;
+  const int shares = uniform_i32(a.cut + 2 * u.b + 1), before = uniform_i32(a.cut + 2 * u.b) + u.row0 / R * shares;
+  // (a cu_q that is none may name more shares than there are)
+  if (shares <= 1 || (int64_t)(before + shares) * a.kv_heads > a.shares) return;
+  const int row = wave * 32 + (lane & 31), place = u.row0 + row;
+  if (row >= u.rows) return;
+  constexpr int64_t wide = (DT * 8 + 1) * 64;
+  const uint64_t* p = reinterpret_cast<const uint64_t*>(a.part_o) + (((int64_t)before * a.kv_heads + h) * kTileWaves + wave) * wide + lane;
+  const int64_t step = (int64_t)a.kv_heads * kTileWaves * wide;
+  float m = kNegInf, l = 0.0f, x[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) x[i] = 0.0f;
+  for (int c = 0; c < shares; c += 4) {
+    uint64_t ml[4], y[4][8];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint64_t* q = p + min(c + k, shares - 1) * step;
+      ml[k] = q[0];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[k][i] = q[(1 + dt * 8 + i) * 64];
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (c + k >= shares) continue;
+      const float m2 = __uint_as_float((uint32_t)ml[k]), l2 = __uint_as_float((uint32_t)(ml[k] >> 32));
+      const float top = fmaxf(m, m2), base = top == kNegInf ? 0.0f : top;
+      const float e = __builtin_amdgcn_exp2f(m - base), e2 = __builtin_amdgcn_exp2f(m2 - base);
+      m = top;
+      l = l * e + l2 * e2;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x[2 * i] = x[2 * i] * e + __uint_as_float((uint32_t)y[k][i]) * e2;
+        x[2 * i + 1] = x[2 * i + 1] * e + __uint_as_float((uint32_t)(y[k][i] >> 32)) * e2;
+      }
+    }
+  }
+  const int tok = u.first + place / a.group, head = h * a.group + place % a.group;
+  const float inv = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+  uint8_t* out = a.out.p + (int64_t)tok * a.out.token + (int64_t)head * a.out.head + (32 * dt + 4 * (lane >> 5)) * 2;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    *reinterpret_cast<u32x2*>(out + 16 * i) =
+        u32x2{bf16_pair(x[4 * i] * inv, x[4 * i + 1] * inv), bf16_pair(x[4 * i + 2] * inv, x[4 * i + 3] * inv)};
+  if (a.lse && dt == 0 && lane < 32) a.lse[(int64_t)tok * a.q_heads + head] = lse_of(m, l);
+}
+
+hipError_t launch_attn_tree_join(const AttnArgs& a, int head_dim, int units, hipStream_t s) {
+  if (head_dim == 64)
+    hipLaunchKernelGGL((attn_tree_join_kernel<64>), dim3((unsigned)units, 2), dim3(kTileWaves * 64), 0, s, a);
+  else
+    hipLaunchKernelGGL((attn_tree_join_kernel<128>), dim3((unsigned)units, 4), dim3(kTileWaves * 64), 0, s, a);
+  return hipGetLastError();
 }
 
 template <int D, bool E4M3>

@@ -141,15 +141,16 @@ def test_tree_attention_refusals():
     plan = ql.qlinear_tree_attention_plan(c, 32, 2, 200, 100, 8000)
     f = plan.facts
     assert f["tile_rows"] == 128 and f["stream_rows"] == 0 and plan._words == 2
-    # two workgroups a compute unit, each with a binary32 output, maximum and sum of 128 rows; where the keys were cut
-    assert f["workspace_bytes"] == 512 * 128 * 130 * 4 + 16
+    # two workgroups a compute unit, each with the binary32 outputs of 128 rows in 256 lanes, a maximum and sum for each
+    # lane; where the keys were cut
+    assert f["workspace_bytes"] == 512 * (128 * 128 + 2 * 256) * 4 + 16
     few = ql.qlinear_tree_attention_plan(c, 32, 2, 16, 8, 8000)
     assert few.facts["stream_rows"] == 32 and few.facts["tile_rows"] == 0
     # contexts of two tiles, or more sequences than are cut: no join
     assert ql.qlinear_tree_attention_plan(c, 32, 2, 200, 100, 128).workspace_bytes == 0
     assert ql.qlinear_tree_attention_plan(c, 32, 513, 51300, 100, 8000).workspace_bytes == 0
     wide = ql.qlinear_tree_attention_plan(c, 32, 64, 64 * 33, 33, 8000).facts       # 130 * 8 units: three times 512
-    assert wide["workspace_bytes"] == 3 * 512 * 128 * 130 * 4 + 64 * 8
+    assert wide["workspace_bytes"] == 3 * 512 * (128 * 128 + 2 * 256) * 4 + 64 * 8
     with pytest.raises(ValueError, match="GPU"):
         ql.qlinear_tree_attention(plan, k, c, k, k, k, k, k)
 
