@@ -180,6 +180,7 @@ __device__ __forceinline__ Unit unit_at(const AttnArgs& a, int n, int R) {
 // cut, @).
 struct TreeCut {
   float per_key;   // shares a key
+  bool rounds;     // more of them than the card takes at once
 };
 
 __device__ __forceinline__ int tree_blocks(const AttnArgs& a, const Sequence& s, int R) {
@@ -200,6 +201,7 @@ __device__ __forceinline__ TreeCut tree_cut(const AttnArgs& a, const Sequence& m
   const int lane = threadIdx.x & 63;
   int units = 0;       // of one KV head
   float keys = 0.0f;   // and theirs
+#pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
     const Sequence s = b0 ? tree_sequence(a, b0 + lane) : mine;
     const int blocks = tree_blocks(a, s, R);
@@ -209,9 +211,10 @@ __device__ __forceinline__ TreeCut tree_cut(const AttnArgs& a, const Sequence& m
   const int most = (4 * units * a.kv_heads + 5 * slots - 1) / (4 * slots) * slots / a.kv_heads;   // units / slots + 1/4, rounded up
   // shares of one KV head with chunks of 64 c keys are between keys / 64 c and that plus the units
   auto count = [&](int c) {
-    const TreeCut cut = {1.0f / (float)(64 * c)};
+    const TreeCut cut = {1.0f / (float)(64 * c), false};
     int n = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 64) {
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.batch; b0 += 64) {
       const Sequence s = b0 ? tree_sequence(a, b0 + lane) : mine;
       n += lane_i32(inclusive_sum(tree_blocks(a, s, R) * tree_shares(s.len, cut)), 63);
     }
@@ -220,6 +223,7 @@ __device__ __forceinline__ TreeCut tree_cut(const AttnArgs& a, const Sequence& m
   const int longest = (a.max_kv + 63) / 64;
   int lo = max(2, (int)(keys / (float)(64 * most))), hi = max(lo, longest);
   if (most > units) hi = min(hi, max(lo, (int)(keys / (float)(64 * (most - units))) + 1));
+#pragma unroll 1
   while (lo < hi) {
     const int mid = (lo + hi) / 2;
     if (count(mid) <= most)
@@ -227,11 +231,11 @@ __device__ __forceinline__ TreeCut tree_cut(const AttnArgs& a, const Sequence& m
     else
       lo = mid + 1;
   }
-  return TreeCut{1.0f / (float)(64 * lo)};
+  return TreeCut{1.0f / (float)(64 * lo), most * a.kv_heads > slots};
 }
 
-// The shares of this lane's sequence, and those before them (of one KV head).  Up
-// to 64 sequences: by falling length of a share, so that the last ones to start
+// The shares of this lane's sequence, and those before them (of one KV head).  Where
+// they start one after the other: by falling length of a share, so that the last ones to start
 // are the short ones (32 sequences of 1,021 .. 8,190 keys, 33 .. 64 nodes of 40 / 8
 // heads, E4M3, 1,024 shares: 188 us in the sequences' order).
 struct TreeShares {
@@ -242,9 +246,10 @@ __device__ __forceinline__ TreeShares tree_shares_of(const AttnArgs& a, const Tr
   t.each = tree_shares(s.len, cut);
   t.all = tree_blocks(a, s, R) * t.each;
   t.before = before + inclusive_sum(t.all) - t.all;
-  if (a.batch <= 64) {
+  if (cut.rounds && a.batch <= 64) {
     const int lane = threadIdx.x & 63, size = s.len / t.each;
     t.before = 0;
+#pragma unroll 1
     for (int j = 0; j < a.batch; ++j) {
       const int other = lane_i32(size, j), n = lane_i32(t.all, j);
       t.before += other > size || (other == size && j < lane) ? n : 0;
@@ -258,6 +263,7 @@ __device__ __forceinline__ Unit tree_unit(const AttnArgs& a, const TreeCut& cut,
                                          int* shares) {
   const int lane = threadIdx.x & 63;
   int before = 0;
+#pragma unroll 1
   for (int b0 = 0; b0 < a.batch; b0 += 64) {
     const Sequence s = b0 ? tree_sequence(a, b0 + lane) : mine;
     const TreeShares t = tree_shares_of(a, cut, s, R, before);

@@ -635,7 +635,7 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
 // it had in the tile kernel, and adds its shares in their order.
 template <int D>
 __global__ void __launch_bounds__(kTileWaves * 64) attn_tree_join_kernel(AttnArgs a) {
-  constexpr int R = kTileRows, DT = D / 32;
+  constexpr int R = kTileRows, DT = D / 32, kAtOnce = 8;   // shares on their way
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6), dt = blockIdx.y;
   const int h = (int)blockIdx.x % a.kv_heads;
   const Unit u = unit_at(a, (int)blockIdx.x / a.kv_heads, R);
@@ -651,18 +651,19 @@ __global__ void __launch_bounds__(kTileWaves * 64) attn_tree_join_kernel(AttnArg
   float m = kNegInf, l = 0.0f, x[16];
 #pragma unroll
   for (int i = 0; i < 16; ++i) x[i] = 0.0f;
-  for (int c = 0; c < shares; c += 4) {
-    uint64_t ml[4], y[4][8];
+  for (int c = 0; c < shares; c += kAtOnce) {
+    uint64_t ml[kAtOnce], y[kAtOnce][8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const uint64_t* q = p + min(c + k, shares - 1) * step;
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (c + k >= shares) break;
+      const uint64_t* q = p + (c + k) * step;
       ml[k] = q[0];
 #pragma unroll
       for (int i = 0; i < 8; ++i) y[k][i] = q[(1 + dt * 8 + i) * 64];
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if (c + k >= shares) continue;
+    for (int k = 0; k < kAtOnce; ++k) {
+      if (c + k >= shares) break;
       const float m2 = __uint_as_float((uint32_t)ml[k]), l2 = __uint_as_float((uint32_t)(ml[k] >> 32));
       const float top = fmaxf(m, m2), base = top == kNegInf ? 0.0f : top;
       const float e = __builtin_amdgcn_exp2f(m - base), e2 = __builtin_amdgcn_exp2f(m2 - base);
