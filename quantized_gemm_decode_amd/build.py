@@ -37,8 +37,10 @@ HIPCC_FLAGS = [
     "-Wno-unused-command-line-argument",
 ]
 # matrix products into vector registers: the decode attention, one workgroup a
-# compute unit, otherwise copies its sums to and from accumulation registers
-EXTRA_FLAGS = {"attention_stream.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
+# compute unit, otherwise copies its sums to and from accumulation registers; the
+# adapters' second product adds each of its sums to an element at once
+EXTRA_FLAGS = {"attention_stream.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"],
+               "lora.hip": ["-mllvm", "-amdgpu-mfma-vgpr-form=1"]}
 
 
 def hipcc():

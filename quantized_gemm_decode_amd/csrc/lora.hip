@@ -37,15 +37,15 @@ __device__ __forceinline__ int lane_adapter(const LoraArgs& a, int block, uint64
 }
 
 // Calls f(adapter, mask of its tokens, first of its tile) for the tiles number
-// slot, slot + slots, ... of the lanes of `left`: up to 16 tokens of one adapter.
+// slot, slot + slots, ... of the lanes of `left`: up to `size` tokens of one adapter.
 template <class F>
-__device__ __forceinline__ void for_tiles(int mine, uint64_t left, int slot, int slots, F f) {
+__device__ __forceinline__ void for_tiles(int mine, uint64_t left, int size, int slot, int slots, F f) {
   for (int n = 0; left;) {
     const int i = lane_i32(mine, __ffsll((unsigned long long)left) - 1);
     const uint64_t same = __ballot(mine == i) & left;
     left &= ~same;
-    const int end = n + (__popcll(same) + 15) / 16;
-    for (; slot < end; slot += slots) f(i, same, (slot - n) * 16);
+    const int end = n + (__popcll(same) + size - 1) / size;
+    for (; slot < end; slot += slots) f(i, same, (slot - n) * size);
     n = end;
   }
 }
@@ -58,11 +58,11 @@ __device__ __forceinline__ int nth_lane(uint64_t mask) {
   return __builtin_amdgcn_ds_permute(at * 4, lane);
 }
 
-// h of tiles of tokens, one chunk of K, TW tiles of 16 ranks: four waves a
+// h of tiles of 16 NT tokens, one chunk of K, TW tiles of 16 ranks: four waves a
 // quarter of the chunk each.
-template <int TW>
+template <int NT, int TW>
 __global__ void __launch_bounds__(kLoraWaves * 64) lora_down_kernel(LoraArgs a) {
-  __shared__ f32x4 sums[kLoraWaves][TW][64];
+  __shared__ f32x4 sums[kLoraWaves][NT * TW][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   const int rows = a.slices * a.rank, groups = (rows + 63) / 64;
@@ -71,32 +71,42 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_down_kernel(LoraArgs a) 
   id /= a.chunks;
   const int row0 = id % groups * 64;
   id /= groups;
-  const int slot = id % a.slots, block = id / a.slots;
+  const int slot = id % a.down_slots, block = id / a.down_slots;
   uint64_t there;
   const int mine = lane_adapter(a, block, &there);
   const int k0 = chunk * a.chunk + wave * (a.chunk / kLoraWaves), k1 = min(a.k, k0 + a.chunk / kLoraWaves);
-  for_tiles(mine, there, slot, a.slots, [&](int i, uint64_t mask, int c0) {
+  for_tiles(mine, there, 16 * NT, slot, a.down_slots, [&](int i, uint64_t mask, int c0) {
     if (i < 0) return;
-    const int n = __popcll(mask), tok = block * kLoraBlock + __shfl(nth_lane(mask), min(c0 + r, n - 1), 64);
-    const uint8_t* wp[TW];
+    const int n = __popcll(mask), order = nth_lane(mask);
+    int tok[NT];
+    const uint8_t *wp[TW], *xp[NT];
 #pragma unroll
     for (int v = 0; v < TW; ++v)
       wp[v] = a.a + i * a.a_step + (int64_t)min(row0 + 16 * v + r, rows - 1) * a.k * 2 + g * 32;
-    const uint8_t* xp = a.x + tok * a.x_row + g * 32;
-    f32x4 h[TW];
 #pragma unroll
-    for (int v = 0; v < TW; ++v) h[v] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int u = 0; u < NT; ++u) {
+      tok[u] = block * kLoraBlock + __shfl(order, min(c0 + 16 * u + r, n - 1), 64);
+      xp[u] = a.x + tok[u] * a.x_row + g * 32;
+    }
+    f32x4 h[NT][TW];
+#pragma unroll
+    for (int u = 0; u < NT; ++u)
+#pragma unroll
+      for (int v = 0; v < TW; ++v) h[u][v] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     // 64 values of K a step, 16 a lane: whole 128-byte lines of a row
     auto step = [&](int k, bool tail) {
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
         const bool in = !tail || k + 16 * g + 8 * half < k1;
         const u32x4 zero = {0u, 0u, 0u, 0u};
-        const u32x4 x = in ? *reinterpret_cast<const u32x4*>(xp + (int64_t)k * 2 + half * 16) : zero;
+        u32x4 x[NT];
+#pragma unroll
+        for (int u = 0; u < NT; ++u) x[u] = in ? *reinterpret_cast<const u32x4*>(xp[u] + (int64_t)k * 2 + half * 16) : zero;
 #pragma unroll
         for (int v = 0; v < TW; ++v) {
           const u32x4 w = in ? *reinterpret_cast<const u32x4*>(wp[v] + (int64_t)k * 2 + half * 16) : zero;
-          h[v] = mma_bf16(w, x, h[v]);
+#pragma unroll
+          for (int u = 0; u < NT; ++u) h[u][v] = mma_bf16(w, x[u], h[u][v]);
         }
       }
     };
@@ -105,15 +115,21 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_down_kernel(LoraArgs a) 
     for (; k + 64 <= k1; k += 64) step(k, false);
     if (k < k1) step(k, true);
 #pragma unroll
-    for (int v = 0; v < TW; ++v) sums[wave][v][lane] = h[v];
-    __syncthreads();
-    // one wave's place of the product for each tile of ranks
-    if (wave < TW) {
-      f32x4 x = sums[0][wave][lane];
+    for (int u = 0; u < NT; ++u)
 #pragma unroll
-      for (int w = 1; w < kLoraWaves; ++w) x += sums[w][wave][lane];
-      if (c0 + r < n && row0 + 16 * wave + 4 * g < rows)
-        *reinterpret_cast<f32x4*>(a.part + ((int64_t)chunk * a.tokens + tok) * rows + row0 + 16 * wave + 4 * g) = x;
+      for (int v = 0; v < TW; ++v) sums[wave][u * TW + v][lane] = h[u][v];
+    __syncthreads();
+    // one wave's place of the product for each tile of tokens and ranks
+    for (int p = wave; p < NT * TW; p += kLoraWaves) {
+      f32x4 x = sums[0][p][lane];
+#pragma unroll
+      for (int w = 1; w < kLoraWaves; ++w) x += sums[w][p][lane];
+      const int u = p / TW, row = row0 + 16 * (p % TW) + 4 * g;
+      int t = tok[0];
+#pragma unroll
+      for (int k = 1; k < NT; ++k) t = u == k ? tok[k] : t;
+      if (c0 + 16 * u + r < n && row < rows)
+        *reinterpret_cast<f32x4*>(a.part + ((int64_t)chunk * a.tokens + t) * rows + row) = x;
     }
     __syncthreads();
   });
@@ -124,19 +140,19 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_down_kernel(LoraArgs a) 
 // store of 16 bytes a lane covers 64 in a row.
 __device__ __forceinline__ int tile_column(int j, int m) { return j / 2 * 32 + m / 4 * 8 + j % 2 * 4 + m % 4; }
 
-// out = y + s B h for tiles of tokens and a range of column tiles of one slice.
+// out = y + s B h for tiles of 16 tokens and a range of column tiles of one slice.
 // BS products of 32 ranks for h rounded and as many for what that left out; ranks
 // of up to 16 have both in one (PACKED).
 template <int BS, bool PACKED>
-__global__ void __launch_bounds__(kLoraWaves * 64) lora_up_kernel(LoraArgs a) {
-  constexpr int HS = PACKED ? 1 : 2 * BS;
+__global__ void __launch_bounds__(kLoraWaves * 64, BS == 1 ? 4 : BS == 2 ? 3 : 2) lora_up_kernel(LoraArgs a) {
+  constexpr int HS = PACKED ? 1 : 2 * BS, PS = PACKED ? 1 : BS;
   __shared__ u32x4 h_lds[HS][64];
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int r = lane & 15, g = lane >> 4;
   int id = blockIdx.x;
   int range = id % a.ranges, slice = 0, first = 0;
   id /= a.ranges;
-  const int slot = id % a.slots, block = id / a.slots;
+  const int slot = id % a.up_slots, block = id / a.up_slots;
   // the slice, and its first column
   const int wide = a.tiles_wg * 64;
   for (;; ++slice) {
@@ -149,27 +165,28 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_up_kernel(LoraArgs a) {
   const int n0 = range * wide + wave * 64, n1 = min(width, range * wide + wide);
   uint64_t there;
   const int mine = lane_adapter(a, block, &there);
-  for_tiles(mine, there, slot, a.slots, [&](int i, uint64_t mask, int c0) {
+  for_tiles(mine, there, 16, slot, a.up_slots, [&](int i, uint64_t mask, int c0) {
     if (i < 0 && a.out == a.y) return;
     const int n = __popcll(mask), order = nth_lane(mask);
     const int tok = block * kLoraBlock + __shfl(order, min(c0 + r, n - 1), 64);
     const bool live = c0 + r < n;
     const uint8_t* b = a.b + (i >= 0 ? i * a.b_step : 0) + (int64_t)first * a.rank * 2;
-    const uint8_t* y = a.y + tok * a.y_row + (int64_t)first * 2;
-    uint8_t* out = a.out + tok * a.out_row + (int64_t)first * 2;
+    const uint8_t* y = a.y + tok * a.y_row + (int64_t)(first + 8 * g) * 2;
+    uint8_t* out = a.out + tok * a.out_row + (int64_t)(first + 8 * g) * 2;
     u32x4 w[4][BS], v[2];
     auto load = [&](int t) {
 #pragma unroll
       for (int half = 0; half < 2; ++half)
-        if (live && t + 32 * half + 8 * g < n1) v[half] = *reinterpret_cast<const u32x4*>(y + (t + 32 * half + 8 * g) * 2);
+        if (live && t + 32 * half + 8 * g < n1) v[half] = *reinterpret_cast<const u32x4*>(y + (t + 32 * half) * 2);
       if (i >= 0) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const uint8_t* p = b + (int64_t)min(t + tile_column(j, r), width - 1) * a.rank * 2;
+          // (an adapter of a slice is shorter than 2^31 bytes)
+          const uint32_t at = (uint32_t)(min(t + tile_column(j, r), width - 1) * a.rank * 2);
 #pragma unroll
           for (int s = 0; s < BS; ++s) {
             const int octet = PACKED ? (g < octets ? g : g - octets) : 4 * s + g;
-            w[j][s] = octet < octets ? *reinterpret_cast<const u32x4*>(p + octet * 16) : u32x4{0u, 0u, 0u, 0u};
+            w[j][s] = octet < octets ? *reinterpret_cast<const u32x4*>(b + (at + octet * 16)) : u32x4{0u, 0u, 0u, 0u};
           }
         }
       }
@@ -178,7 +195,7 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_up_kernel(LoraArgs a) {
     if (i >= 0) {
       // h of the tile's tokens, in the order of the products' operands
       const float scale = a.scales ? a.scales[i] : 1.0f;
-      for (int s = wave; s < (PACKED ? 1 : BS); s += kLoraWaves) {
+      for (int s = wave; s < PS; s += kLoraWaves) {
         const int place = 4 * s + g, octet = PACKED && place >= octets ? place - octets : place;
         u32x4 hi = {0u, 0u, 0u, 0u}, lo = {0u, 0u, 0u, 0u};
         if (octet < octets) {
@@ -219,20 +236,17 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_up_kernel(LoraArgs a) {
       }
       lds_barrier();
     }
-    u32x4 h[HS];
-    if (i >= 0) {
-#pragma unroll
-      for (int s = 0; s < HS; ++s) h[s] = h_lds[s][lane];
-    }
     for (int t = n0; t < n1; t += 64 * kLoraWaves) {
       f32x4 o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) o[j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       if (i >= 0) {
 #pragma unroll
-        for (int s = 0; s < HS; ++s)
+        for (int s = 0; s < HS; ++s) {
+          const u32x4 h = h_lds[s][lane];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) o[j] = mma_bf16(w[j][s % BS], h[s], o[j]);
+          for (int j = 0; j < 4; ++j) o[j] = mma_bf16(w[j][s % BS], h, o[j]);
+        }
       }
       const u32x4 now[2] = {v[0], v[1]};
       if (t + 64 * kLoraWaves < n1) load(t + 64 * kLoraWaves);
@@ -248,38 +262,46 @@ __global__ void __launch_bounds__(kLoraWaves * 64) lora_up_kernel(LoraArgs a) {
                              __uint_as_float(x[k] & 0xffff0000u) + d[k % 2 * 2 + 1]);
           }
         }
-        *reinterpret_cast<u32x4*>(out + (t + 32 * half + 8 * g) * 2) = x;
+        *reinterpret_cast<u32x4*>(out + (t + 32 * half) * 2) = x;
       }
     }
     lds_barrier();
   });
 }
 
-hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
-  const int blocks = (a.tokens + kLoraBlock - 1) / kLoraBlock, rows = a.slices * a.rank, groups = (rows + 63) / 64;
-  const dim3 down((unsigned)(blocks * a.slots * groups * a.chunks)), up((unsigned)(blocks * a.slots * a.ranges));
-  const dim3 threads(kLoraWaves * 64);
-  const int tiles = rows >= 64 ? 4 : (rows + 15) / 16;
+template <int NT>
+static void launch_down(const LoraArgs& a, int blocks, hipStream_t s) {
+  const int rows = a.slices * a.rank, groups = (rows + 63) / 64, tiles = rows >= 64 ? 4 : (rows + 15) / 16;
+  const dim3 grid((unsigned)(blocks * a.down_slots * groups * a.chunks)), threads(kLoraWaves * 64);
   if (tiles == 1)
-    hipLaunchKernelGGL((lora_down_kernel<1>), down, threads, 0, s, a);
+    hipLaunchKernelGGL((lora_down_kernel<NT, 1>), grid, threads, 0, s, a);
   else if (tiles == 2)
-    hipLaunchKernelGGL((lora_down_kernel<2>), down, threads, 0, s, a);
+    hipLaunchKernelGGL((lora_down_kernel<NT, 2>), grid, threads, 0, s, a);
   else if (tiles == 3)
-    hipLaunchKernelGGL((lora_down_kernel<3>), down, threads, 0, s, a);
+    hipLaunchKernelGGL((lora_down_kernel<NT, 3>), grid, threads, 0, s, a);
   else
-    hipLaunchKernelGGL((lora_down_kernel<4>), down, threads, 0, s, a);
+    hipLaunchKernelGGL((lora_down_kernel<NT, 4>), grid, threads, 0, s, a);
+}
+
+hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
+  const int blocks = (a.tokens + kLoraBlock - 1) / kLoraBlock;
+  if (a.wide)
+    launch_down<2>(a, blocks, s);
+  else
+    launch_down<1>(a, blocks, s);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  const dim3 grid((unsigned)(blocks * a.up_slots * a.ranges)), threads(kLoraWaves * 64);
   if (a.rank <= 16)
-    hipLaunchKernelGGL((lora_up_kernel<1, true>), up, threads, 0, s, a);
+    hipLaunchKernelGGL((lora_up_kernel<1, true>), grid, threads, 0, s, a);
   else if (a.rank <= 32)
-    hipLaunchKernelGGL((lora_up_kernel<1, false>), up, threads, 0, s, a);
+    hipLaunchKernelGGL((lora_up_kernel<1, false>), grid, threads, 0, s, a);
   else if (a.rank <= 64)
-    hipLaunchKernelGGL((lora_up_kernel<2, false>), up, threads, 0, s, a);
+    hipLaunchKernelGGL((lora_up_kernel<2, false>), grid, threads, 0, s, a);
   else if (a.rank <= 96)
-    hipLaunchKernelGGL((lora_up_kernel<3, false>), up, threads, 0, s, a);
+    hipLaunchKernelGGL((lora_up_kernel<3, false>), grid, threads, 0, s, a);
   else
-    hipLaunchKernelGGL((lora_up_kernel<4, false>), up, threads, 0, s, a);
+    hipLaunchKernelGGL((lora_up_kernel<4, false>), grid, threads, 0, s, a);
   return hipGetLastError();
 }
 

@@ -53,20 +53,24 @@ ql_status lora_shape(const ql_lora* l, int64_t tokens, qlk::LoraArgs* a) {
   a->b_step = l->b_adapter_stride * 2;
   const int64_t blocks = (tokens + qlk::kLoraBlock - 1) / qlk::kLoraBlock;
   // a decode batch can hold as many tiles as adapters (and tokens without one),
-  // and one more for every 16 tokens; a prompt's block of 64 tokens has four
-  const int64_t slots = blocks > 1 ? 4 : std::max<int64_t>(1, std::min<int64_t>(tokens, l->adapters + 1 + tokens / 16));
-  a->slots = (int)slots;
-  const int64_t groups = (rows + 63) / 64, units = std::max<int64_t>(1, blocks * slots);
-  int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((l->in_features + 511) / 512, 512 / (units * groups)));
+  // and one more for every 16 tokens; a prompt's block of 64 tokens has four, or two
+  // of 32
+  a->wide = blocks > 1;
+  const int64_t few = std::max<int64_t>(1, std::min<int64_t>(tokens, l->adapters + 1 + tokens / 16));
+  a->down_slots = (int)(a->wide ? 2 : few);
+  a->up_slots = (int)(a->wide ? 4 : few);
+  const int64_t groups = (rows + 63) / 64, down = std::max<int64_t>(1, blocks * a->down_slots * groups),
+                up = std::max<int64_t>(1, blocks * a->up_slots);
+  int64_t chunks = std::max<int64_t>(1, std::min<int64_t>((l->in_features + 511) / 512, 1024 / down));
   const int64_t chunk = ((l->in_features + chunks - 1) / chunks + 255) / 256 * 256;
   chunks = (l->in_features + chunk - 1) / chunk;
   a->chunk = (int)chunk;
   a->chunks = (int)chunks;
-  a->tiles_wg = (int)std::max<int64_t>(4, std::min<int64_t>(32, units * tiles / 1024 / 4 * 4));
+  a->tiles_wg = (int)std::max<int64_t>(4, std::min<int64_t>(32, up * tiles / (a->wide ? 1024 : 512) / 4 * 4));
   int64_t ranges = 0;
   for (int i = 0; i < l->slices; ++i) ranges += ((l->widths[i] + 63) / 64 + a->tiles_wg - 1) / a->tiles_wg;
   a->ranges = (int)ranges;
-  if (units * groups * chunks >= kMaxWorkgroups || units * ranges >= kMaxWorkgroups)
+  if (down * chunks >= kMaxWorkgroups || up * ranges >= kMaxWorkgroups)
     return fail(QL_E_UNSUPPORTED, "2^24 workgroups or more");
   return QL_OK;
 }

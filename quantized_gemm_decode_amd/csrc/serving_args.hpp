@@ -24,7 +24,8 @@ struct LoraArgs {
   int tokens, adapters, rank, k, slices;
   int width[kLoraSlices];
   int chunk, chunks;       // K of a partial sum (a multiple of 256: 64 a step of each wave), their number
-  int slots;               // workgroups that share a block's tiles of tokens
+  int wide;                // first product: tiles of 32 tokens, not 16
+  int down_slots, up_slots;  // workgroups that share a block's tiles of tokens, of each product
   int tiles_wg;            // 64-wide column tiles of a workgroup of the second product
   int ranges;              // of all slices together
 };
