@@ -105,37 +105,6 @@ __device__ __forceinline__ void load_v(const AttnArgs& a, const Groups& at, int 
     t->x[j] = *reinterpret_cast<const u32x4*>(v + j * (Staged<D, E4M3>::RP * (int)a.vc.token) + lane);
 }
 
-// The same rows straight into LDS, without registers (bf16: nothing to
-// convert): 16 bytes a lane from row + off, to `to` and the lanes' places behind
-// it.  Lanes load the pieces that their places hold.  The caller waits for it.
-__device__ __forceinline__ void load_to_lds(const uint8_t* row, uint32_t off, const uint8_t* to) {
-  const uint32_t at = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) const uint8_t*)to);
-  asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(at), "v"(off), "s"(row) : "memory");
-}
-template <int D>
-__device__ __forceinline__ void fetch_k(const AttnArgs& a, const Groups& at, int i, uint8_t* kl) {
-  using S = Staged<D, false>;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const uint8_t* k = a.kc.p + pick(at.k_lo, at.k_hi, i);
-#pragma unroll
-  for (int j = 0; j < S::PASSES; ++j) {
-    const int row = j * S::RP + lane / S::CH;
-    load_to_lds(k, (uint32_t)(row * (int)a.kc.token + k_piece<D>(row, lane % S::CH) * 16), kl + (wave * 16 + j * S::RP) * D * 2);
-  }
-}
-template <int D>
-__device__ __forceinline__ void fetch_v(const AttnArgs& a, const Groups& at, int i, uint8_t* vl) {
-  using S = Staged<D, false>;
-  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const uint8_t* v = a.vc.p + pick(at.v_lo, at.v_hi, i);
-#pragma unroll
-  for (int j = 0; j < S::PASSES; ++j) {
-    const int row = j * S::RP + lane / S::CH, c = lane % S::CH;
-    load_to_lds(v, (uint32_t)(row * (int)a.vc.token + (v_block<D>(row, c / 4) * 4 + c % 4) * 16),
-                vl + (wave * 16 + j * S::RP) * D * 2);
-  }
-}
-
 // 16 E4M3 codes as two pieces of bf16.
 __device__ __forceinline__ void widen(const u32x4& c, u32x4* lo, u32x4* hi) {
   *lo = u32x4{e4m3_to_bf16<false>(c.x), e4m3_to_bf16<true>(c.x), e4m3_to_bf16<false>(c.y), e4m3_to_bf16<true>(c.y)};
@@ -506,40 +475,26 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
     // step T: scores of tile T + 1, weights of keys 32 .. 95 and sums over
     // keys 0 .. 63 of tile T; meanwhile K of tile T + 2 and V of tile T + 1
     // come in, one after the other through the same registers
-    // Trees stream long contexts past few rows: both come in at once, from the
-    // start of the step on, bf16 straight into LDS (16 sequences of 515 .. 4,099
-    // keys, 32 nodes of 32 / 8 heads: 45 us one after the other)
+    // (trees of few nodes, bf16, 128-wide heads: both at once, straight into LDS,
+    // is no faster; 16 sequences of 515 .. 4,099 keys, 32 nodes of 32 / 8 heads: 45 us either way)
     auto step = [&](int T, auto hidden) {
-      constexpr bool HIDDEN = decltype(hidden)::value, FETCH = TREE && D == 128 && !E4M3 && !HIDDEN;
+      constexpr bool HIDDEN = decltype(hidden)::value;
       const int key = begin + T * kTileKeys;
       const uint8_t* kl = k_lds[(T + 1) & 1];
       const uint8_t* vl = v_lds[T & 1];
-      if constexpr (FETCH) {
-        fetch_v<D>(a, at, (T + 1) & 63, v_lds[(T + 1) & 1]);
-        if (T + 2 < tiles) {
-          if (((T + 2) & 63) == 0) at = groups_at(a, table, h, ((key + 2 * kTileKeys) >> 4) + wave + 4 * lane, last_sub);
-          fetch_k<D>(a, at, (T + 2) & 63, k_lds[T & 1]);
-        }
-      } else {
-        load_v<D, E4M3>(a, at, (T + 1) & 63, v_lane, &staged);
-      }
+      load_v<D, E4M3>(a, at, (T + 1) & 63, v_lane, &staged);
       if (HIDDEN) mask(s1, key + 32);
       refer(s1, vl, 0, p0);
       inner_step<D>(kl, 0, vl, 0, q, s1, &w, p0, o, &s0, p1);
-      if constexpr (!FETCH) {
-        store_v<D, E4M3>(staged, key + kTileKeys, u.len, v_lds[(T + 1) & 1], HIDDEN && part(T + 1), &dropped);
-        if (T + 2 < tiles) {
-          if (((T + 2) & 63) == 0) at = groups_at(a, table, h, ((key + 2 * kTileKeys) >> 4) + wave + 4 * lane, last_sub);
-          load_k<D, E4M3>(a, at, (T + 2) & 63, k_lane, &staged);
-        }
+      store_v<D, E4M3>(staged, key + kTileKeys, u.len, v_lds[(T + 1) & 1], HIDDEN && part(T + 1), &dropped);
+      if (T + 2 < tiles) {
+        if (((T + 2) & 63) == 0) at = groups_at(a, table, h, ((key + 2 * kTileKeys) >> 4) + wave + 4 * lane, last_sub);
+        load_k<D, E4M3>(a, at, (T + 2) & 63, k_lane, &staged);
       }
       if (HIDDEN) mask(s0, key + kTileKeys);
       refer(s0, vl, 1, p1);
       inner_step<D>(kl, 1, vl, 1, q, s0, &w, p1, o, &s1, p0);
-      if constexpr (FETCH)
-        __builtin_amdgcn_s_waitcnt(0x0f70);   // vmcnt 0: this wave's share has arrived
-      else if (T + 2 < tiles)
-        store_k<D, E4M3>(staged, k_lds[T & 1]);
+      if (T + 2 < tiles) store_k<D, E4M3>(staged, k_lds[T & 1]);
       lds_barrier();
     };
     // tiles [first, last) are seen whole; a loop each, for the hidden ones' work
@@ -599,12 +554,10 @@ __global__ void __launch_bounds__(kTileWaves * 64, tile_workgroups(D)) attn_tile
       a.lse[(int64_t)tok * a.q_heads + head] = lse_of(w.m, sum);
   } else {
     if constexpr (TREE) {
-      // as the registers lie, for the join's lanes to read in the same way.  Written through (at the point that is
-      // coherent for all XCDs): left in the L2s, it waits for the kernel's end to be written back, 0.35 us a MB
+      // as the registers lie, for the join's lanes to read in the same way
       uint64_t* out = reinterpret_cast<uint64_t*>(a.part_o) + ((int64_t)blockIdx.x * kTileWaves + wave) * (DT * 8 + 1) * 64 + lane;
       auto put = [&](int i, float x, float y) {
-        __hip_atomic_store(out + i * 64, (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x), __ATOMIC_RELAXED,
-                           __HIP_MEMORY_SCOPE_AGENT);
+        out[i * 64] = (uint64_t)__float_as_uint(y) << 32 | __float_as_uint(x);
       };
       put(0, w.m, sum);
 #pragma unroll
