@@ -85,10 +85,12 @@ ql_status check_matrix(const void* p, int64_t stride, int64_t width, int64_t tok
 }
 
 // Entries of a vocabulary row that a workgroup takes: long slices, which leave
-// fewer histograms to add, where they still fill the card.
+// fewer histograms to add, where they still give every compute unit two.  (4,096,
+// 8,192 and 16,384 entries; 8 rows of 32,000: 24, 27 and 34 us; 8 of 151,936: 38, 37
+// and 43; 64 of 151,936: 82, 64 and 61.)
 int sample_entries(int64_t rows, int64_t vocab) {
   int entries = qlk::kSampleWide;
-  while (entries > qlk::kSampleNarrow && rows * ((vocab + entries - 1) / entries) < 256) entries /= 2;
+  while (entries > qlk::kSampleNarrow && rows * ((vocab + entries - 1) / entries) < 512) entries /= 2;
   return entries;
 }
 
@@ -104,10 +106,10 @@ SampleSpace sample_space(int64_t rows, int64_t vocab) {
   s.hist = 0;
   s.cand = s.hist + all * qlk::kSampleBuckets * 8;
   s.best = s.cand + rows * vocab * 8;
-  s.state = s.best + rows * 8;
+  s.state = s.best + all * 8;
   s.top = s.state + rows * (int64_t)sizeof(qlk::SampleRow);
   s.count = s.top + all * 4;
-  s.end = (s.count + rows * 4 + 15) / 16 * 16;
+  s.end = (s.count + rows * qlk::kSampleCountStep * 4 + 15) / 16 * 16;
   return s;
 }
 

@@ -32,6 +32,7 @@ struct LoraArgs {
 
 constexpr int kSampleBuckets = 512;
 constexpr int kSampleWide = 16384, kSampleNarrow = 4096;   // entries of a slice
+constexpr int kSampleCountStep = 32;   // a row's counter has a 128-byte line to itself
 
 // What a row's histograms say of it, and what is kept at last.
 struct SampleRow {
@@ -61,9 +62,9 @@ struct SampleArgs {
   float* probs;            // [rows, vocab] or null
   uint64_t* hist;          // [rows, slices, kSampleBuckets]: entries (high bits) and their mass
   float* top;              // [rows, slices]: a slice's largest logit
-  uint64_t* best;          // [rows]: best score among the surely kept entries
+  uint64_t* best;          // [rows, slices]: best score among a slice's surely kept entries
   uint64_t* cand;          // [rows, vocab]: candidates
-  int32_t* count;          // [rows]: candidates
+  int32_t* count;          // [rows, kSampleCountStep], the first: candidates
   SampleRow* state;        // [rows]
   int rows, vocab, slices, entries;
 };
