@@ -11,6 +11,9 @@
 // node's number is at least d, and rises along the branch, so rows moved in
 // their order never overwrite one that is still to be moved; a thread moves
 // the same 16 bytes of every row, so that order needs no barrier.
+//
+// Measured on MI355X: 4 sequences of 13 nodes 4.5 us, 64 of 64 nodes (4.4 MB moved)
+// 5.8 us; a launch alone takes 4.4.
 #include "attention_args.hpp"
 #include "device_common.hpp"
 
