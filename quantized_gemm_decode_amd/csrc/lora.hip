@@ -234,7 +234,9 @@ __global__ void __launch_bounds__(kLoraWaves * 64, BS == 1 ? 4 : BS == 2 ? 3 : 2
           for (int k = 0; k < 4; ++k) {
             const float e = x[k / 2][k % 2 * 2] * scale, f = x[k / 2][k % 2 * 2 + 1] * scale;
             hi[k] = bf16_pair(e, f);
-            lo[k] = bf16_pair(e - __uint_as_float(hi[k] << 16), f - __uint_as_float(hi[k] & 0xffff0000u));
+            // (nothing is left of an infinity)
+            const float e2 = e - __uint_as_float(hi[k] << 16), f2 = f - __uint_as_float(hi[k] & 0xffff0000u);
+            lo[k] = bf16_pair(e2 == e2 ? e2 : 0.0f, f2 == f2 ? f2 : 0.0f);
           }
         }
         if (PACKED) {
