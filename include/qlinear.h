@@ -808,8 +808,9 @@ ql_status qlinear_lora(const ql_lora* lora, int64_t tokens, const void* x, int64
  * Logits of +inf share the probability.
  *
  * What is kept does not depend on rounding in binary32: weights are computed in
- * binary64 and summed as integers, to about 10^-11 of a weight (entries of less
- * than 2^-90 of the largest weigh nothing in the sums).  Results do
+ * binary64 and summed as integers, to about 10^-11 of a weight and 10^-16 of it
+ * for every |l_v| / temperature (entries of less than 2^-90 of the largest weigh
+ * nothing in the sums).  Results do
  * not depend on timing.  The workspace (qlinear_sample_workspace_bytes, 16-byte
  * aligned; about 8 bytes an entry) needs no initialisation; concurrent calls need
  * distinct ones.  Up to 65535 rows and 2^24 entries a row.  Enqueue-only.

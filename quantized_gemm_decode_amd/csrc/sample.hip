@@ -103,18 +103,21 @@ __device__ __forceinline__ Rules rules_of(const SampleArgs& a, int row) {
 // logits are more than 2^29 of them apart: a bucket then holds equal ones.)
 __device__ __forceinline__ double line_of(float l, double grid) { return floor((double)l * grid); }
 
-// An entry's mass in its bucket, in steps of 2^-34: exp((f - 1/2) / 8) for the
-// part f of l grid above the line, by the polynomial that meets it at the six
-// Chebyshev nodes of [0, 1] (off by 3 10^-12 at most).  The low bits of 2^52 + x
-// are x rounded.
-__device__ __forceinline__ uint64_t mass_word(float l, double grid) {
-  const double f = __builtin_amdgcn_fract((double)l * grid);
+// exp((f - 1/2) / 8) in steps of 2^-34, and `above` more, for f in [0, 1): the
+// polynomial that meets it at the six Chebyshev nodes (off by 3 10^-12 at most).
+__device__ __forceinline__ double mass_of(double f, double above = 0.0) {
   double p = kMassOne * 2.54348632162432e-07;
   p = fma(p, f, kMassOne * 9.53864143867337e-06);
   p = fma(p, f, kMassOne * 0.0003058076755491678);
   p = fma(p, f, kMassOne * 0.007339162402444752);
   p = fma(p, f, kMassOne * 0.11742663303627268);
-  p = fma(p, f, kMassOne * 0.9394130628109114 + 4503599627370496.0);
+  return fma(p, f, kMassOne * 0.9394130628109114 + above);
+}
+
+// An entry's mass in its bucket, that of the part of l grid above the line.  The
+// low bits of 2^52 + x are x rounded.
+__device__ __forceinline__ uint64_t mass_word(float l, double grid) {
+  const double p = mass_of(__builtin_amdgcn_fract((double)l * grid), 4503599627370496.0);
   return (uint64_t)__double_as_longlong(p) - (uint64_t(0x433) << 52);
 }
 
@@ -827,15 +830,26 @@ __global__ void __launch_bounds__(kFinishThreads) sample_finish_kernel(SampleArg
 constexpr int kWriteThreads = 256;
 
 // Probabilities: w over the mass of the kept entries.
+//
+// w of (l - top) grid = n + f is exp((f - 1/2) / 8), the series of mass_word, times
+// exp((n + 1/2) / 8) in two factors, of n / 32 and n % 32, that a workgroup works out once:
+// half the binary64 operations of an exponential of each entry's own (40 rows of 128,256,
+// top-p: 16 us so).
 template <bool BF16>
 __global__ void __launch_bounds__(kWriteThreads) sample_write_kernel(SampleArgs a) {
-  const int row = blockIdx.y, v = ((int)blockIdx.x * kWriteThreads + (int)threadIdx.x) * 8;
-  if (v >= a.vocab) return;
+  const int row = blockIdx.y, t = threadIdx.x, v = ((int)blockIdx.x * kWriteThreads + t) * 8;
+  __shared__ double factors[48];   // of 32 k lines below (k 0 .. 15), over the total; of 0 .. 31 lines
+  float x[8], p[8];
+  if (v < a.vocab) load_logits<BF16>(a, row, v, x);
   const SampleRow s = a.state[row];
   const Rules r = rules_of(a, row);
   const double per = 1.0 / s.total;
-  float x[8], p[8];
-  load_logits<BF16>(a, row, v, x);
+  if (t < 48) {
+    const double f = exp2_of((t < 16 ? -32.0 * t : 16.5 - t) * (0.125 * kLog2E));
+    factors[t] = t < 16 ? f * (per / kMassOne) : f;
+  }
+  __syncthreads();
+  if (v >= a.vocab) return;
 #pragma unroll
   for (int j = 0; j < 8; ++j) {
     p[j] = 0.0f;
@@ -844,8 +858,14 @@ __global__ void __launch_bounds__(kWriteThreads) sample_write_kernel(SampleArgs 
     const double below = s.line - line_of(x[j], r.grid);
     const bool in = below < s.lo || s.lo == kSampleBuckets;
     if (in || ((below <= s.hi || s.hi == kSampleBuckets - 1) && key_of(x[j], v + j) >= s.least)) {
-      const double w = weight_of(x[j], s.top, r.rate);
-      if (in || w >= (double)r.m) p[j] = (float)(w * per);
+      const double d = ((double)x[j] - (double)s.top) * r.grid, n = floor(d);
+      if (n > -(double)kSampleBuckets && (in || !(r.m > 0.0f))) {
+        const int k = (int)-n;
+        p[j] = (float)(mass_of(d - n) * (factors[k / 32] * factors[16 + k % 32]));
+      } else {
+        const double w = weight_of(x[j], s.top, r.rate);
+        if (in || w >= (double)r.m) p[j] = (float)(w * per);
+      }
     }
   }
   float* out = a.probs + (int64_t)row * a.vocab + v;
