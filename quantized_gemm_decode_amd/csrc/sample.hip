@@ -28,7 +28,7 @@
 // Measured on MI355X, latency throughout (logits are read at 5 TB/s in 4 us by 64
 // rows of 151,936 bf16): 1 row of 32,001: 19.4 us (scan 3.7, collect 7.8, finish 8.3);
 // 64 rows of 151,936 bf16, all rules mixed: 59 us (14.5, 26, 17-21); 40 rows of
-// 128,256 with top-p and probabilities: 64 us (9, 21, 22, write 16, which moves 41 MB).
+// 128,256 with top-p and probabilities: 63 us (9, 21, 22, write 14, which moves 41 MB).
 //   scan: an LDS atomic an entry, and binary64 masses.
 //   collect: the sum of the histograms is a chain of loads, exponentials and a
 //     prefix sum (most of a single row's 7.8 us), then the logits once more, from the
@@ -834,7 +834,7 @@ constexpr int kWriteThreads = 256;
 // w of (l - top) grid = n + f is exp((f - 1/2) / 8), the series of mass_word, times
 // exp((n + 1/2) / 8) in two factors, of n / 32 and n % 32, that a workgroup works out once:
 // half the binary64 operations of an exponential of each entry's own (40 rows of 128,256,
-// top-p: 16 us so).
+// top-p: 14.3 us, 15.9 so).
 template <bool BF16>
 __global__ void __launch_bounds__(kWriteThreads) sample_write_kernel(SampleArgs a) {
   const int row = blockIdx.y, t = threadIdx.x, v = ((int)blockIdx.x * kWriteThreads + t) * 8;
