@@ -10,6 +10,7 @@
 
 #include "api_common.hpp"
 #include "attention_args.hpp"
+#include "tree_cut.hpp"
 
 using qlapi::aligned;
 using qlapi::aligned16;
@@ -238,7 +239,7 @@ ql_status plan_tree(const ql_attention_shape& s, int64_t rows, Part* p) {
   const int64_t units = std::min(s.batch * blocks, s.tokens * group / R + s.batch) * s.kv_heads;
   const int64_t slots = qlk::attn_tile_slots(s.head_dim);
   const bool cut = s.batch <= 512 && s.max_kv > 128;
-  const int64_t shares = cut ? (4 * units + 5 * slots - 1) / (4 * slots) * slots : units;
+  const int64_t shares = cut ? qlk::tree_most(units, (int)slots) : units;
   if (s.tokens * s.q_heads >= (int64_t(1) << 31)) return fail(QL_E_UNSUPPORTED, "tokens * q_heads exceeds 2^31");
   if (shares >= kMaxWorkgroups || s.tokens * s.q_heads / 4 + s.kv_heads >= kMaxWorkgroups)
     return fail(QL_E_UNSUPPORTED, "2^24 workgroups or more");

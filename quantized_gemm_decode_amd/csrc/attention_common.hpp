@@ -11,6 +11,7 @@
 
 #include "attention_args.hpp"
 #include "device_common.hpp"
+#include "tree_cut.hpp"
 
 namespace qlk {
 
@@ -173,16 +174,6 @@ __device__ __forceinline__ Unit unit_at(const AttnArgs& a, int n, int R) {
   return unit_of(a, s, blocks - 1 - (n - start(s.b, s.first)), R);
 }
 
-// Trees: the units' keys are cut by the lengths found, into equal shares of a
-// unit that are as many as the card takes at once (or for more units than that, a
-// multiple).  A host's bound of the lengths would leave the card idle behind the
-// longest ones (16 sequences of 515 .. 4,099 keys, 32 nodes of 32 / 8 heads: 54 us so
-// cut, 46 by the lengths found).
-struct TreeCut {
-  float per_key;   // shares a key
-  bool rounds;     // more of them than the card takes at once
-};
-
 __device__ __forceinline__ int tree_blocks(const AttnArgs& a, const Sequence& s, int R) {
   return min(((s.end - s.first) * a.group + R - 1) / R, a.row_blocks);
 }
@@ -194,44 +185,17 @@ __device__ __forceinline__ Sequence tree_sequence(const AttnArgs& a, int b) {
   return Sequence{b, q0, q1, min(max(a.seq_lens[b], 0), a.max_kv)};
 }
 
-// Shares of a unit.  (Rounding of the product only moves a border between counts.)
-__device__ __forceinline__ int tree_shares(int len, const TreeCut& cut) { return max(1, (int)ceilf((float)len * cut.per_key)); }
-
+// The cut of a batch, a sequence a lane.
 __device__ __forceinline__ TreeCut tree_cut(const AttnArgs& a, const Sequence& mine, int R, int slots) {
   const int lane = threadIdx.x & 63;
-  int units = 0;       // of one KV head
-  float keys = 0.0f;   // and theirs
-#pragma unroll 1
-  for (int b0 = 0; b0 < a.batch; b0 += 64) {
-    const Sequence s = b0 ? tree_sequence(a, b0 + lane) : mine;
-    const int blocks = tree_blocks(a, s, R);
-    units += lane_i32(inclusive_sum(blocks), 63);
-    keys += (float)lane_i32(inclusive_sum((int)min((int64_t)blocks * ((s.len + 63) >> 6), (int64_t)1 << 24)), 63) * 64.0f;
-  }
-  const int most = (4 * units * a.kv_heads + 5 * slots - 1) / (4 * slots) * slots / a.kv_heads;   // units / slots + 1/4, rounded up
-  // shares of one KV head with chunks of 64 c keys are between keys / 64 c and that plus the units
-  auto count = [&](int c) {
-    const TreeCut cut = {1.0f / (float)(64 * c), false};
-    int n = 0;
+  auto each = [&](auto f) {
 #pragma unroll 1
     for (int b0 = 0; b0 < a.batch; b0 += 64) {
       const Sequence s = b0 ? tree_sequence(a, b0 + lane) : mine;
-      n += lane_i32(inclusive_sum(tree_blocks(a, s, R) * tree_shares(s.len, cut)), 63);
+      f(tree_blocks(a, s, R), s.len);
     }
-    return n;
   };
-  const int longest = (a.max_kv + 63) / 64;
-  int lo = max(2, (int)(keys / (float)(64 * most))), hi = max(lo, longest);
-  if (most > units) hi = min(hi, max(lo, (int)(keys / (float)(64 * (most - units))) + 1));
-#pragma unroll 1
-  while (lo < hi) {
-    const int mid = (lo + hi) / 2;
-    if (count(mid) <= most)
-      hi = mid;
-    else
-      lo = mid + 1;
-  }
-  return TreeCut{1.0f / (float)(64 * lo), most * a.kv_heads > slots};
+  return tree_cut_of(each, [](int x) { return lane_i32(inclusive_sum(x), 63); }, a.kv_heads, a.max_kv, slots);
 }
 
 // The shares of this lane's sequence, and those before them (of one KV head).  Where
