@@ -601,9 +601,9 @@ __global__ void __launch_bounds__(kTileWaves * 64) attn_tree_join_kernel(AttnArg
   const int h = (int)blockIdx.x % a.kv_heads;
   const Unit u = unit_at(a, (int)blockIdx.x / a.kv_heads, R);
   if (u.rows == 0) return;
-  const int shares = uniform_i32(a.cut + 2 * u.b + 1), before = uniform_i32(a.cut + 2 * u.b) + u.row0 / R * shares;
-  // (a cu_q that is none may name more shares than there are)
-  if (shares <= 1 || (int64_t)(before + shares) * a.kv_heads > a.shares) return;
+  const int shares = uniform_i32(a.cut + 2 * u.b + 1);
+  const int before = tree_first_share(uniform_i32(a.cut + 2 * u.b), u.row0 / R, shares, a.kv_heads, a.shares);
+  if (before < 0) return;
   const int row = wave * 32 + (lane & 31), place = u.row0 + row;
   if (row >= u.rows) return;
   constexpr int64_t wide = (DT * 8 + 1) * 64;

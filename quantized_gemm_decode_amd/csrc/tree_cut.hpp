@@ -69,4 +69,14 @@ __host__ __device__ __forceinline__ TreeCut tree_cut_of(Each each, Total total, 
   return TreeCut{1.0f / (64.0f * (float)lo), (int64_t)most * kv_heads > slots};
 }
 
+// The first of the shares of block `block` of a sequence (before: shares before the
+// sequence, of one KV head, as the tile kernel counted them); -1: not cut, or not
+// among the shares that were launched.  (Sequences that overlap, as no cu_q has
+// them, may count more than 32 bits hold.)
+__host__ __device__ __forceinline__ int tree_first_share(int before, int block, int shares, int kv_heads, int launched) {
+  const int64_t first = before + (int64_t)block * shares;
+  if (shares <= 1 || first < 0 || first + shares > launched / kv_heads) return -1;
+  return (int)first;
+}
+
 }  // namespace qlk
