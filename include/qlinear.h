@@ -813,7 +813,9 @@ ql_status qlinear_lora(const ql_lora* lora, int64_t tokens, const void* x, int64
  * nothing in the sums).  Results do
  * not depend on timing.  The workspace (qlinear_sample_workspace_bytes, 16-byte
  * aligned; about 8 bytes an entry) needs no initialisation; concurrent calls need
- * distinct ones.  Up to 65535 rows and 2^24 entries a row.  Enqueue-only.
+ * distinct ones; one of a size for some rows and vocabulary serves every call of no
+ * more rows and no longer a vocabulary.  Up to 65535 rows and 2^24 entries a row.
+ * Enqueue-only.
  */
 typedef enum { QL_LOGITS_F32 = 0, QL_LOGITS_BF16 = 1 } ql_logits_type;
 

@@ -94,12 +94,26 @@ ql_status check_matrix(const void* p, int64_t stride, int64_t width, int64_t tok
 // fewer histograms to add, where they still give every compute unit two.  (4,096,
 // 8,192 and 16,384 entries; 8 rows of 32,000: 24, 27 and 34 us; 8 of 151,936: 38, 37
 // and 43; 64 of 151,936: 82, 64 and 61.)
+constexpr int64_t kSampleFill = 512;
+
+int64_t slices_of(int64_t vocab, int entries) { return (vocab + entries - 1) / entries; }
+
 int sample_entries(int64_t rows, int64_t vocab) {
   int entries = qlk::kSampleWide;
-  while (entries > qlk::kSampleNarrow && rows * ((vocab + entries - 1) / entries) < 512) entries /= 2;
+  while (entries > qlk::kSampleNarrow && rows * slices_of(vocab, entries) < kSampleFill) entries /= 2;
   return entries;
 }
 
+// The most slices of all rows together that a call of up to that many rows and
+// entries has.  (Those shorter than kSampleWide are at most twice as many as the
+// longer ones that were too few.)
+int64_t most_slices(int64_t rows, int64_t vocab) {
+  return std::max(rows * slices_of(vocab, qlk::kSampleWide),
+                  std::min(2 * (kSampleFill - 1), rows * slices_of(vocab, qlk::kSampleNarrow)));
+}
+
+// Places in the workspace; `end` does not fall with fewer rows or a shorter
+// vocabulary, so the largest call's workspace serves all.
 struct SampleSpace {
   int64_t slices, entries, hist, cand, best, state, top, count, end;
 };
@@ -107,7 +121,7 @@ struct SampleSpace {
 SampleSpace sample_space(int64_t rows, int64_t vocab) {
   SampleSpace s;
   s.entries = sample_entries(rows, vocab);
-  s.slices = (vocab + s.entries - 1) / s.entries;
+  s.slices = slices_of(vocab, (int)s.entries);
   const int64_t all = rows * s.slices;
   s.hist = 0;
   s.cand = s.hist + all * qlk::kSampleBuckets * 8;
@@ -115,7 +129,8 @@ SampleSpace sample_space(int64_t rows, int64_t vocab) {
   s.state = s.best + all * 8;
   s.top = s.state + rows * (int64_t)sizeof(qlk::SampleRow);
   s.count = s.top + all * 4;
-  s.end = (s.count + rows * qlk::kSampleCountStep * 4 + 15) / 16 * 16;
+  const int64_t more = most_slices(rows, vocab) - all;   // room of smaller calls
+  s.end = (s.count + rows * qlk::kSampleCountStep * 4 + more * (qlk::kSampleBuckets * 8 + 8 + 4) + 15) / 16 * 16;
   return s;
 }
 

@@ -285,7 +285,7 @@ def qlinear_sample_workspace_bytes(rows, vocab):
 
 
 def sample_workspace(rows, vocab, device="cuda"):
-    """Device memory for qlinear_sample (any contents)."""
+    """Device memory for qlinear_sample (any contents), with up to that many rows and entries."""
     return torch.empty(max(16, qlinear_sample_workspace_bytes(rows, vocab)), dtype=torch.uint8, device=device)
 
 

@@ -1,0 +1,31 @@
+"""Smaller calls in the workspace of a larger one: the same results, and nothing
+behind it is written."""
+
+import pytest
+import torch
+
+import quantized_gemm_decode_amd as ql
+from tests import test_gpu_sample as sample
+from tests.gpu_util import requires_gpu
+
+pytestmark = [pytest.mark.gpu, requires_gpu]
+GUARD = 1 << 20
+
+
+def guarded(size):
+    """A workspace of just that size, and the memory behind it."""
+    buf = torch.full((size + GUARD,), 255, dtype=torch.uint8, device="cuda")
+    return buf[:size], buf[size:]
+
+
+@pytest.mark.parametrize("rows,vocab,most_rows,most_vocab", [(127, 32001, 128, 32001), (26, 151936, 27, 151936), (63, 128256, 64, 128256),
+                                                           (64, 114688, 64, 114689), (1, 20000, 30, 40000)])
+def test_sampling(rows, vocab, most_rows, most_vocab):
+    logits, noise = sample.problem(rows, rows, vocab, True)
+    want = sample.run(logits, noise, probs=False, **sample.columns(rows))
+    ws, behind = guarded(ql.qlinear_sample_workspace_bytes(most_rows, most_vocab))
+    tokens, logs = torch.zeros(rows, dtype=torch.int32, device="cuda"), torch.zeros(rows, device="cuda")
+    dev = {k: torch.tensor(v, dtype=torch.int32 if k == "top_k" else torch.float32).cuda() for k, v in sample.columns(rows).items()}
+    ql.qlinear_sample(logits, noise, tokens, ws, logprobs=logs, **dev)
+    assert (tokens.cpu().numpy() == want[0]).all() and (logs.double().cpu().numpy() == want[1]).all()
+    assert (behind == 255).all()
