@@ -764,9 +764,10 @@ ql_status qlinear_verify_draft(int64_t batch, int64_t n_drafts, int64_t max_draf
  *
  * Sums are binary32; the inner sum enters its product to 2^-16 of it, and out is
  * rounded to bf16 once.  (An infinity in B may make NaN of its column, as the
- * part that rounding left out of the inner sum may be 0.)  The workspace (qlinear_lora_workspace_bytes; 0 for sizes
- * that qlinear_lora refuses) needs no initialisation; concurrent calls need
- * distinct ones.  Enqueue-only; no atomics.
+ * part that rounding left out of the inner sum may be 0.)  The workspace
+ * (qlinear_lora_workspace_bytes; 0 for sizes that qlinear_lora refuses) needs no
+ * initialisation; concurrent calls need distinct ones; one for some number of
+ * tokens serves every call of fewer of the same sizes.  Enqueue-only; no atomics.
  */
 typedef struct {
   const void* a;

@@ -81,6 +81,14 @@ ql_status lora_shape(const ql_lora* l, int64_t tokens, qlk::LoraArgs* a) {
   return QL_OK;
 }
 
+// The most partial sums (chunks of K of all tokens) that a call of up to a.tokens
+// tokens has: up to a block of tokens any number of chunks; with more of them 1024 /
+// (2 blocks groups), 512 a block and group over its 64 tokens.
+int64_t most_parts(const qlk::LoraArgs& a) {
+  const int64_t tokens = a.tokens, cut = (a.k + 511) / 512, groups = (a.slices * a.rank + 63) / 64;
+  return std::max(tokens, std::min(tokens * cut, std::max<int64_t>(cut, 512 / groups) * qlk::kLoraBlock));
+}
+
 ql_status check_matrix(const void* p, int64_t stride, int64_t width, int64_t tokens, const char* name) {
   if (!p) return fail(QL_E_INVALID, "%s is NULL", name);
   if (!aligned16(p)) return fail(QL_E_ALIGN, "%s is not 16-byte aligned", name);
@@ -147,7 +155,7 @@ extern "C" {
 int64_t qlinear_lora_workspace_bytes(const ql_lora* lora, int64_t tokens) {
   qlk::LoraArgs a{};
   if (lora_shape(lora, tokens, &a) != QL_OK) return 0;
-  return (int64_t)a.chunks * a.tokens * a.slices * a.rank * 4;
+  return most_parts(a) * a.slices * a.rank * 4;
 }
 
 ql_status qlinear_lora(const ql_lora* lora, int64_t tokens, const void* x, int64_t x_stride, const void* y, int64_t y_stride,

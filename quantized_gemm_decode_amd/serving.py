@@ -265,7 +265,7 @@ def qlinear_lora_workspace_bytes(stack, tokens):
 
 
 def lora_workspace(stack, tokens, device="cuda"):
-    """Device memory for qlinear_lora with `tokens` tokens (any contents)."""
+    """Device memory for qlinear_lora with up to `tokens` tokens (any contents)."""
     return torch.empty(max(16, qlinear_lora_workspace_bytes(stack, tokens)), dtype=torch.uint8, device=device)
 
 

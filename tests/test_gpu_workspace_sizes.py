@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import quantized_gemm_decode_amd as ql
-from tests import test_gpu_sample as sample
+from tests import test_gpu_lora as lora, test_gpu_sample as sample
 from tests.gpu_util import requires_gpu
 
 pytestmark = [pytest.mark.gpu, requires_gpu]
@@ -29,3 +29,13 @@ def test_sampling(rows, vocab, most_rows, most_vocab):
     ql.qlinear_sample(logits, noise, tokens, ws, logprobs=logs, **dev)
     assert (tokens.cpu().numpy() == want[0]).all() and (logs.double().cpu().numpy() == want[1]).all()
     assert (behind == 255).all()
+
+
+@pytest.mark.parametrize("tokens,most,k", [(4096, 4097, 4096), (1, 2000, 4096), (64, 65, 8192), (300, 5000, 2048)])
+def test_adapters(tokens, most, k):
+    p = lora.Problem(tokens, [i // 40 % 5 - 1 for i in range(tokens)], 4, 16, k, [64, 64, 64])
+    want = p.run()
+    ws, behind = guarded(ql.qlinear_lora_workspace_bytes(p.stack, most))
+    out = torch.zeros_like(p.y)
+    ql.qlinear_lora(p.stack, p.x, p.y, p.adapters.cuda(), ws, out=out)
+    assert torch.equal(out, want) and (behind == 255).all()
