@@ -733,7 +733,8 @@ ql_status qlinear_tree_commit(int64_t batch, int64_t tokens, int64_t max_depth, 
  *   out_tokens int32 [batch, max_drafts + 1]: the accepted drafts, the next
  *   token, then -1;  accepted int32 [batch]: the number of accepted drafts.
  * The workspace (qlinear_verify_workspace_bytes, 16-byte aligned) needs no
- * initialisation.
+ * initialisation; one for some batch and vocabulary serves every call of no more
+ * sequences and no longer a vocabulary.
  */
 int64_t qlinear_verify_workspace_bytes(int64_t batch, int64_t vocab);
 ql_status qlinear_verify_draft(int64_t batch, int64_t n_drafts, int64_t max_drafts, int64_t vocab,

@@ -414,6 +414,17 @@ ql_status run_plan(ql_attention_plan p, const ql_rows* q, const ql_kv_cache* cac
   return e == hipSuccess ? QL_OK : hip_fail(e, "attention launch");
 }
 
+// Slices of a vocabulary row: enough workgroups for the card with few
+// sequences, at least 1024 entries (4 a thread) each, at most kVerifySlice.  With
+// 512, 1,024 and 2,048 workgroups, us: 4 x 151,936 entries 7.4, 7.9, 7.9; 16 x 151,936
+// 10.9, 10.2, 10.5; 64 x 32,001 9.8, 9.4, 10.1.
+struct VerifySlices {
+  int64_t least, most;   // whatever the sequences
+  explicit VerifySlices(int64_t vocab)
+      : least(std::max<int64_t>(1, (vocab + qlk::kVerifySlice - 8) / (qlk::kVerifySlice - 4))), most(std::max<int64_t>(1, vocab / 1024)) {}
+  int of(int64_t batch) const { return (int)std::max(least, std::min<int64_t>(most, 1024 / std::max<int64_t>(1, batch))); }
+};
+
 }  // namespace
 
 extern "C" {
@@ -486,18 +497,11 @@ ql_status qlinear_tree_attention(ql_attention_plan p, const ql_rows* q, const ql
   return run_plan(p, q, cache, page_table, table_stride, seq_lens, cu_q, sees, sees_words, out, lse, workspace, stream);
 }
 
-// Slices of a vocabulary row: enough workgroups for the card with few
-// sequences, at least 1024 entries (4 a thread) each, at most kVerifySlice.  With
-// 512, 1,024 and 2,048 workgroups, us: 4 x 151,936 entries 7.4, 7.9, 7.9; 16 x 151,936
-// 10.9, 10.2, 10.5; 64 x 32,001 9.8, 9.4, 10.1.
-static int verify_slices(int64_t batch, int64_t vocab) {
-  const int64_t most = std::max<int64_t>(1, vocab / 1024), least = (vocab + qlk::kVerifySlice - 8) / (qlk::kVerifySlice - 4);
-  return (int)std::max<int64_t>({1, least, std::min<int64_t>(most, 1024 / std::max<int64_t>(1, batch))});
-}
-
+// Room for the most slices of any call of no more sequences and entries.
 int64_t qlinear_verify_workspace_bytes(int64_t batch, int64_t vocab) {
   if (batch <= 0 || vocab <= 0) return 0;
-  return (batch * verify_slices(batch, vocab) * 8 + 15) / 16 * 16;
+  const VerifySlices s(vocab);
+  return (std::max(batch * s.least, std::min<int64_t>(batch * s.most, 1024)) * 8 + 15) / 16 * 16;
 }
 
 ql_status qlinear_verify_draft(int64_t batch, int64_t n_drafts, int64_t max_drafts, int64_t vocab,
@@ -531,7 +535,7 @@ ql_status qlinear_verify_draft(int64_t batch, int64_t n_drafts, int64_t max_draf
   a.batch = (int)batch;
   a.vocab = (int)vocab;
   a.max_drafts = (int)max_drafts;
-  a.slices = verify_slices(batch, vocab);
+  a.slices = VerifySlices(vocab).of(batch);
   hipError_t e = qlk::launch_verify(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? QL_OK : hip_fail(e, "draft verification launch");
 }

@@ -215,7 +215,7 @@ def qlinear_verify_workspace_bytes(batch, vocab):
 
 
 def verify_workspace(batch, vocab, device="cuda"):
-    """Device memory for qlinear_verify_draft (any contents)."""
+    """Device memory for qlinear_verify_draft (any contents), with up to that many sequences and entries."""
     return torch.empty(max(16, qlinear_verify_workspace_bytes(batch, vocab)), dtype=torch.uint8, device=device)
 
 

@@ -39,3 +39,18 @@ def test_adapters(tokens, most, k):
     out = torch.zeros_like(p.y)
     ql.qlinear_lora(p.stack, p.x, p.y, p.adapters.cuda(), ws, out=out)
     assert torch.equal(out, want) and (behind == 255).all()
+
+
+@pytest.mark.parametrize("batch,vocab,most", [(512, 3000, 513), (8, 32001, 9), (6, 151936, 7)])
+def test_verification(batch, vocab, most):
+    """Without drafts the next token is argmax p / noise."""
+    g = torch.Generator().manual_seed(vocab)
+    probs = torch.rand(batch, vocab, generator=g).cuda()
+    noise = torch.ones(batch, vocab, device="cuda")
+    ws, behind = guarded(ql.qlinear_verify_workspace_bytes(most, vocab))
+    out, accepted = (torch.zeros(*s, dtype=torch.int32, device="cuda") for s in ((batch, 2), (batch,)))
+    none = torch.zeros(0, dtype=torch.int32, device="cuda")
+    ql.qlinear_verify_draft(probs, None, none, torch.zeros(batch + 1, dtype=torch.int32, device="cuda"),
+                            torch.zeros(0, device="cuda"), noise, out, accepted, ws)
+    assert torch.equal(out[:, 0].long(), probs.argmax(-1)) and not accepted.any() and (out[:, 1] == -1).all()
+    assert (behind == 255).all()

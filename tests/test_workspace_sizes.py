@@ -62,3 +62,16 @@ def test_adapter_sizes_hold_what_a_call_needs():
             s = lora(adapters, rank, k, slices)
             need = -(-k // chunk) * tokens * slices * rank * 4
             assert ql.lib().qlinear_lora_workspace_bytes(ctypes.byref(s), tokens) >= need, (adapters, rank, k, slices, tokens)
+
+
+@pytest.mark.parametrize("vocab", (1, 1023, 2048, 4096, 32001, 151936, 1 << 20, 1 << 30))
+def test_verification_sequences(vocab):
+    size = lambda b: ql.qlinear_verify_workspace_bytes(b, vocab)    # noqa: E731
+    assert rises(size, range(1, 3000)) is None
+    assert rises(size, [3000 + 97 * i for i in range(600)] + [65535]) is None
+
+
+@pytest.mark.parametrize("batch", (1, 2, 3, 7, 64, 100, 511, 512, 513, 1024, 65535))
+def test_verification_vocabularies(batch):
+    steps = sorted({1, 7} | {k * m + d for k in range(1, 3000) for m in (1024, 4092) for d in (-1, 0, 1, 4, 5)})
+    assert rises(lambda v: ql.qlinear_verify_workspace_bytes(batch, v), steps) is None
