@@ -373,13 +373,17 @@ __device__ __forceinline__ SampleRow settle_row(const SampleArgs& a, int row, co
   }
   __syncthreads();
   // the border lies where the mass reaches p of the first k's, which is known up to the k-th's bucket: the first
-  // bucket that reaches it (rounding of these sums allowed for)
+  // bucket that reaches it (rounding of these sums allowed for).  Ends are compared with the limits, and with nothing
+  // else: a bucket's start is worked out apart from the end before it, and a limit may lie between the two.
   const bool k_found = k_mass[1] >= 0.0;
   if (p_on) {
     const double least = (double)r.p * (k_found ? k_mass[0] : all.mass) * (1.0 - 1e-10),
                  most = (double)r.p * (k_found ? k_mass[1] : all.mass) * (1.0 + 1e-10);
-    if (end >= least && (b == 0 || before.mass < least)) atomicMin(&p_lo, b);
-    if (end >= most && (b == 0 || before.mass < most)) atomicMin(&p_hi, b);
+    const uint64_t reach = __ballot(end >= least), pass = __ballot(end >= most);
+    if (lane == 0) {
+      if (reach) atomicMin(&p_lo, b + __ffsll((unsigned long long)reach) - 1);
+      if (pass) atomicMin(&p_hi, b + __ffsll((unsigned long long)pass) - 1);
+    }
   }
   __syncthreads();
   // a k beyond the entries that have mass cuts nothing that top-p has not
