@@ -797,6 +797,7 @@ ql_status qlinear_lora(const ql_lora* lora, int64_t tokens, const void* x, int64
  * distribution (as for qlinear_verify_draft) that draws v in proportion to w_v.
  *   logits  binary32 or bf16 [rows, vocab], rows logits_stride elements apart
  *   noise   binary32 [rows, vocab], positive and finite; read at kept entries only
+ *           (the quotient is a binary32 number)
  *   tokens  int32 [rows]
  *   logprobs  binary32 [rows] or NULL: logarithm of the token's probability
  *           among the kept entries

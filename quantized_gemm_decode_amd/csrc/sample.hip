@@ -433,16 +433,18 @@ __device__ __forceinline__ uint64_t cand_mass(float l, const SampleRow& s, doubl
 
 // The best score among many entries, a wave together: few can be the best one,
 // so binary32's exponential and reciprocal pick out those that come within 10^-4
-// of the best so far (what these can be off by while w is a binary32 number).
+// of the best so far (what these can be off by).  Both end in 0 below 2^-126:
+// weights are taken 2^60 times as large, which reaches below binary32's smallest
+// number, and only bounds that no such reciprocal passes are made.
 struct BestScore {
   uint64_t best = 0;   // this lane's
-  float bound = 0.0f;  // of the wave's
+  float bound = 0.0f;  // of the wave's, 2^60 times
   __device__ __forceinline__ void add(const bool (&in)[4], const uint64_t (&key)[4], const float (&noise)[4], float top, double rate) {
     float about[4], most = 0.0f;
     bool near = false;
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-      about[u] = __builtin_amdgcn_exp2f((logit_of(key[u]) - top) * (float)rate) * __builtin_amdgcn_rcpf(noise[u]);
+      about[u] = __builtin_amdgcn_exp2f(fmaf(logit_of(key[u]) - top, (float)rate, 60.0f)) * __builtin_amdgcn_rcpf(noise[u]);
       near |= in[u] && !(about[u] < bound);
       most = in[u] ? fmaxf(most, about[u]) : most;
     }
@@ -454,7 +456,7 @@ struct BestScore {
         best = score > best ? score : best;
       }
     most = wave_max(most) * (1.0f - 1e-4f);
-    bound = most > 1e-30f && most < 1e30f ? fmaxf(bound, most) : bound;
+    bound = most > 0x1p-60f && most < 0x1p120f ? fmaxf(bound, most) : bound;
   }
 };
 
