@@ -35,6 +35,7 @@
 namespace qlk {
 
 constexpr int kLoraWaves = 4;
+constexpr float kMostBf16 = 0x1.fep127f;
 
 // The adapter of this lane's token of block `block`, -1 without one; lanes
 // beyond the tokens are not in `there`.
@@ -233,10 +234,9 @@ __global__ void __launch_bounds__(kLoraWaves * 64, BS == 1 ? 4 : BS == 2 ? 3 : 2
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const float e = x[k / 2][k % 2 * 2] * scale, f = x[k / 2][k % 2 * 2 + 1] * scale;
-            hi[k] = bf16_pair(e, f);
-            // (nothing is left of an infinity)
-            const float e2 = e - __uint_as_float(hi[k] << 16), f2 = f - __uint_as_float(hi[k] & 0xffff0000u);
-            lo[k] = bf16_pair(e2 == e2 ? e2 : 0.0f, f2 == f2 ? f2 : 0.0f);
+            // (no larger than bf16 holds: what is beyond, infinities and NaN are left to the second number)
+            hi[k] = bf16_pair(fminf(fmaxf(e, -kMostBf16), kMostBf16), fminf(fmaxf(f, -kMostBf16), kMostBf16));
+            lo[k] = bf16_pair(e - __uint_as_float(hi[k] << 16), f - __uint_as_float(hi[k] & 0xffff0000u));
           }
         }
         if (PACKED) {
