@@ -677,7 +677,10 @@ ql_status qlinear_attention(ql_attention_plan plan, const ql_rows* q, const ql_k
  * set is taken: a token whose bits are 0 sees the context alone, and is 0 with lse
  * -inf where there is none.  sees_words >= ceil(max_q / 64); a new token beyond
  * them is seen by none.  Keys were rotated at the positions of their nodes (context
- * + depth) and appended in the nodes' order.  Plans: causal, no window.  A plan of
+ * + depth) and appended in the nodes' order.  Plans: causal, no window; both kernels
+ * cut the keys by the lengths they find, and max_kv need only be a bound.  As there,
+ * the weights enter their product with V to 2^-16 for sequences of plans of up to 32
+ * rows (max_q times q_heads / kv_heads), rounded to bf16 (2^-8) above that.  A plan of
  * either kind serves only its own call.
  */
 ql_status qlinear_tree_attention_plan(const ql_attention_shape* shape, ql_attention_plan* out_plan);
@@ -699,7 +702,8 @@ ql_status qlinear_tree_attention(ql_attention_plan plan, const ql_rows* q, const
  *   accepted int32 [batch]: the number of accepted drafts;
  *   new_lens int32 [batch] or NULL: the cached length without the rejected nodes,
  *     seq_lens[b] - nodes + 1 + accepted (not seq_lens itself).
- * A sequence without nodes has accepted 0, no token and its own length.
+ * A sequence without nodes has accepted 0, no token and its own length.  The outputs
+ * must not overlap the inputs.
  * In each of the n_caches caches (host array of descriptors, all layers in one
  * launch for up to 32 of them; pages of one size, found by one page table; n_caches
  * 0: none) the d-th accepted node's keys and values move to the place d behind the
@@ -760,8 +764,9 @@ ql_status qlinear_verify_draft(int64_t batch, int64_t n_drafts, int64_t max_draf
  * in a pool of all layers.  rank: a multiple of 8 up to 128 (adapters of a lower
  * one are padded with zeros); in_features and widths multiples of 8 up to 2^20.
  * Tokens of one adapter need not be neighbours; a batch of more than 64 tokens
- * runs best where they mostly are, as the tokens of a request.  What one adapter's
- * weights hold reaches only its own tokens.
+ * runs best where they mostly are, as the tokens of a request (65 tokens of 32
+ * adapters in turn take five times as long as 64).  What one adapter's weights hold
+ * reaches only its own tokens.
  *
  * Sums are binary32; the inner sum enters its product to 2^-16 of it, and out is
  * rounded to bf16 once.  (An infinity in B may make NaN of its column, as the
@@ -811,7 +816,7 @@ ql_status qlinear_lora(const ql_lora* lora, int64_t tokens, const void* x, int64
  * Logits of +inf share the probability.
  *
  * What is kept does not depend on rounding in binary32: weights are computed in
- * binary64 and summed as integers, to about 10^-11 of a weight and 10^-16 of it
+ * binary64 and summed as integers, to 4 10^-11 of a weight and 10^-16 of it
  * for every |l_v| / temperature (entries of less than 2^-90 of the largest weigh
  * nothing in the sums).  Results do
  * not depend on timing.  The workspace (qlinear_sample_workspace_bytes, 16-byte

@@ -52,8 +52,8 @@
 // and have a join of their own.  1 sequence of 1,031 keys, 26 nodes, 32 / 8 heads of
 // 128: 15.5 us, latency (10) and the join (6); 16 of 515 .. 4,099, 32 nodes: 55 us, 46 of
 // them reading at 3.3 TB/s behind a start of about 8 us, 9 the join of 35 MB of
-// partial results; 32 of 1,021 .. 8,190, 33 .. 64 nodes of 40 / 8 heads, E4M3: 175 us, 650
-// TFLOP/s of the visible pairs' flops.
+// partial results; 32 of 1,021 .. 8,190, 33 .. 64 nodes of 40 / 8 heads, E4M3: 174 .. 178 us
+// (160 .. 166 and the join's 15), 640 .. 650 TFLOP/s of the visible pairs' flops.
 #include "attention_common.hpp"
 
 #include <type_traits>

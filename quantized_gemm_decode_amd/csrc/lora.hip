@@ -28,7 +28,8 @@
 //   4,093 tokens of 8 adapters, R 16, widths 4096 + 1024 + 1024, 138 MB: 57 us (17.5 + 38).
 //     The second launch reads y and writes out (100 MB) at 2.7 TB/s: without the reads it
 //     is 17 us shorter, without the writes 16; deeper prefetch, other orders
-//     of the columns and non-temporal accesses gave nothing.
+//     of the columns and non-temporal accesses gave nothing (accesses through LDS, of
+//     whole runs of a row for 64 bytes of 16 rows, have not been tried).
 #include "attention_common.hpp"
 #include "serving_args.hpp"
 

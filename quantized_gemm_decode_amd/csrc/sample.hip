@@ -26,12 +26,12 @@
 // short series, times a factor of the bucket.
 //
 // Measured on MI355X, latency throughout (logits are read at 5 TB/s in 4 us by 64
-// rows of 151,936 bf16): 1 row of 32,001: 19.4 us (scan 3.7, collect 7.8, finish 8.3);
-// 64 rows of 151,936 bf16, all rules mixed: 59 us (14.5, 26, 17-21); 40 rows of
-// 128,256 with top-p and probabilities: 63 us (9, 21, 22, write 14, which moves 41 MB).
+// rows of 151,936 bf16): 1 row of 32,001: 19.4 us (scan 3.7, collect 8.0, finish 8.4);
+// 64 rows of 151,936 bf16, all rules mixed: 60 us (14, 26, 17-21); 40 rows of
+// 128,256 with top-p and probabilities: 64 us (9, 21, 23, write 14, which moves 41 MB).
 //   scan: an LDS atomic an entry, and binary64 masses.
 //   collect: the sum of the histograms is a chain of loads, exponentials and a
-//     prefix sum (most of a single row's 7.8 us), then the logits once more, from the
+//     prefix sum (most of a single row's 8 us), then the logits once more, from the
 //     caches; loading them a piece ahead gave nothing.
 //   finish: a workgroup a row; how often it counts depends on the candidates (64
 //     rows without rules: 48 us, with top-k 38, with top-p 69).
